@@ -281,7 +281,7 @@ def _plain_blocks(s):
     need = torch.where(total <= width, total - held, 0)
     first = s["cursor"].long() + torch.cumsum(need, 0) - need
     ends = torch.cumsum(new, 0)
-    ok = (total <= width) & (first + need <= s["free"].numel()) & (ends <= t)
+    ok = (total <= width) & ((need == 0) | (first + need <= s["free"].numel())) & (ends <= t)
     cols = torch.arange(width, device=DEV)[None]
     fresh = (cols >= held[:, None]) & (cols < total[:, None]) & ok[:, None]
     at = (first[:, None] + cols - held[:, None]).clamp(0, s["free"].numel() - 1)
