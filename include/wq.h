@@ -9,7 +9,8 @@
  *   frees or synchronises; all work is enqueued asynchronously on `stream`
  *   (a hipStream_t; NULL means the default stream).
  * - Every buffer is dense and row-major ("contiguous"); the row stride is the
- *   row length.  Base pointers must be 16-byte aligned (WQ_EALIGN otherwise).
+ *   row length, unless an entry point takes a stride.  Base pointers must be
+ *   16-byte aligned (WQ_EALIGN otherwise) where an entry point does not say less.
  * - Shapes and divisibility are validated on the host before anything is
  *   launched: violations return WQ_EINVAL, unsupported dtype/block/group
  *   combinations WQ_EUNSUPPORTED, launch failures WQ_EHIP.  An error return
@@ -439,6 +440,140 @@ wq_status wq_w4a8_dequant(const uint32_t* wq, const uint8_t* s8, int64_t N, int6
 wq_status wq_moe_gemm_w4a8(const uint8_t* x8, int64_t T, const float* a_scale, const int32_t* row_token, int64_t R,
                            const int32_t* offsets, int32_t experts, int64_t N, int64_t K, const uint32_t* wq,
                            const uint8_t* s8, const float* ch, uint16_t* y, void* stream);
+
+/*
+ * 8-bit key/value cache
+ * ---------------------
+ * The cache of a decoder's attention in the MX manner: E4M3 elements with one
+ * E8M0 scale per block, the block being the tokens of one page and one head.
+ * A page holds `page` tokens, a power of two in {16, 32, 64, 128}; page ids run
+ * from 0 to num_pages - 1.
+ *   k_codes   num_pages x heads x page x head_dim E4M3 bytes
+ *   v_codes   num_pages x heads x head_dim x page E4M3 bytes (values are kept
+ *             transposed: the tokens of one channel are contiguous, which is
+ *             the operand order of the product with the probabilities)
+ *   k_scales, v_scales   num_pages x heads E8M0 bytes (255, the E8M0 NaN, is
+ *             outside the contract)
+ * head_dim is 64 or 128.  A request is a row of the block table: its pages in
+ * order, token j of the request standing in page table[j / page] at offset
+ * j % page.  The slot of a token is page_id * page + offset.
+ * Index arrays (int32 and int64) and the scales need their natural alignment
+ * only; codes, keys, values, queries and outputs are 16-byte aligned.
+ */
+
+/*
+ * wq_kv_blocks -- block tables, slot map and positions of one step, from the
+ * requests' lengths.
+ *
+ * Request i holds ctx_lens[i] tokens in the cache and gets new_lens[i] more
+ * (negative lengths count as 0).  It holds ceil(ctx / page) pages and needs
+ * ceil((ctx + new) / page) - ceil(ctx / page) more, which it takes from
+ * free_pages, in request order, from free_pages[cursor[0]] on.  A request is
+ * refused when its pages do not fit its table row (then it takes none), when
+ * the list ends before its last page, or when its tokens end behind row
+ * `tokens` (the pages it would have taken are not given to others): its table
+ * row stays as it was, its length stays ctx, and its tokens get no slot.
+ *
+ * ctx_lens, new_lens  batch int32.
+ * free_pages  num_free int32 page ids (NULL when num_free is 0).  Not changed.
+ * cursor      one int32 >= 0, or NULL for 0: how many of them are taken already.
+ * block_table batch x max_blocks int32.  The first ceil(ctx / page) entries of
+ *             a row are read; the entries of new pages are written; the others
+ *             stay as they were.
+ * tokens      rows of the token arrays, at least 0; new tokens of request i are
+ *             rows [cu_new[i], cu_new[i + 1]).
+ * slots       `tokens` int64 (output): slot of each new token; -1 behind the last
+ *             request, for a refused request, and for a token whose page id
+ *             is negative.
+ * positions   `tokens` int32 (output): position of each new token in its
+ *             request; -1 where it has no slot.
+ * cu_new      batch + 1 int32 (output): running sums of new_lens, at most `tokens`.
+ * kv_lens     batch int32 (output): ctx + new, or ctx for a refused request.
+ * state       2 int32 (output): the cursor behind the last page taken
+ *             (cursor + the pages of the requests not refused), and how many
+ *             requests were refused.
+ * Outputs must not overlap inputs (equal pointers are WQ_EINVAL): a step is a
+ * function of its inputs, and calling it again changes nothing.
+ */
+wq_status wq_kv_blocks(const int32_t* ctx_lens, const int32_t* new_lens, int64_t batch, const int32_t* free_pages,
+                       int64_t num_free, const int32_t* cursor, int32_t page, int32_t* block_table, int64_t max_blocks,
+                       int64_t tokens, int64_t* slots, int32_t* positions, int32_t* cu_new, int32_t* kv_lens,
+                       int32_t* state, void* stream);
+
+/*
+ * wq_kv_append -- fp32/bf16 keys and values -> their slots of the cache.
+ *
+ * Tokens whose slots follow one another inside a page are written together (a
+ * run).  Per run and head, and for keys and values apart: amax over the
+ * run's elements; need = the least E8M0 code c with amax <= 448 * 2^(c-127)
+ * (0 for an all-zero run).  A run that begins at offset 0 opens its page: its
+ * scale is need.  Any other run extends the page: the scale becomes the larger
+ * of need and the page's scale, and where that grows the codes of the tokens
+ * before the run are multiplied by 2^(old - new) and rounded again (exact but
+ * for results below 2^-6).  Element codes are x * 2^(127-c) rounded to nearest
+ * even.  Bytes of tokens behind the run stay as they were.
+ * NaN elements give 0x7F with their sign and infinities +-448; both are left
+ * out of amax.
+ *
+ * k, v     tokens x heads x head_dim, dtype x_dtype (WQ_F32 or WQ_BF16); rows of
+ *          a token are k_stride / v_stride elements apart (at least
+ *          heads * head_dim, a multiple of 8), the elements of a row dense.
+ * slots    `tokens` int64 device slots; a token whose slot is outside
+ *          [0, num_pages * page) is skipped.
+ * A page may be written by one run of a call only: two runs on one page (a
+ * slot given twice, or a gap inside a page) leave that page's codes and scale
+ * unspecified.
+ */
+wq_status wq_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride, int x_dtype,
+                       const int64_t* slots, int64_t tokens, int32_t heads, int32_t head_dim, int32_t page,
+                       int64_t num_pages, uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes, uint8_t* v_scales,
+                       void* stream);
+
+/*
+ * wq_kv_attention -- causal attention of new tokens over the cache: decode
+ * steps, drafted tokens, prompts and chunks of prompts, mixed in one batch.
+ *
+ * Request i has queries in rows [cu_q[i], cu_q[i + 1]) and kv_lens[i] tokens in
+ * the cache, its own newest ones among them (append first).  Query t of n
+ * stands at position p = kv_len - n + t and sees the tokens j with
+ * max(0, p - window + 1) <= j <= p (window 0: no lower limit).  With s_j =
+ * sm_scale * q . k_j (softcap c > 0: c * tanh(s_j / c)):
+ *   out = sum_j exp(s_j) v_j / sum_j exp(s_j),  lse = log sum_j exp(s_j).
+ * Query head h reads key/value head h / (q_heads / kv_heads).  fp32 scores,
+ * softmax statistics and sums; the probabilities are rounded to bf16 for the
+ * second product, the output once.  A row that sees no token gets out 0 and
+ * lse -inf.  Rows behind cu_q[batch] stay as they were.
+ *
+ * q           tokens x q_heads x head_dim bf16; rows of a token q_stride elements
+ *             apart (at least q_heads * head_dim, a multiple of 8).
+ * cu_q        batch + 1 int32, cu_q[0] = 0, non-decreasing, at most `tokens`.
+ * kv_lens     batch int32.
+ * block_table batch x max_blocks int32.  These three are device data the host
+ *             cannot check: row ranges are clamped to [0, tokens] (a decreasing
+ *             pair is an empty request), lengths to [0, max_blocks * page], and
+ *             the tokens of a page whose id is outside [0, num_pages) are
+ *             not seen, so that no access leaves the buffers.
+ * max_q       the largest number of queries of one request, or 0 if unknown.
+ *             Only the choice of kernels depends on it.
+ * softcap     >= 0, finite; window >= 0; sm_scale > 0, finite.
+ * out         tokens x q_heads x head_dim bf16, dense (output).
+ * lse         tokens x q_heads fp32 (output), or NULL.
+ * workspace   wq_kv_attention_workspace_size bytes, 16-byte aligned, for this
+ *             call alone while it runs; its contents need no preparation and
+ *             mean nothing afterwards.
+ * Keys with NaN codes make the rows that see them NaN.  A NaN value code may
+ * reach every row of its request: it is outside the contract.
+ */
+wq_status wq_kv_attention(const void* q_bf16, int64_t q_stride, const int32_t* cu_q, const int32_t* kv_lens,
+                          int64_t batch, int64_t tokens, int64_t max_q, int32_t q_heads, int32_t kv_heads,
+                          int32_t head_dim, const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                          const uint8_t* v_scales, int32_t page, int64_t num_pages, const int32_t* block_table,
+                          int64_t max_blocks, float sm_scale, float softcap, int64_t window, uint16_t* out,
+                          float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace wq_kv_attention needs for this problem (0 for sizes it refuses). */
+size_t wq_kv_attention_workspace_size(int64_t batch, int64_t tokens, int64_t max_q, int32_t q_heads, int32_t kv_heads,
+                                      int32_t head_dim, int32_t page, int64_t max_blocks);
 
 #ifdef __cplusplus
 }

@@ -34,6 +34,7 @@ dequant   packed weights + scales -> bf16 operands
 gemm      fp64 reference matmul and the acceptance bound
 w8a8      W8A8 FP8: static per-tensor activation quantizer, 128 x 128 weight
           blocks, the block-scaled fp32 reference
+kv        8-bit paged key/value cache: block tables, append, causal attention
 w4a8      MoE routing, W4A8 scale recipe, INT4 -> E4M3 lookup table, grouped GEMM
 
 Parity status: every function is pinned by CPU tests against values the pages

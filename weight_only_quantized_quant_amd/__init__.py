@@ -52,6 +52,13 @@ _SIGS = {
     "wq_w4a8_prepack": ([_vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp], ctypes.c_int),
     "wq_w4a8_dequant": ([_vp, _vp, _i64, _i64, _vp, _vp], ctypes.c_int),
     "wq_moe_gemm_w4a8": ([_vp, _i64, _vp, _vp, _i64, _vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "wq_kv_blocks": ([_vp, _vp, _i64, _vp, _i64, _vp, _i32, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp],
+                     ctypes.c_int),
+    "wq_kv_append": ([_vp, _i64, _vp, _i64, ctypes.c_int, _vp, _i64, _i32, _i32, _i32, _i64, _vp, _vp, _vp, _vp, _vp],
+                     ctypes.c_int),
+    "wq_kv_attention": ([_vp, _i64, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i64, _vp,
+                         _i64, ctypes.c_float, ctypes.c_float, _i64, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "wq_kv_attention_workspace_size": ([_i64, _i64, _i64, _i32, _i32, _i32, _i32, _i64], _sz),
     "wq_util_stream_read": ([_vp, _i64, ctypes.c_uint32, _vp, _vp], ctypes.c_int),
     "wq_util_spin": ([_i64, ctypes.c_uint32, _vp, _vp], ctypes.c_int),
     "wq_util_clock": ([_i64, _vp, _vp], ctypes.c_int),
@@ -391,6 +398,164 @@ def wq_moe_gemm_w4a8(x8: torch.Tensor, a_scale: torch.Tensor, row_token, offsets
                                 wq.data_ptr(), s8.data_ptr(), ch.data_ptr(), y.data_ptr(), _stream()),
            "wq_moe_gemm_w4a8")
     return y
+
+
+# ---------------------------------------------------------------------------
+# 8-bit key/value cache
+# ---------------------------------------------------------------------------
+def _same_device(t, device, name):
+    _dev(t, name)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _index(t, dtype, shape, device, name):
+    """A contiguous device tensor of integers on `device`."""
+    _same_device(t, device, name)
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _token_rows(t, name):
+    """Elements between the tokens of a [tokens, heads, dim] tensor whose rows are dense
+    (a slice of a fused projection's output may have a larger stride)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    n, h, d = t.shape
+    if n <= 1 and t.is_contiguous():
+        return h * d
+    sn, sh, sd = t.stride()
+    if sd != 1 or (sh != d and h > 1):
+        raise ValueError(f"the heads of a token of {name} must be dense")
+    return sn if n > 1 else h * d
+
+
+def _kv_cache(k_codes, k_scales, v_codes, v_scales, device):
+    """(num_pages, heads, page, head_dim) of a cache."""
+    for t, name in ((k_codes, "k_codes"), (k_scales, "k_scales"), (v_codes, "v_codes"), (v_scales, "v_scales")):
+        _same_device(t, device, name)
+        if t.dtype != torch.uint8:
+            raise ValueError(f"{name} must be uint8")
+    if k_codes.dim() != 4:
+        raise ValueError("k_codes must be [num_pages, heads, page, head_dim]")
+    n, h, p, d = k_codes.shape
+    if v_codes.shape != (n, h, d, p):
+        raise ValueError("v_codes must be [num_pages, heads, head_dim, page]")
+    if k_scales.shape != (n, h) or v_scales.shape != (n, h):
+        raise ValueError("k_scales and v_scales must be [num_pages, heads]")
+    return n, h, p, d
+
+
+def _on(device):
+    """The launch goes to the tensors' device, whichever is current."""
+    return torch.cuda.device(device)
+
+
+def wq_kv_blocks(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor, block_table: torch.Tensor,
+                 page: int, tokens: int, cursor=None):
+    """Block tables, slot map and positions of one step.  ctx_lens, new_lens int32 [B];
+    free_pages int32 [F] page ids, the first cursor[0] of them taken already; block_table int32
+    [B, W], completed in place.  Returns (slots int64 [tokens], positions int32 [tokens],
+    cu_new int32 [B + 1], kv_lens int32 [B], state int32 [2]: the next cursor and the number of
+    refused requests)."""
+    _dev(ctx_lens, "ctx_lens")
+    d = ctx_lens.device
+    if ctx_lens.dtype != torch.int32 or ctx_lens.dim() != 1:
+        raise ValueError("ctx_lens must be int32 [batch]")
+    B = ctx_lens.shape[0]
+    nl = _index(new_lens, torch.int32, (B,), d, "new_lens")
+    _same_device(free_pages, d, "free_pages")
+    _same_device(block_table, d, "block_table")
+    if free_pages.dtype != torch.int32 or free_pages.dim() != 1:
+        raise ValueError("free_pages must be int32 [pages]")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be int32 [batch, max_blocks]")
+    cur = None
+    if cursor is not None:
+        _same_device(cursor, d, "cursor")
+        if cursor.dtype != torch.int32 or cursor.numel() < 1:
+            raise ValueError("cursor must be int32 of at least one element")
+        cur = cursor.data_ptr()
+    tokens = int(tokens)
+    if tokens < 0:
+        raise ValueError("tokens must not be negative")
+    with _on(d):
+        slots = torch.empty(tokens, dtype=torch.int64, device=d)
+        positions, cu_new, kv_lens, state = torch.empty(tokens + 2 * B + 3, dtype=torch.int32,
+                                                        device=d).split((tokens, B + 1, B, 2))
+        _check(lib.wq_kv_blocks(ctx_lens.data_ptr(), nl, B, free_pages.data_ptr(), free_pages.shape[0], cur, page,
+                                block_table.data_ptr(), block_table.shape[1], tokens, slots.data_ptr(),
+                                positions.data_ptr(), cu_new.data_ptr(), kv_lens.data_ptr(), state.data_ptr(),
+                                _stream()), "wq_kv_blocks")
+    return slots, positions, cu_new, kv_lens, state
+
+
+def wq_kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor,
+                 v_codes: torch.Tensor, v_scales: torch.Tensor) -> None:
+    """Quantize k, v (bf16/fp32 [tokens, heads, head_dim], tokens may be strided) into their slots
+    (int64 [tokens], negative: skipped) of the cache: codes uint8 [N, heads, page, head_dim] and
+    [N, heads, head_dim, page], E8M0 scales uint8 [N, heads]."""
+    ks, vs = _token_rows(k, "k"), _token_rows(v, "v")
+    d = k.device
+    n, h, p, dim = _kv_cache(k_codes, k_scales, v_codes, v_scales, d)
+    if k.shape[1] != h or k.shape[2] != dim or v.shape != k.shape or v.dtype != k.dtype or v.device != d:
+        raise ValueError(f"k and v must be [tokens, {h}, {dim}] of one dtype on one device")
+    T = k.shape[0]
+    sp = _index(slots, torch.int64, (T,), d, "slots")
+    with _on(d):
+        _check(lib.wq_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, _x_dtype(k), sp, T, h, dim, p, n,
+                                k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+                                _stream()), "wq_kv_append")
+
+
+def wq_kv_attention_workspace_size(batch: int, tokens: int, max_q: int, q_heads: int, kv_heads: int, head_dim: int,
+                                   page: int, max_blocks: int) -> int:
+    return int(lib.wq_kv_attention_workspace_size(batch, tokens, max_q, q_heads, kv_heads, head_dim, page, max_blocks))
+
+
+def wq_kv_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
+                    v_scales: torch.Tensor, block_table: torch.Tensor, cu_q: torch.Tensor, kv_lens: torch.Tensor,
+                    sm_scale=None, softcap: float = 0.0, window: int = 0, max_q: int = 0, out=None,
+                    return_lse: bool = False, workspace=None):
+    """Causal attention of q (bf16 [tokens, q_heads, head_dim], tokens may be strided; request i has
+    rows cu_q[i] .. cu_q[i + 1]) over the cache's kv_lens[i] tokens of the pages block_table[i].
+    cu_q int32 [B + 1], kv_lens int32 [B], block_table int32 [B, W].  sm_scale defaults to
+    head_dim ** -0.5; max_q: the largest number of queries of one request if known.  Returns out
+    bf16 [tokens, q_heads, head_dim] (and lse fp32 [tokens, q_heads])."""
+    qs = _token_rows(q, "q")
+    d = q.device
+    n, h, p, dim = _kv_cache(k_codes, k_scales, v_codes, v_scales, d)
+    T, hq, qd = q.shape
+    if q.dtype != torch.bfloat16 or qd != dim:
+        raise ValueError(f"q must be bfloat16 [tokens, q_heads, {dim}]")
+    _same_device(block_table, d, "block_table")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2:
+        raise ValueError("block_table must be int32 [batch, max_blocks]")
+    B, width = block_table.shape
+    cu = _index(cu_q, torch.int32, (B + 1,), d, "cu_q")
+    kl = _index(kv_lens, torch.int32, (B,), d, "kv_lens")
+    if sm_scale is None:
+        sm_scale = dim ** -0.5
+    if out is not None:
+        _same_device(out, d, "out")
+    with _on(d):
+        out = _out(out, (T, hq, dim), torch.bfloat16, d, "out")
+        lse = torch.empty((T, hq), dtype=torch.float32, device=d) if return_lse else None
+        need = lib.wq_kv_attention_workspace_size(B, T, max_q, hq, h, dim, p, width)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=d) if need else None
+        else:
+            _same_device(workspace, d, "workspace")
+        ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        _check(lib.wq_kv_attention(q.data_ptr(), qs, cu, kl, B, T, max_q, hq, h, dim, k_codes.data_ptr(),
+                                   k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), p, n,
+                                   block_table.data_ptr(), width, float(sm_scale), float(softcap), int(window),
+                                   out.data_ptr(), lse.data_ptr() if return_lse else None, ws, ws_bytes, _stream()),
+               "wq_kv_attention")
+    return (out, lse) if return_lse else out
 
 
 # ---------------------------------------------------------------------------
