@@ -304,78 +304,682 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_append(
 // ---------------------------------------------------------------------------
 // Attention
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float e4m3_value(uint32_t byte) {
-  return __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(byte, 1.0f, false)[0];
-}
-__device__ __forceinline__ float e8m0_value(uint32_t c) { return __builtin_ldexpf(1.0f, (int)c - 127); }
+// Both attention kernels compute the transposed products S^T = K q^T and
+// O^T = V^T P^T on bf16 matrix cores, the E4M3 bytes converted with their
+// page's scale on the way (exact).  A row of the query tile is then a column
+// of both products, so that a lane holds scores, probabilities, statistics and
+// sums of one row only: the softmax needs no more than one or two exchanges
+// between lanes per tile, and the probabilities that a lane computed are
+// the very operand elements it has to supply to the second product.  The
+// order of the tokens along the second product's inner axis is free as long
+// as V^T follows it, so it is chosen such that a lane's probabilities belong to
+// 16 consecutive tokens: one page, one scale, and one 16-byte load per
+// channel of V^T.
+//
+// Rows of one key/value head are numbered r = query * group + head in group:
+// the `group` query heads that share a key/value head share its tiles.
+constexpr int TILE = 64;                      // tokens per step
+constexpr int DROWS = 16;                     // rows of a decode tile
+constexpr int PROWS = 128;                    // rows of a prompt tile
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
-// One wave per (row, query head): 64 tokens at a time, a lane's token in the
-// scores, a lane's channels in the sums.
-template <int D>
-__global__ __launch_bounds__(64) void k_kv_attention(
-    const uint16_t* __restrict__ q, int64_t q_stride, const int32_t* __restrict__ cu_q,
-    const int32_t* __restrict__ kv_lens, int64_t batch, int64_t tokens, int q_heads, int kv_heads,
-    const uint8_t* __restrict__ k_codes, const uint8_t* __restrict__ k_scales, const uint8_t* __restrict__ v_codes,
-    const uint8_t* __restrict__ v_scales, int log_page, int64_t num_pages, const int32_t* __restrict__ table,
-    int64_t max_blocks, float sm_scale, float softcap, int64_t window, uint16_t* __restrict__ out,
-    float* __restrict__ lse) {
-  __shared__ float qs[D];
-  const int lane = threadIdx.x, head = blockIdx.y, kvh = head / (q_heads / kv_heads);
-  const int64_t row = blockIdx.x;
-  int64_t a = 0, z = batch;                   // the first request whose end is behind the row
-  while (a < z) {
-    const int64_t mid = (a + z) >> 1;
-    if (cu_q[mid + 1] > row) z = mid;
-    else a = mid + 1;
+struct KvArgs {
+  const uint16_t* q;
+  int64_t q_stride;
+  const int32_t* cu_q;
+  const int32_t* kv_lens;
+  int64_t batch, tokens;
+  int q_heads, kv_heads, group;
+  const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  int log_page;
+  int64_t num_pages;
+  const int32_t* table;
+  int64_t max_blocks;
+  float sm_scale, softcap;
+  int64_t window;
+  uint16_t* out;
+  float* lse;
+};
+
+// Partial results of split rows: `used[0]` slots are in use; slot s of head h
+// holds rows * D sums and (maximum, sum) pairs.  `rec` names the slot's rows
+// in the entry of the first split, with the number of splits that follow.
+struct KvRec {
+  int32_t splits;                             // 0 in the entries of the other splits
+  int32_t rows;
+  int64_t row0;                               // query row of the tensors times group, plus head in group
+};
+struct KvPart {
+  int64_t splits;                             // aim: items per head, over which the tiles are spread
+  int min_tiles;                              // no split is shorter
+  int64_t* used;
+  KvRec* rec;
+  float* sums;
+  float* stats;
+};
+
+// Which requests a launch takes: all of them, those whose rows fit one decode
+// tile, or the others.
+enum { REQ_ALL, REQ_SHORT, REQ_LONG };
+
+// One item of work: rows [r0, r0 + rows) of a request, tiles of its share.
+struct KvItem {
+  int64_t request, q0, n, len;                // first query row, queries, tokens in the cache
+  int64_t r0;
+  int rows, splits, split;
+  int64_t slot;                               // partial slot, where splits > 1
+};
+
+__device__ __forceinline__ int64_t wave_sum(int64_t v) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// Every wave finds its item itself, from the lengths: the tiles of all
+// requests are spread evenly over about part.splits items, a request of
+// `tiles` tiles being cut into ceil(tiles / share) splits per row tile.
+// Splits, not tokens, are scanned, so that a long context beside short ones
+// fills the chip as well as equal ones do.  False if there is no such item.
+template <int R, int WHICH>
+__device__ __forceinline__ bool kv_find(const KvArgs& A, const KvPart& part, int64_t item, bool count_all, KvItem& it) {
+  const int lane = threadIdx.x & 63;
+  const int64_t cap = A.max_blocks << A.log_page;
+  auto request = [&](int64_t i, int64_t& q0, int64_t& n, int64_t& len, int64_t& tiles, int64_t& row_tiles) {
+    q0 = n = len = 0;
+    if (i < A.batch) {
+      int64_t a = A.cu_q[i], z = A.cu_q[i + 1];
+      len = A.kv_lens[i];
+      a = a < 0 ? 0 : a;
+      z = z > A.tokens ? A.tokens : z;
+      q0 = a;
+      n = z > a ? z - a : 0;
+      len = len < 0 ? 0 : len > cap ? cap : len;
+    }
+    const int64_t rows = n * A.group;
+    if (WHICH == REQ_SHORT ? rows > DROWS : WHICH == REQ_LONG ? rows <= DROWS : false) n = 0;
+    row_tiles = n > 0 ? (rows + R - 1) / R : 0;
+    const int64_t first = len - n - A.window + 1;      // lowest token any query sees
+    const int64_t lo = A.window > 0 && first > 0 ? first : 0;
+    tiles = len > 0 ? ((len - 1) / TILE) - lo / TILE + 1 : 0;
+  };
+  int64_t q0, n, len, tiles, row_tiles, total = 0;
+  for (int64_t base = 0; base < A.batch; base += 64) {
+    request(base + lane, q0, n, len, tiles, row_tiles);
+    total += tiles * row_tiles;
   }
-  if (a >= batch || cu_q[a] > row || cu_q[a] < 0) return;
-  const int64_t cap = max_blocks << log_page;
-  int64_t len = kv_lens[a];
-  len = len < 0 ? 0 : len > cap ? cap : len;
-  const int64_t end = cu_q[a + 1] < tokens ? cu_q[a + 1] : tokens;
-  const int64_t pos = len - end + row;
-  const int64_t lo = window > 0 && pos - window + 1 > 0 ? pos - window + 1 : 0;
-  for (int d = lane; d < D; d += 64) qs[d] = bf16_to_f32(q[row * q_stride + (int64_t)head * D + d]);
+  total = wave_sum(total);
+  int64_t share = (total + part.splits - 1) / part.splits;
+  share = share < part.min_tiles ? part.min_tiles : share;
+  int64_t items = 0, slots = 0;
+  bool found = false;
+  for (int64_t base = 0; base < A.batch; base += 64) {
+    if (A.batch > 64) request(base + lane, q0, n, len, tiles, row_tiles);
+    const int64_t splits = tiles > share ? (tiles + share - 1) / share : 1;
+    const int64_t own = row_tiles * splits, part_own = splits > 1 ? own : 0;
+    const int64_t end = items + wave_scan(own, lane), part_end = slots + wave_scan(part_own, lane);
+    const unsigned long long at = __ballot(end > item);
+    if (at && !found) {
+      const int src = __builtin_ctzll(at);
+      const int64_t s = __shfl(splits, src, 64), idx = item - __shfl(end - own, src, 64);
+      it.request = base + src;
+      it.q0 = __shfl(q0, src, 64);
+      it.n = __shfl(n, src, 64);
+      it.len = __shfl(len, src, 64);
+      it.splits = (int)s;
+      it.split = (int)(idx % s);
+      it.r0 = (__shfl(row_tiles, src, 64) - 1 - idx / s) * R;      // the longest rows first
+      const int64_t left = it.n * A.group - it.r0;
+      it.rows = left < R ? (int)left : R;
+      it.slot = __shfl(part_end - part_own, src, 64) + idx;
+      found = true;
+    }
+    if (found && !count_all) return true;
+    items = __shfl(end, 63, 64);
+    slots = __shfl(part_end, 63, 64);
+  }
+  if (count_all && threadIdx.x == 0) part.used[0] = slots;
+  return found;
+}
+
+// Tiles [t0, t1) of the item: the tokens its rows see, cut into it.splits shares.
+__device__ __forceinline__ void kv_tiles(const KvArgs& A, const KvItem& it, int64_t& lo, int64_t& hi, int64_t& t0,
+                                         int64_t& t1) {
+  const int64_t p0 = it.len - it.n + it.r0 / A.group, p1 = it.len - it.n + (it.r0 + it.rows - 1) / A.group;
+  hi = p1 + 1 < 0 ? 0 : p1 + 1;               // one behind the last token seen
+  lo = A.window > 0 && p0 - A.window + 1 > 0 ? p0 - A.window + 1 : 0;
+  lo = lo < hi ? lo : hi;
+  const int64_t a = lo / TILE, n = hi > lo ? (hi + TILE - 1) / TILE - a : 0;
+  t0 = a + n * it.split / it.splits;
+  t1 = a + n * (it.split + 1) / it.splits;
+}
+
+// cap * tanh(s / cap): 1 - 2 / (e^2x + 1), and below .2, where that cancels,
+// the series up to x^7 (the next term is under 6e-8 of the result there).
+__device__ __forceinline__ float kv_softcap(float s, float cap, float inv_cap) {
+  const float x = __builtin_fabsf(s * inv_cap), y = x * x;
+  const float big = 1.0f - 2.0f * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x * (2.0f * LOG2E)) + 1.0f);
+  const float small = x + x * y * (-1.0f / 3.0f + y * (2.0f / 15.0f + y * (-17.0f / 315.0f)));
+  return __builtin_copysignf(cap * (x < 0.2f ? small : big), s);
+}
+
+// Eight E4M3 bytes with E8M0 scale operand -> eight bf16.
+__device__ __forceinline__ bf16x8_t e4m3_bf16x8(uint32_t a, uint32_t b, float scale) {
+  const u32x4_t w = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, true)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, true))};
+  return __builtin_bit_cast(bf16x8_t, w);
+}
+
+// Keeps the bytes of tokens [lo, hi) of a 16-byte piece that begins at token j.
+__device__ __forceinline__ u32x4_t keep_tokens(u32x4_t v, int64_t j, int64_t lo, int64_t hi) {
+  const int a = lo > j ? (lo - j < 16 ? (int)(lo - j) : 16) : 0;
+  const int z = hi > j ? (hi - j < 16 ? (int)(hi - j) : 16) : 0;
+#pragma unroll
+  for (int w = 0; w < 4; w++) {
+    const int aw = a - 4 * w < 0 ? 0 : a - 4 * w > 4 ? 4 : a - 4 * w;
+    const int zw = z - 4 * w < 0 ? 0 : z - 4 * w > 4 ? 4 : z - 4 * w;
+    v[w] &= (uint32_t)((1ull << (8 * zw)) - 1) & ~(uint32_t)((1ull << (8 * aw)) - 1);
+  }
+  return v;
+}
+
+// Decode: 16 rows (the query heads of a group, for one token or a few drafted
+// ones) per workgroup; its 4 waves take the item's tiles in turn, each with
+// its own running maximum and sums, which are joined in LDS at the end.
+// Bound by the bytes of K and V: they go from HBM straight into the registers
+// that feed v_mfma_f32_16x16x32_bf16, the next tile's K loads leaving as soon
+// as this tile's scores are done and its V loads after its sums, so that a
+// wave always has 8 to 16 KB in flight.
+//
+// Lane l = 16 g + m.  K tile a (of 4): operand row m is token
+// 16 (m / 4) + 4 a + m % 4, result rows 4 g + i are then tokens 16 g + 4 a + i.
+template <int D, bool CAP, int WHICH>
+__global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, const KvPart part) {
+  constexpr int KP = D / 64, DT = D / 16;
+  __shared__ __attribute__((aligned(16))) float so[4][DROWS][D + 4];
+  __shared__ float sm[4][DROWS], sl[4][DROWS];
+  const int64_t item = blockIdx.x / A.kv_heads;
+  const int kvh = (int)(blockIdx.x % A.kv_heads);
+  KvItem it;
+  if (!kv_find<DROWS, WHICH>(A, part, item, blockIdx.x == 0, it)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, g = lane >> 4;
+  int64_t lo, hi, t0, t1;
+  kv_tiles(A, it, lo, hi, t0, t1);
+
+  // query fragments: columns m of q^T; row m's limits
+  bf16x8_t qf[KP][2];
+  const bool live = m < it.rows;
+  const int64_t r = it.r0 + (live ? m : 0), qrow = it.q0 + r / A.group;
+  const int64_t pos = it.len - it.n + r / A.group;
+  const int64_t rlo = A.window > 0 && pos - A.window + 1 > 0 ? pos - A.window + 1 : 0;
+  {
+    const uint16_t* qp = A.q + qrow * A.q_stride + (kvh * A.group + r % A.group) * D;
+#pragma unroll
+    for (int p = 0; p < KP; p++)
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        u32x4_t w = ld16(qp + 64 * p + 16 * g + 8 * h);
+        if (!live) w = u32x4_t{0, 0, 0, 0};
+        qf[p][h] = __builtin_bit_cast(bf16x8_t, w);
+      }
+  }
+  const int64_t row_min = it.len - it.n + it.r0 / A.group;         // position of the tile's first row
+  const int64_t row_max = it.len - it.n + (it.r0 + it.rows - 1) / A.group;
+  const int64_t lo_max = A.window > 0 && row_max - A.window + 1 > 0 ? row_max - A.window + 1 : 0;
+  const int32_t* tab = A.table + it.request * A.max_blocks;
+  const int64_t page_bytes = (int64_t)D << A.log_page;
+  const int in_page = (1 << A.log_page) - 1;
+  const int64_t last_col = A.max_blocks - 1;
+
+  u32x4_t kr[4][KP], vr[DT];
+  uint32_t ksc, vsc;
+  bool kok, vok;
+  int idk, idv;                               // page ids of the next tile to load
+  auto load_ids = [&](int64_t t) {
+    const int64_t j = t * TILE;
+    const int64_t ck = (j + 16 * (m >> 2)) >> A.log_page, cv = (j + 16 * g) >> A.log_page;
+    idk = tab[ck < last_col ? ck : last_col];
+    idv = tab[cv < last_col ? cv : last_col];
+  };
+  auto load_k = [&](int64_t t) {
+    kok = idk >= 0 && idk < A.num_pages;
+    const int64_t block = (int64_t)(kok ? idk : 0) * A.kv_heads + kvh;
+    ksc = A.k_scales[block];
+    const uint8_t* p = A.k_codes + block * page_bytes +
+                       (((t * TILE + 16 * (m >> 2)) & in_page) + (m & 3)) * D + 16 * g;
+#pragma unroll
+    for (int a = 0; a < 4; a++)
+#pragma unroll
+      for (int h = 0; h < KP; h++) kr[a][h] = ld16(p + 4 * a * D + 64 * h);
+  };
+  auto load_v = [&](int64_t t) {
+    vok = idv >= 0 && idv < A.num_pages;
+    const int64_t block = (int64_t)(vok ? idv : 0) * A.kv_heads + kvh;
+    vsc = A.v_scales[block];
+    const uint8_t* p = A.v_codes + block * page_bytes + ((int64_t)m << A.log_page) + ((t * TILE + 16 * g) & in_page);
+#pragma unroll
+    for (int d = 0; d < DT; d++) vr[d] = ld16(p + ((int64_t)(16 * d) << A.log_page));
+  };
+
+  f32x4_t o[DT];
+#pragma unroll
+  for (int d = 0; d < DT; d++) o[d] = f32x4_t{0, 0, 0, 0};
+  float mx = -INFINITY, l = 0.0f;
+  const float c = CAP ? LOG2E : A.sm_scale * LOG2E;
+  const float inv_cap = CAP ? A.sm_scale / A.softcap : 0.0f;
+  int64_t t = t0 + wave;
+  if (t < t1) {
+    load_ids(t);
+    load_k(t);
+    load_v(t);
+    if (t + 4 < t1) load_ids(t + 4);
+  }
+  for (; t < t1; t += 4) {
+    const int64_t j0 = t * TILE + 16 * g;     // this lane's 16 tokens in scores and V^T
+    const bool more = t + 4 < t1;
+    f32x4_t s[4];
+    const float ks = e8m0_as_scale(ksc);
+#pragma unroll
+    for (int a = 0; a < 4; a++) {
+      s[a] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int p = 0; p < KP; p++) {
+        const u32x4_t w = kr[a][p];
+        s[a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e4m3_bf16x8(w[0], w[1], ks), qf[p][0], s[a], 0, 0, 0);
+        s[a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e4m3_bf16x8(w[2], w[3], ks), qf[p][1], s[a], 0, 0, 0);
+      }
+    }
+    if (more) load_k(t + 4);
+    if constexpr (CAP) {
+#pragma unroll
+      for (int a = 0; a < 4; a++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) s[a][i] = kv_softcap(s[a][i], A.softcap, inv_cap);
+    }
+    // tokens outside a row's limits, and bytes of V that no row may see
+    float vs = e8m0_as_scale(vsc);
+    if (t * TILE + TILE - 1 > row_min || t * TILE < lo_max || __any(!vok)) {
+#pragma unroll
+      for (int a = 0; a < 4; a++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const int64_t j = j0 + 4 * a + i;
+          s[a][i] = j <= pos && j >= rlo && vok ? s[a][i] : -INFINITY;
+        }
+      const int64_t a = vok ? lo : 0, z = vok ? hi : 0;
+      if (j0 + 16 <= a || j0 >= z) vs = 1.0f;
+#pragma unroll
+      for (int d = 0; d < DT; d++) vr[d] = keep_tokens(vr[d], j0, a, z);
+    }
+    float mt = -INFINITY;
+#pragma unroll
+    for (int a = 0; a < 4; a++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) mt = __builtin_fmaxf(mt, s[a][i]);
+    mt = __builtin_fmaxf(mt, __shfl_xor(mt, 16, 64));
+    mt = __builtin_fmaxf(mt, __shfl_xor(mt, 32, 64)) * c;
+    if (__any(mt > mx)) {
+      const float mn = __builtin_fmaxf(mx, mt);
+      const float f = mx == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx - mn);
+      mx = mn;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < DT; d++) o[d] *= f;
+    }
+    const float off = mx == -INFINITY ? 0.0f : mx;
+    uint32_t pw[8];
+#pragma unroll
+    for (int a = 0; a < 4; a++) {
+      float p[4];
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[a][i], c, -off));
+        l += p[i];
+      }
+      // bf16 for the matrix cores: half a step of 2^-8 per probability, the sum l keeps fp32
+      pw[2 * a] = pack_bf16x2(p[0], p[1]);
+      pw[2 * a + 1] = pack_bf16x2(p[2], p[3]);
+    }
+    const bf16x8_t p0 = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[0], pw[1], pw[2], pw[3]}));
+    const bf16x8_t p1 = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[4], pw[5], pw[6], pw[7]}));
+#pragma unroll
+    for (int d = 0; d < DT; d++) {
+      o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e4m3_bf16x8(vr[d][0], vr[d][1], vs), p0, o[d], 0, 0, 0);
+      o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e4m3_bf16x8(vr[d][2], vr[d][3], vs), p1, o[d], 0, 0, 0);
+    }
+    if (more) {
+      load_v(t + 4);
+      if (t + 8 < t1) load_ids(t + 8);
+    }
+  }
+  l += __shfl_xor(l, 16, 64);
+  l += __shfl_xor(l, 32, 64);
+  if (g == 0) {
+    sm[wave][m] = mx;
+    sl[wave][m] = l;
+  }
+#pragma unroll
+  for (int d = 0; d < DT; d++) *reinterpret_cast<f32x4_t*>(&so[wave][m][16 * d + 4 * g]) = o[d];
   __syncthreads();
-  float m = -INFINITY, l = 0.0f, o[D / 64] = {};
-  for (int64_t base = lo & ~(int64_t)63; base <= pos; base += 64) {
-    const int64_t j = base + lane;
-    const bool in = j >= lo && j <= pos;
-    const int64_t id = in ? table[a * max_blocks + (j >> log_page)] : -1;
-    const bool seen = id >= 0 && id < num_pages;
-    const int64_t block = seen ? id * kv_heads + kvh : 0;
-    const int off = (int)(j & ((1 << log_page) - 1));
-    float s = -INFINITY;
-    if (seen) {
-      const uint8_t* kp = k_codes + ((block << log_page) + off) * D;
-      float dot = 0.0f;
-      for (int d = 0; d < D; d++) dot = __builtin_fmaf(qs[d], e4m3_value(kp[d]), dot);
-      s = dot * e8m0_value(k_scales[block]) * sm_scale;
-      if (softcap > 0.0f) s = softcap * tanhf(s / softcap);
+
+  // join the waves: thread (row, channels)
+  constexpr int CH = D / 16;
+  const int row = tid / 16, ch = (tid % 16) * CH;
+  if (row >= it.rows) return;
+  float M = sm[0][row];
+#pragma unroll
+  for (int w = 1; w < 4; w++) M = __builtin_fmaxf(M, sm[w][row]);
+  float L = 0.0f, acc[CH];
+#pragma unroll
+  for (int i = 0; i < CH; i++) acc[i] = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 4; w++) {
+    const float f = sm[w][row] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(sm[w][row] - M);
+    L += f * sl[w][row];
+#pragma unroll
+    for (int i = 0; i < CH; i++) acc[i] = __builtin_fmaf(f, so[w][row][ch + i], acc[i]);
+  }
+  const int64_t rr = it.r0 + row;
+  if (it.splits > 1) {
+    const int64_t at = (it.slot * A.kv_heads + kvh) * DROWS + row;
+#pragma unroll
+    for (int i = 0; i < CH; i += 4)
+      *reinterpret_cast<f32x4_t*>(part.sums + at * D + ch + i) = f32x4_t{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
+    if (ch == 0) {
+      part.stats[2 * at] = M;
+      part.stats[2 * at + 1] = L;
     }
-    const float mt = group_max(s, 64);
-    const float mn = __builtin_fmaxf(m, mt);
-    const float use = mn == -INFINITY ? 0.0f : mn;
-    const float keep = expf(m - use);
-    float p = seen ? expf(s - use) : 0.0f;
-    float sum = p;
-    for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x, 64);
-    l = l * keep + sum;
-    m = mn;
-    const float pv = seen ? p * e8m0_value(v_scales[block]) : 0.0f;
-    for (int e = 0; e < D / 64; e++) o[e] *= keep;
-    for (int i = 0; i < 64; i++) {
-      if (!__shfl((int)seen, i, 64)) continue;
-      const int64_t bi = __shfl(block, i, 64);
-      const int oi = __shfl(off, i, 64);
-      const float pi = __shfl(pv, i, 64);
-      for (int e = 0; e < D / 64; e++)
-        o[e] = __builtin_fmaf(pi, e4m3_value(v_codes[((bi * D + lane + 64 * e) << log_page) + oi]), o[e]);
+    if (tid == 0 && kvh == 0) part.rec[it.slot] = KvRec{it.split ? 0 : it.splits, it.rows, it.q0 * A.group + it.r0};
+    return;
+  }
+  const int64_t orow = (it.q0 + rr / A.group) * A.q_heads + kvh * A.group + rr % A.group;
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  uint32_t w[CH / 2];
+#pragma unroll
+  for (int i = 0; i < CH / 2; i++) w[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+  if constexpr (CH == 8) *reinterpret_cast<u32x4_t*>(A.out + orow * D + ch) = u32x4_t{w[0], w[1], w[2], w[3]};
+  else *reinterpret_cast<u32x2_t*>(A.out + orow * D + ch) = u32x2_t{w[0], w[1]};
+  if (A.lse && ch == 0) A.lse[orow] = L == 0.0f ? -INFINITY : (M + __builtin_log2f(L)) * LN2;
+}
+
+// Prompts and chunks: 128 rows per workgroup, 32 per wave.  Bound by the
+// matrix cores and the exponentials: a tile of 64 tokens is converted to bf16
+// once per workgroup, on its way from registers (loaded a step ahead) to LDS,
+// where it lies in operand order (each fragment 1 KB contiguous, its 16-byte
+// units permuted by an xor so that neither the writes nor the reads conflict),
+// and feeds v_mfma_f32_32x32x16_bf16.
+//
+// Lane l = 32 h + m.  Within a 32-token half u of the tile, operand row
+// 8 (r / 4) + 4 h + r % 4 is token 32 u + 16 h + r: result register r of lane
+// half h is that token.
+template <int D, bool CAP>
+__global__ __launch_bounds__(KV_THREADS, 2) void k_kv_prompt(const KvArgs A, const KvPart part) {
+  constexpr int KS = D / 16, DT = D / 32, ST = D / 64;             // k steps, channel tiles, 16-byte pieces a thread
+  constexpr int XK = D == 128 ? 1 : 2;
+  __shared__ __attribute__((aligned(16))) uint8_t sk[2][TILE * D * 2], sv[2][TILE * D * 2];
+  __shared__ int sok[2][4];
+  const int64_t item = blockIdx.x / A.kv_heads;
+  const int kvh = (int)(blockIdx.x % A.kv_heads);
+  KvItem it;
+  if (!kv_find<PROWS, REQ_LONG>(A, part, item, blockIdx.x == 0, it)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 31, h = lane >> 5;
+  int64_t lo, hi, t0, t1;
+  kv_tiles(A, it, lo, hi, t0, t1);
+
+  const int wrow = wave * 32;                 // first row of the wave in the tile
+  const bool live = wrow + m < it.rows;
+  const int64_t r = it.r0 + (live ? wrow + m : 0), qrow = it.q0 + r / A.group;
+  const int64_t pos = it.len - it.n + r / A.group;
+  const int64_t rlo = A.window > 0 && pos - A.window + 1 > 0 ? pos - A.window + 1 : 0;
+  bf16x8_t qf[KS];
+  {
+    const uint16_t* qp = A.q + qrow * A.q_stride + (kvh * A.group + r % A.group) * D;
+#pragma unroll
+    for (int k = 0; k < KS; k++) {
+      u32x4_t w = ld16(qp + 16 * k + 8 * h);
+      if (!live) w = u32x4_t{0, 0, 0, 0};
+      qf[k] = __builtin_bit_cast(bf16x8_t, w);
     }
   }
-  const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
-  for (int e = 0; e < D / 64; e++) out[(row * q_heads + head) * D + lane + 64 * e] = (uint16_t)f32_to_bf16_bits(o[e] * inv);
-  if (lse && lane == 0) lse[row * q_heads + head] = l == 0.0f ? -INFINITY : m + logf(l);
+  const int64_t w_last = wrow + 31 < it.rows ? wrow + 31 : it.rows - 1;      // below wrow: an idle wave
+  const int64_t w_min = it.len - it.n + (it.r0 + wrow) / A.group;
+  const int64_t w_max = it.len - it.n + (it.r0 + w_last) / A.group;
+  const int64_t w_lo_min = A.window > 0 && w_min - A.window + 1 > 0 ? w_min - A.window + 1 : 0;
+  const int64_t w_lo_max = A.window > 0 && w_max - A.window + 1 > 0 ? w_max - A.window + 1 : 0;
+  const int32_t* tab = A.table + it.request * A.max_blocks;
+  const int64_t page_bytes = (int64_t)D << A.log_page;
+  const int in_page = (1 << A.log_page) - 1;
+  const int64_t last_col = A.max_blocks - 1;
+
+  // staging: piece x = tid + 256 i is K token x / KS, channels 16 (x % KS)..,
+  // and V^T channel x / 4, tokens 16 (x % 4)..
+  u32x4_t kr[ST], vr[ST];
+  uint32_t ksc[ST], vsc;
+  bool vok;
+  int idk[ST], idv;
+  auto load_ids = [&](int64_t t) {
+#pragma unroll
+    for (int i = 0; i < ST; i++) {
+      const int64_t c = (t * TILE + (tid + KV_THREADS * i) / KS) >> A.log_page;
+      idk[i] = tab[c < last_col ? c : last_col];
+    }
+    const int64_t c = (t * TILE + 16 * (tid & 3)) >> A.log_page;
+    idv = tab[c < last_col ? c : last_col];
+  };
+  auto load = [&](int64_t t) {
+#pragma unroll
+    for (int i = 0; i < ST; i++) {
+      const int x = tid + KV_THREADS * i, tok = x / KS;
+      const int64_t block = (int64_t)(idk[i] >= 0 && idk[i] < A.num_pages ? idk[i] : 0) * A.kv_heads + kvh;
+      ksc[i] = A.k_scales[block];
+      kr[i] = ld16(A.k_codes + block * page_bytes + ((t * TILE + tok) & in_page) * D + 16 * (x % KS));
+    }
+    vok = idv >= 0 && idv < A.num_pages;
+    const int64_t block = (int64_t)(vok ? idv : 0) * A.kv_heads + kvh;
+    vsc = A.v_scales[block];
+#pragma unroll
+    for (int i = 0; i < ST; i++) {
+      const int d = (tid + KV_THREADS * i) / 4;
+      vr[i] = ld16(A.v_codes + block * page_bytes + ((int64_t)d << A.log_page) + ((t * TILE + 16 * (tid & 3)) & in_page));
+    }
+  };
+  auto store = [&](int64_t t, int buf) {
+#pragma unroll
+    for (int i = 0; i < ST; i++) {
+      const int x = tid + KV_THREADS * i, tok = x / KS, k = x % KS, u = tok >> 5, th = (tok >> 4) & 1, tr = tok & 15;
+      const int row = 8 * (tr >> 2) + 4 * th + (tr & 3);
+      const float s = e8m0_as_scale(ksc[i]);
+      uint8_t* p = sk[buf] + ((u * KS + k) * 64 + (row ^ (XK * k))) * 16;
+      *reinterpret_cast<bf16x8_t*>(p) = e4m3_bf16x8(kr[i][0], kr[i][1], s);
+      *reinterpret_cast<bf16x8_t*>(p + 32 * 16) = e4m3_bf16x8(kr[i][2], kr[i][3], s);
+    }
+    const int tg = tid & 3;
+    const int64_t j = t * TILE + 16 * tg;
+    float s = e8m0_as_scale(vsc);
+    const bool edge = !vok || j < lo || j + 16 > hi;
+    if (!vok || j + 16 <= lo || j >= hi) s = 1.0f;
+#pragma unroll
+    for (int i = 0; i < ST; i++) {
+      const int d = (tid + KV_THREADS * i) / 4;
+      u32x4_t w = vr[i];
+      if (edge) w = keep_tokens(w, j, vok ? lo : 0, vok ? hi : 0);
+      uint8_t* p = sv[buf] + (((d >> 5) * 4 + 2 * (tg >> 1)) * 64 + 32 * (tg & 1) + ((d & 31) ^ (2 * tg))) * 16;
+      *reinterpret_cast<bf16x8_t*>(p) = e4m3_bf16x8(w[0], w[1], s);
+      *reinterpret_cast<bf16x8_t*>(p + 64 * 16) = e4m3_bf16x8(w[2], w[3], s);
+    }
+    if (tid < 4) sok[buf][tid] = vok;
+  };
+
+  f32x16_t o[DT];
+#pragma unroll
+  for (int d = 0; d < DT; d++)
+#pragma unroll
+    for (int i = 0; i < 16; i++) o[d][i] = 0.0f;
+  float mx = -INFINITY, l = 0.0f;
+  const float c = CAP ? LOG2E : A.sm_scale * LOG2E;
+  const float inv_cap = CAP ? A.sm_scale / A.softcap : 0.0f;
+  if (t0 < t1) {
+    load_ids(t0);
+    load(t0);
+    load_ids(t0 + 1);
+    store(t0, 0);
+    load(t0 + 1);
+    load_ids(t0 + 2);
+  }
+  __syncthreads();
+  for (int64_t t = t0; t < t1; t++) {
+    const int buf = (int)(t - t0) & 1;
+    if (t + 1 < t1) {
+      store(t + 1, buf ^ 1);
+      load(t + 2);                            // past t1: a clamped column, not used
+      load_ids(t + 3);
+    }
+    const int64_t j0 = t * TILE;
+    if (w_last >= wrow && j0 <= w_max && j0 + TILE > w_lo_min) {
+      f32x16_t s[2];
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+#pragma unroll
+        for (int i = 0; i < 16; i++) s[u][i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KS; k++) {
+          const bf16x8_t a = *reinterpret_cast<const bf16x8_t*>(sk[buf] + ((u * KS + k) * 64 + 32 * h + (m ^ (XK * k))) * 16);
+          s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, qf[k], s[u], 0, 0, 0);
+        }
+      }
+      if constexpr (CAP) {
+#pragma unroll
+        for (int u = 0; u < 2; u++)
+#pragma unroll
+          for (int i = 0; i < 16; i++) s[u][i] = kv_softcap(s[u][i], A.softcap, inv_cap);
+      }
+      const bool ok0 = sok[buf][h], ok1 = sok[buf][2 + h];
+      if (j0 + TILE - 1 > w_min || j0 < w_lo_max || __any(!ok0 || !ok1)) {
+#pragma unroll
+        for (int u = 0; u < 2; u++)
+#pragma unroll
+          for (int i = 0; i < 16; i++) {
+            const int64_t j = j0 + 32 * u + 16 * h + i;
+            s[u][i] = j <= pos && j >= rlo && (u ? ok1 : ok0) ? s[u][i] : -INFINITY;
+          }
+      }
+      float mt = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < 2; u++)
+#pragma unroll
+        for (int i = 0; i < 16; i++) mt = __builtin_fmaxf(mt, s[u][i]);
+      mt = __builtin_fmaxf(mt, __shfl_xor(mt, 32, 64)) * c;
+      if (__any(mt > mx)) {
+        const float mn = __builtin_fmaxf(mx, mt);
+        const float f = mx == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx - mn);
+        mx = mn;
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < DT; d++) o[d] *= f;
+      }
+      const float off = mx == -INFINITY ? 0.0f : mx;
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+        uint32_t pw[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          const float a = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][2 * i], c, -off));
+          const float b = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][2 * i + 1], c, -off));
+          l += a + b;
+          pw[i] = pack_bf16x2(a, b);          // half a step of 2^-8 per probability, l keeps fp32
+        }
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          const bf16x8_t p = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[4 * e], pw[4 * e + 1], pw[4 * e + 2], pw[4 * e + 3]}));
+#pragma unroll
+          for (int d = 0; d < DT; d++) {
+            const bf16x8_t a = *reinterpret_cast<const bf16x8_t*>(
+                sv[buf] + ((d * 4 + 2 * u + e) * 64 + 32 * h + (m ^ (2 * (2 * u + h)))) * 16);
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, p, o[d], 0, 0, 0);
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+  l += __shfl_xor(l, 32, 64);
+  const bool split = it.splits > 1;
+  if (split && tid == 0 && kvh == 0)
+    part.rec[it.slot] = KvRec{it.split ? 0 : it.splits, it.rows, it.q0 * A.group + it.r0};
+  if (!live) return;
+  if (split) {
+    const int64_t at = (it.slot * A.kv_heads + kvh) * PROWS + wrow + m;
+#pragma unroll
+    for (int d = 0; d < DT; d++)
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        *reinterpret_cast<f32x4_t*>(part.sums + at * D + 32 * d + 8 * i + 4 * h) =
+            f32x4_t{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+    if (h == 0) {
+      part.stats[2 * at] = mx;
+      part.stats[2 * at + 1] = l;
+    }
+    return;
+  }
+  const int64_t orow = qrow * A.q_heads + kvh * A.group + r % A.group;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+  for (int d = 0; d < DT; d++)
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      *reinterpret_cast<u32x2_t*>(A.out + orow * D + 32 * d + 8 * i + 4 * h) =
+          u32x2_t{pack_bf16x2(o[d][4 * i] * inv, o[d][4 * i + 1] * inv),
+                  pack_bf16x2(o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv)};
+  if (A.lse && h == 0) A.lse[orow] = l == 0.0f ? -INFINITY : (mx + __builtin_log2f(l)) * LN2;
+}
+
+// Joins the splits of 16 rows of one head: thread (row, channels).
+template <int D, int R>
+__device__ __forceinline__ void kv_join(const KvArgs& A, const KvPart& part, int64_t slot, int sub, int kvh) {
+  if (slot >= part.used[0]) return;
+  const KvRec rec = part.rec[slot];
+  constexpr int CH = D / 16;
+  const int row = sub * 16 + threadIdx.x / 16, ch = (threadIdx.x % 16) * CH;
+  if (rec.splits == 0 || row >= rec.rows) return;
+  const int64_t step = (int64_t)A.kv_heads * R;
+  const int64_t at = (slot * A.kv_heads + kvh) * R + row;
+  float M = -INFINITY;
+  for (int s = 0; s < rec.splits; s++) M = __builtin_fmaxf(M, part.stats[2 * (at + s * step)]);
+  float L = 0.0f, acc[CH];
+#pragma unroll
+  for (int i = 0; i < CH; i++) acc[i] = 0.0f;
+  for (int s = 0; s < rec.splits; s++) {
+    const int64_t a = at + s * step;
+    const float ms = part.stats[2 * a];
+    const float f = ms == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ms - M);
+    L += f * part.stats[2 * a + 1];
+#pragma unroll
+    for (int i = 0; i < CH; i += 4) {
+      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(part.sums + a * D + ch + i);
+#pragma unroll
+      for (int e = 0; e < 4; e++) acc[i + e] = __builtin_fmaf(f, v[e], acc[i + e]);
+    }
+  }
+  const int64_t rr = rec.row0 + row;
+  const int64_t orow = rr / A.group * A.q_heads + kvh * A.group + rr % A.group;
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll
+  for (int i = 0; i < CH; i += 4)
+    *reinterpret_cast<u32x2_t*>(A.out + orow * D + ch + i) =
+        u32x2_t{pack_bf16x2(acc[i] * inv, acc[i + 1] * inv), pack_bf16x2(acc[i + 2] * inv, acc[i + 3] * inv)};
+  if (A.lse && ch == 0) A.lse[orow] = L == 0.0f ? -INFINITY : (M + __builtin_log2f(L)) * LN2;
+}
+
+// Workgroups of the decode slots first, then PROWS / 16 for each prompt slot.
+template <int D>
+__global__ __launch_bounds__(KV_THREADS) void k_kv_join(const KvArgs A, const KvPart dec, const KvPart pro,
+                                                        int64_t dec_slots) {
+  const int kvh = (int)(blockIdx.x % A.kv_heads);
+  const int64_t x = blockIdx.x / A.kv_heads;
+  if (x < dec_slots) kv_join<D, DROWS>(A, dec, x, 0, kvh);
+  else kv_join<D, PROWS>(A, pro, (x - dec_slots) / (PROWS / 16), (int)((x - dec_slots) % (PROWS / 16)), kvh);
 }
 
 int log2_page(int page) {
@@ -457,10 +1061,93 @@ wq_status wq_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v
   return wq_launch_status();
 }
 
+}  // extern "C"
+
+namespace {
+
+// Splits aimed at, over all key/value heads, and the fewest tiles of a split.
+constexpr int64_t DEC_ITEMS = 1024, PRO_ITEMS = 512;
+constexpr int DEC_MIN = 4, PRO_MIN = 4;
+
+// What a call launches and where its workspace lies.  Items per head are at
+// most splits + row tiles; slots (items of requests with two splits or more)
+// at most 2 * splits, and no more than the tiles of the table's width allow.
+struct KvPlan {
+  bool decode, prompt, join;
+  int64_t dec_splits, dec_items, dec_slots, pro_splits, pro_items, pro_slots;
+  size_t dec_rec, dec_sums, dec_stats, pro_used, pro_rec, pro_sums, pro_stats, bytes;
+};
+
+KvPlan kv_plan(int64_t batch, int64_t tokens, int64_t max_q, int q_heads, int kv_heads, int head_dim, int page,
+               int64_t max_blocks) {
+  KvPlan p = {};
+  const int64_t group = q_heads / kv_heads, reqs = batch < tokens ? batch : tokens;
+  const int64_t tiles = (max_blocks * page + TILE - 1) / TILE;
+  p.decode = true;
+  p.prompt = !(max_q > 0 && max_q * group <= DROWS) && tokens * group > DROWS;
+  p.dec_splits = (DEC_ITEMS + kv_heads - 1) / kv_heads;
+  p.pro_splits = (PRO_ITEMS + kv_heads - 1) / kv_heads;
+  const int64_t dec_rows = p.prompt ? reqs : tokens * group / DROWS + reqs;
+  const int64_t pro_rows = p.prompt ? tokens * group / PROWS + reqs : 0;
+  p.dec_items = dec_rows + p.dec_splits;
+  p.pro_items = p.prompt ? pro_rows + p.pro_splits : 0;
+  auto slots = [&](int64_t rows, int64_t splits, int min_tiles) {
+    if (tiles <= min_tiles) return (int64_t)0;
+    const int64_t most = (tiles + min_tiles - 1) / min_tiles;
+    return rows > 2 * splits / most ? 2 * splits : rows * most;
+  };
+  p.dec_slots = slots(dec_rows, p.dec_splits, DEC_MIN);
+  p.pro_slots = p.prompt ? slots(pro_rows, p.pro_splits, PRO_MIN) : 0;
+  p.join = p.dec_slots + p.pro_slots > 0;
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t a = at;
+    at += (n + 255) & ~(size_t)255;
+    return a;
+  };
+  take(8);
+  p.dec_rec = take(p.dec_slots * sizeof(KvRec));
+  p.dec_sums = take((size_t)p.dec_slots * kv_heads * DROWS * head_dim * 4);
+  p.dec_stats = take((size_t)p.dec_slots * kv_heads * DROWS * 8);
+  p.pro_used = take(8);
+  p.pro_rec = take(p.pro_slots * sizeof(KvRec));
+  p.pro_sums = take((size_t)p.pro_slots * kv_heads * PROWS * head_dim * 4);
+  p.pro_stats = take((size_t)p.pro_slots * kv_heads * PROWS * 8);
+  p.bytes = at;
+  return p;
+}
+
+bool kv_sizes_ok(int64_t batch, int64_t tokens, int64_t max_q, int32_t q_heads, int32_t kv_heads, int32_t page,
+                 int64_t max_blocks) {
+  return batch >= 0 && batch <= 0x7FFFFFFF && tokens >= 0 && tokens <= 0x7FFFFFFF && max_q >= 0 &&
+         max_q <= 0x7FFFFFFF && kv_heads >= 1 && q_heads >= kv_heads && q_heads % kv_heads == 0 && q_heads <= 65535 &&
+         max_blocks >= 1 && max_blocks <= 0x7FFFFFFF / page;
+}
+
+template <int D, bool CAP>
+void launch_attention(const KvArgs& A, const KvPlan& p, const KvPart& dec, const KvPart& pro, hipStream_t s) {
+  const unsigned h = (unsigned)A.kv_heads;
+  if (p.prompt) {
+    k_kv_prompt<D, CAP><<<(unsigned)p.pro_items * h, KV_THREADS, 0, s>>>(A, pro);
+    k_kv_decode<D, CAP, REQ_SHORT><<<(unsigned)p.dec_items * h, KV_THREADS, 0, s>>>(A, dec);
+  } else {
+    k_kv_decode<D, CAP, REQ_ALL><<<(unsigned)p.dec_items * h, KV_THREADS, 0, s>>>(A, dec);
+  }
+  if (p.join)
+    k_kv_join<D><<<(unsigned)((p.dec_slots + p.pro_slots * (PROWS / 16)) * h), KV_THREADS, 0, s>>>(A, dec, pro,
+                                                                                               p.dec_slots);
+}
+
+}  // namespace
+
+extern "C" {
+
 size_t wq_kv_attention_workspace_size(int64_t batch, int64_t tokens, int64_t max_q, int32_t q_heads, int32_t kv_heads,
                                       int32_t head_dim, int32_t page, int64_t max_blocks) {
-  (void)batch, (void)tokens, (void)max_q, (void)q_heads, (void)kv_heads, (void)head_dim, (void)page, (void)max_blocks;
-  return 0;
+  if ((head_dim != 64 && head_dim != 128) || log2_page(page) < 0 ||
+      !kv_sizes_ok(batch, tokens, max_q, q_heads, kv_heads, page, max_blocks))
+    return 0;
+  return kv_plan(batch, tokens, max_q, q_heads, kv_heads, head_dim, page, max_blocks).bytes;
 }
 
 wq_status wq_kv_attention(const void* q_bf16, int64_t q_stride, const int32_t* cu_q, const int32_t* kv_lens,
@@ -470,9 +1157,7 @@ wq_status wq_kv_attention(const void* q_bf16, int64_t q_stride, const int32_t* c
                           int64_t max_blocks, float sm_scale, float softcap, int64_t window, uint16_t* out,
                           float* lse, void* workspace, size_t ws_bytes, void* stream) {
   if ((head_dim != 64 && head_dim != 128) || log2_page(page) < 0) return WQ_EUNSUPPORTED;
-  if (batch < 0 || batch > 0x7FFFFFFF || tokens < 0 || tokens > 0x7FFFFFFF || max_q < 0 || kv_heads < 1 ||
-      q_heads < kv_heads || q_heads % kv_heads || q_heads > 65535 || num_pages < 1 || max_blocks < 1 ||
-      max_blocks > 0x7FFFFFFF / page || window < 0)
+  if (!kv_sizes_ok(batch, tokens, max_q, q_heads, kv_heads, page, max_blocks) || num_pages < 1 || window < 0)
     return WQ_EINVAL;
   if (!(sm_scale > 0.0f) || !(sm_scale < INFINITY) || !(softcap >= 0.0f) || !(softcap < INFINITY)) return WQ_EINVAL;
   const int64_t row = (int64_t)q_heads * head_dim;
@@ -484,19 +1169,26 @@ wq_status wq_kv_attention(const void* q_bf16, int64_t q_stride, const int32_t* c
   if (batch > 0 && tokens > 0 && (!q_bf16 || !cu_q || !kv_lens || !block_table || !out)) return WQ_EINVAL;
   if (!wq_aligned(q_bf16) || !wq_aligned(out) || !wq_aligned(k_codes) || !wq_aligned(v_codes) || !wq_aligned(workspace))
     return WQ_EALIGN;
-  if (ws_bytes < wq_kv_attention_workspace_size(batch, tokens, max_q, q_heads, kv_heads, head_dim, page, max_blocks))
-    return WQ_EINVAL;
   if (batch == 0 || tokens == 0) return WQ_OK;
-  const dim3 grid((unsigned)tokens, (unsigned)q_heads);
-  const int lp = log2_page(page);
-  if (head_dim == 128)
-    k_kv_attention<128><<<grid, 64, 0, (hipStream_t)stream>>>(
-        (const uint16_t*)q_bf16, q_stride, cu_q, kv_lens, batch, tokens, q_heads, kv_heads, k_codes, k_scales, v_codes,
-        v_scales, lp, num_pages, block_table, max_blocks, sm_scale, softcap, window, out, lse);
-  else
-    k_kv_attention<64><<<grid, 64, 0, (hipStream_t)stream>>>(
-        (const uint16_t*)q_bf16, q_stride, cu_q, kv_lens, batch, tokens, q_heads, kv_heads, k_codes, k_scales, v_codes,
-        v_scales, lp, num_pages, block_table, max_blocks, sm_scale, softcap, window, out, lse);
+  const KvPlan p = kv_plan(batch, tokens, max_q, q_heads, kv_heads, head_dim, page, max_blocks);
+  if (ws_bytes < p.bytes || !workspace) return WQ_EINVAL;
+  if ((p.pro_items > p.dec_items ? p.pro_items : p.dec_items) * kv_heads > 0x7FFFFFFF / KV_THREADS) return WQ_EINVAL;
+  const KvArgs A = {(const uint16_t*)q_bf16, q_stride, cu_q, kv_lens, batch, tokens, q_heads, kv_heads,
+                    q_heads / kv_heads, k_codes, k_scales, v_codes, v_scales, log2_page(page), num_pages, block_table,
+                    max_blocks, sm_scale, softcap, window, out, lse};
+  uint8_t* ws = (uint8_t*)workspace;
+  const KvPart dec = {p.dec_splits, DEC_MIN, (int64_t*)ws, (KvRec*)(ws + p.dec_rec), (float*)(ws + p.dec_sums),
+                      (float*)(ws + p.dec_stats)};
+  const KvPart pro = {p.pro_splits, PRO_MIN, (int64_t*)(ws + p.pro_used), (KvRec*)(ws + p.pro_rec),
+                      (float*)(ws + p.pro_sums), (float*)(ws + p.pro_stats)};
+  hipStream_t s = (hipStream_t)stream;
+  if (head_dim == 128) {
+    if (softcap > 0.0f) launch_attention<128, true>(A, p, dec, pro, s);
+    else launch_attention<128, false>(A, p, dec, pro, s);
+  } else {
+    if (softcap > 0.0f) launch_attention<64, true>(A, p, dec, pro, s);
+    else launch_attention<64, false>(A, p, dec, pro, s);
+  }
   return wq_launch_status();
 }
 
