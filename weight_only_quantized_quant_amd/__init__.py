@@ -403,18 +403,42 @@ def wq_moe_gemm_w4a8(x8: torch.Tensor, a_scale: torch.Tensor, row_token, offsets
 # ---------------------------------------------------------------------------
 # 8-bit key/value cache
 # ---------------------------------------------------------------------------
-def _same_device(t, device, name):
-    _dev(t, name)
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-
-
-def _index(t, dtype, shape, device, name):
-    """A contiguous device tensor of integers on `device`."""
-    _same_device(t, device, name)
-    if t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}")
+# These calls are made once per layer of a decode step, where the host's time is the
+# operator's time: one look at a tensor that is as it should be, the words only when it is not.
+def _on(t, dev, dtype, name):
+    """A contiguous tensor of `dtype` on GPU `dev`."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous():
+        _dev(t, name)
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+        raise ValueError(f"{name} is on {t.device}, the first argument on cuda:{dev}")
     return t.data_ptr()
+
+
+def _index(t, dev, dtype, shape, name):
+    """The same, of a given shape."""
+    ptr = _on(t, dev, dtype, name)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be of shape {shape}, not {tuple(t.shape)}")
+    return ptr
+
+
+class _Launch:
+    """The launch goes to the tensors' device, whichever is current, and to its current stream."""
+
+    def __init__(self, dev):
+        self.dev = dev
+
+    def __enter__(self):
+        self.back = torch.cuda.current_device()
+        if self.back != self.dev:
+            torch.cuda.set_device(self.dev)
+        return torch._C._cuda_getCurrentRawStream(self.dev)
+
+    def __exit__(self, *exc):
+        if self.back != self.dev:
+            torch.cuda.set_device(self.back)
+        return False
 
 
 def _token_rows(t, name):
@@ -425,20 +449,16 @@ def _token_rows(t, name):
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim]")
     n, h, d = t.shape
-    if n <= 1 and t.is_contiguous():
-        return h * d
     sn, sh, sd = t.stride()
     if sd != 1 or (sh != d and h > 1):
         raise ValueError(f"the heads of a token of {name} must be dense")
     return sn if n > 1 else h * d
 
 
-def _kv_cache(k_codes, k_scales, v_codes, v_scales, device):
-    """(num_pages, heads, page, head_dim) of a cache."""
-    for t, name in ((k_codes, "k_codes"), (k_scales, "k_scales"), (v_codes, "v_codes"), (v_scales, "v_scales")):
-        _same_device(t, device, name)
-        if t.dtype != torch.uint8:
-            raise ValueError(f"{name} must be uint8")
+def _kv_cache(k_codes, k_scales, v_codes, v_scales, dev):
+    """(num_pages, heads, page, head_dim) of a cache and the addresses of its four tensors."""
+    kc, ks = _on(k_codes, dev, torch.uint8, "k_codes"), _on(k_scales, dev, torch.uint8, "k_scales")
+    vc, vs = _on(v_codes, dev, torch.uint8, "v_codes"), _on(v_scales, dev, torch.uint8, "v_scales")
     if k_codes.dim() != 4:
         raise ValueError("k_codes must be [num_pages, heads, page, head_dim]")
     n, h, p, d = k_codes.shape
@@ -446,12 +466,7 @@ def _kv_cache(k_codes, k_scales, v_codes, v_scales, device):
         raise ValueError("v_codes must be [num_pages, heads, head_dim, page]")
     if k_scales.shape != (n, h) or v_scales.shape != (n, h):
         raise ValueError("k_scales and v_scales must be [num_pages, heads]")
-    return n, h, p, d
-
-
-def _on(device):
-    """The launch goes to the tensors' device, whichever is current."""
-    return torch.cuda.device(device)
+    return n, h, p, d, kc, ks, vc, vs
 
 
 def wq_kv_blocks(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor, block_table: torch.Tensor,
@@ -462,34 +477,28 @@ def wq_kv_blocks(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: tor
     cu_new int32 [B + 1], kv_lens int32 [B], state int32 [2]: the next cursor and the number of
     refused requests)."""
     _dev(ctx_lens, "ctx_lens")
-    d = ctx_lens.device
+    dev = ctx_lens.get_device()
     if ctx_lens.dtype != torch.int32 or ctx_lens.dim() != 1:
         raise ValueError("ctx_lens must be int32 [batch]")
     B = ctx_lens.shape[0]
-    nl = _index(new_lens, torch.int32, (B,), d, "new_lens")
-    _same_device(free_pages, d, "free_pages")
-    _same_device(block_table, d, "block_table")
-    if free_pages.dtype != torch.int32 or free_pages.dim() != 1:
-        raise ValueError("free_pages must be int32 [pages]")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table must be int32 [batch, max_blocks]")
+    nl = _index(new_lens, dev, torch.int32, (B,), "new_lens")
+    free = _on(free_pages, dev, torch.int32, "free_pages")
+    table = _on(block_table, dev, torch.int32, "block_table")
+    if free_pages.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("free_pages must be [pages] and block_table [batch, max_blocks]")
     cur = None
     if cursor is not None:
-        _same_device(cursor, d, "cursor")
-        if cursor.dtype != torch.int32 or cursor.numel() < 1:
-            raise ValueError("cursor must be int32 of at least one element")
-        cur = cursor.data_ptr()
-    tokens = int(tokens)
+        cur = _on(cursor, dev, torch.int32, "cursor")
+        if cursor.numel() < 1:
+            raise ValueError("cursor must have an element")
     if tokens < 0:
         raise ValueError("tokens must not be negative")
-    with _on(d):
-        slots = torch.empty(tokens, dtype=torch.int64, device=d)
-        positions, cu_new, kv_lens, state = torch.empty(tokens + 2 * B + 3, dtype=torch.int32,
-                                                        device=d).split((tokens, B + 1, B, 2))
-        _check(lib.wq_kv_blocks(ctx_lens.data_ptr(), nl, B, free_pages.data_ptr(), free_pages.shape[0], cur, page,
-                                block_table.data_ptr(), block_table.shape[1], tokens, slots.data_ptr(),
-                                positions.data_ptr(), cu_new.data_ptr(), kv_lens.data_ptr(), state.data_ptr(),
-                                _stream()), "wq_kv_blocks")
+    with _Launch(dev) as stream:
+        slots = ctx_lens.new_empty(tokens, dtype=torch.int64)
+        positions, cu_new, kv_lens, state = ctx_lens.new_empty(tokens + 2 * B + 3).split((tokens, B + 1, B, 2))
+        _check(lib.wq_kv_blocks(ctx_lens.data_ptr(), nl, B, free, free_pages.shape[0], cur, page, table,
+                                block_table.shape[1], tokens, slots.data_ptr(), positions.data_ptr(),
+                                cu_new.data_ptr(), kv_lens.data_ptr(), state.data_ptr(), stream), "wq_kv_blocks")
     return slots, positions, cu_new, kv_lens, state
 
 
@@ -498,17 +507,16 @@ def wq_kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_codes:
     """Quantize k, v (bf16/fp32 [tokens, heads, head_dim], tokens may be strided) into their slots
     (int64 [tokens], negative: skipped) of the cache: codes uint8 [N, heads, page, head_dim] and
     [N, heads, head_dim, page], E8M0 scales uint8 [N, heads]."""
-    ks, vs = _token_rows(k, "k"), _token_rows(v, "v")
-    d = k.device
-    n, h, p, dim = _kv_cache(k_codes, k_scales, v_codes, v_scales, d)
-    if k.shape[1] != h or k.shape[2] != dim or v.shape != k.shape or v.dtype != k.dtype or v.device != d:
-        raise ValueError(f"k and v must be [tokens, {h}, {dim}] of one dtype on one device")
+    k_stride, v_stride = _token_rows(k, "k"), _token_rows(v, "v")
+    dev = k.get_device()
+    n, h, p, dim, kc, ks, vc, vs = _kv_cache(k_codes, k_scales, v_codes, v_scales, dev)
     T = k.shape[0]
-    sp = _index(slots, torch.int64, (T,), d, "slots")
-    with _on(d):
-        _check(lib.wq_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, _x_dtype(k), sp, T, h, dim, p, n,
-                                k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
-                                _stream()), "wq_kv_append")
+    if k.shape != (T, h, dim) or v.shape != k.shape or v.dtype != k.dtype or v.get_device() != dev:
+        raise ValueError(f"k and v must be [tokens, {h}, {dim}] of one dtype on one device")
+    sp = _index(slots, dev, torch.int64, (T,), "slots")
+    with _Launch(dev) as stream:
+        _check(lib.wq_kv_append(k.data_ptr(), k_stride, v.data_ptr(), v_stride, _x_dtype(k), sp, T, h, dim, p, n, kc,
+                                ks, vc, vs, stream), "wq_kv_append")
 
 
 def wq_kv_attention_workspace_size(batch: int, tokens: int, max_q: int, q_heads: int, kv_heads: int, head_dim: int,
@@ -525,35 +533,35 @@ def wq_kv_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tens
     cu_q int32 [B + 1], kv_lens int32 [B], block_table int32 [B, W].  sm_scale defaults to
     head_dim ** -0.5; max_q: the largest number of queries of one request if known.  Returns out
     bf16 [tokens, q_heads, head_dim] (and lse fp32 [tokens, q_heads])."""
-    qs = _token_rows(q, "q")
-    d = q.device
-    n, h, p, dim = _kv_cache(k_codes, k_scales, v_codes, v_scales, d)
+    q_stride = _token_rows(q, "q")
+    dev = q.get_device()
+    n, h, p, dim, kc, ks, vc, vs = _kv_cache(k_codes, k_scales, v_codes, v_scales, dev)
     T, hq, qd = q.shape
-    if q.dtype != torch.bfloat16 or qd != dim:
+    if q.dtype is not torch.bfloat16 or qd != dim:
         raise ValueError(f"q must be bfloat16 [tokens, q_heads, {dim}]")
-    _same_device(block_table, d, "block_table")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2:
-        raise ValueError("block_table must be int32 [batch, max_blocks]")
+    table = _on(block_table, dev, torch.int32, "block_table")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [batch, max_blocks]")
     B, width = block_table.shape
-    cu = _index(cu_q, torch.int32, (B + 1,), d, "cu_q")
-    kl = _index(kv_lens, torch.int32, (B,), d, "kv_lens")
+    cu = _index(cu_q, dev, torch.int32, (B + 1,), "cu_q")
+    kl = _index(kv_lens, dev, torch.int32, (B,), "kv_lens")
     if sm_scale is None:
         sm_scale = dim ** -0.5
-    if out is not None:
-        _same_device(out, d, "out")
-    with _on(d):
-        out = _out(out, (T, hq, dim), torch.bfloat16, d, "out")
-        lse = torch.empty((T, hq), dtype=torch.float32, device=d) if return_lse else None
-        need = lib.wq_kv_attention_workspace_size(B, T, max_q, hq, h, dim, p, width)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=d) if need else None
+    with _Launch(dev) as stream:
+        if out is None:
+            out = q.new_empty((T, hq, dim))
         else:
-            _same_device(workspace, d, "workspace")
-        ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-        _check(lib.wq_kv_attention(q.data_ptr(), qs, cu, kl, B, T, max_q, hq, h, dim, k_codes.data_ptr(),
-                                   k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), p, n,
-                                   block_table.data_ptr(), width, float(sm_scale), float(softcap), int(window),
-                                   out.data_ptr(), lse.data_ptr() if return_lse else None, ws, ws_bytes, _stream()),
+            _index(out, dev, torch.bfloat16, (T, hq, dim), "out")
+        lse = q.new_empty((T, hq), dtype=torch.float32) if return_lse else None
+        if workspace is None:
+            ws_bytes = lib.wq_kv_attention_workspace_size(B, T, max_q, hq, h, dim, p, width)
+            workspace = q.new_empty(ws_bytes, dtype=torch.uint8)
+        else:
+            _on(workspace, dev, workspace.dtype, "workspace")
+            ws_bytes = workspace.numel() * workspace.element_size()
+        _check(lib.wq_kv_attention(q.data_ptr(), q_stride, cu, kl, B, T, max_q, hq, h, dim, kc, ks, vc, vs, p, n,
+                                   table, width, sm_scale, softcap, window, out.data_ptr(),
+                                   lse.data_ptr() if return_lse else None, workspace.data_ptr(), ws_bytes, stream),
                "wq_kv_attention")
     return (out, lse) if return_lse else out
 

@@ -13,6 +13,7 @@ using namespace wq;
 namespace {
 
 constexpr int KV_THREADS = 256;
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 
 // ---------------------------------------------------------------------------
 // Block tables and slot maps
@@ -27,12 +28,22 @@ __device__ __forceinline__ int64_t wave_scan(int64_t v, int lane) {
   return v;
 }
 
+// The first of `count` running sums that is above v (the last one is).
+__device__ __forceinline__ int first_above(const int64_t* sums, int count, int64_t v) {
+  int a = 0, z = count - 1;
+  while (a < z) {
+    const int mid = (a + z) >> 1;
+    if (sums[mid] > v) z = mid;
+    else a = mid + 1;
+  }
+  return a;
+}
+
 // Every workgroup scans the lengths of all requests (256 at a time: running
 // sums of new tokens and of the pages needed, kept in LDS for the chunk) and
 // writes its own rows of the token arrays, found by binary search in the
-// chunk's token ends, and the table rows of the requests i with
-// i % workgroups equal to its own number, one wave a row.  Workgroup 0 writes
-// the per-request outputs.  There is no dependence between workgroups, so one
+// chunk's token ends, and its share of the new table entries, found in the
+// same way.  Workgroup 0 writes the per-request outputs.  There is no dependence between workgroups, so one
 // launch does it all: the new pages of a token come from the free list
 // itself, not from the table that another workgroup fills.
 __global__ __launch_bounds__(KV_THREADS) void k_kv_blocks(
@@ -42,7 +53,8 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_blocks(
     int32_t* __restrict__ positions, int32_t* __restrict__ cu_new, int32_t* __restrict__ kv_lens,
     int32_t* __restrict__ state) {
   __shared__ int64_t ends[KV_THREADS];       // token rows up to and with each request of the chunk
-  __shared__ int64_t firsts[KV_THREADS];     // its first new page's place in free_pages, -1 if refused
+  __shared__ int64_t page_ends[KV_THREADS];  // places of free_pages up to and with its new pages
+  __shared__ int64_t firsts[KV_THREADS];     // the place of its first new page, -1 if refused
   __shared__ int32_t ctxs[KV_THREADS];
   __shared__ int32_t news[KV_THREADS];
   __shared__ int64_t wave_sum[2][KV_THREADS / 64];
@@ -89,31 +101,25 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_blocks(
         kv_lens[i] = ok ? (int32_t)after : c;
       }
     }
-    const int64_t tok_first = tok_before;
+    page_ends[tid] = first + need;
+    const int64_t tok_first = tok_before, page_first = page_before;
     for (int w = 0; w < KV_THREADS / 64; w++) {
       tok_before += wave_sum[0][w];
       page_before += wave_sum[1][w];
     }
     __syncthreads();
     const int count = (int)(batch - base < KV_THREADS ? batch - base : KV_THREADS);
-    // table rows
-    const int64_t off = base % gridDim.x;
-    int r0 = (int)(((int64_t)blockIdx.x + gridDim.x - off) % gridDim.x);
-    for (int64_t r = r0 + (int64_t)wave * gridDim.x; r < count; r += (int64_t)gridDim.x * (KV_THREADS / 64)) {
-      const int64_t f = firsts[r];
-      if (f < 0) continue;
-      const int64_t h = (ctxs[r] + page - 1) >> log_page, t = ((int64_t)ctxs[r] + news[r] + page - 1) >> log_page;
-      for (int64_t j = h + lane; j < t; j += 64) table[(base + r) * max_blocks + j] = free_pages[f + j - h];
+    // table entries: the chunk's new pages in turn, each found in the running sums
+    const int64_t pages = page_before - page_first;
+    for (int64_t j = (int64_t)blockIdx.x * KV_THREADS + tid; j < pages; j += (int64_t)gridDim.x * KV_THREADS) {
+      const int a = first_above(page_ends, count, page_first + j);
+      const int64_t col = (((int64_t)ctxs[a] + news[a] + page - 1) >> log_page) - (page_ends[a] - (page_first + j));
+      if (firsts[a] >= 0) table[(base + a) * max_blocks + col] = free_pages[page_first + j];
     }
     // token rows of this chunk's requests
     const int64_t lo = row0 > tok_first ? row0 : tok_first, hi = row1 < tok_before ? row1 : tok_before;
     for (int64_t row = lo + tid; row < hi; row += KV_THREADS) {
-      int a = 0, z = count - 1;               // the first request whose end is behind the row
-      while (a < z) {
-        const int mid = (a + z) >> 1;
-        if (ends[mid] > row) z = mid;
-        else a = mid + 1;
-      }
+      const int a = first_above(ends, count, row);
       int64_t slot = -1;
       const int64_t pos = ctxs[a] + row - (ends[a] - news[a]);
       if (firsts[a] >= 0) {
@@ -173,60 +179,164 @@ __device__ __forceinline__ uint32_t e4m3_word_shifted(uint32_t w, int shift) {
   return e4m3_word(v);
 }
 
-// The least E8M0 code c with amax <= 448 * 2^(c-127): 448 = 1.75 * 2^8, so
+// The least E8M0 code c with amax <= 448 * 2^(c-127), amax as its bits: 448 = 1.75 * 2^8, so
 // the biased exponent less 8, one more where the fraction is above .75.
-__device__ __forceinline__ int e8m0_cover(float amax) {
-  const uint32_t bits = __float_as_uint(amax);
+__device__ __forceinline__ int e8m0_cover(uint32_t bits) {
   const int c = (int)(bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   return c > 0 ? c : 0;
 }
 
+// Eight elements as they were loaded.
+template <bool BF16>
+struct Raw8 {
+  uint32_t w[BF16 ? 4 : 8];
+  // the larger of m and the magnitudes, as bit patterns: one half word each for
+  // bf16 (both halves of m), one word for fp32; NaN and infinity come out largest
+  __device__ __forceinline__ uint32_t magnitude(uint32_t m) const {
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 4 : 8); i++) {
+      if constexpr (BF16) {
+        const u16x2_t a = __builtin_bit_cast(u16x2_t, w[i] & 0x7FFF7FFFu), b = __builtin_bit_cast(u16x2_t, m);
+        m = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(a, b));
+      } else {
+        const uint32_t a = w[i] & 0x7FFFFFFFu;
+        m = a > m ? a : m;
+      }
+    }
+    return m;
+  }
+  __device__ __forceinline__ void widen(float v[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+      v[i] = BF16 ? (i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2])) : __uint_as_float(w[BF16 ? 0 : i]);
+  }
+  // E4M3 codes of x * 2^(127-c); the finite magnitudes are at most 448 then
+  __device__ __forceinline__ u32x2_t codes(float scale_as_e8m0) const {
+    u32x2_t out;
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      s16x2_t r = {0, 0};
+      if constexpr (BF16) {
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, w[2 * h]), scale_as_e8m0, false);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, w[2 * h + 1]), scale_as_e8m0, true);
+      } else {
+        const uint32_t* f = w + (BF16 ? 0 : 4 * h);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, __uint_as_float(f[0]), __uint_as_float(f[1]), scale_as_e8m0, false);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, __uint_as_float(f[2]), __uint_as_float(f[3]), scale_as_e8m0, true);
+      }
+      out[h] = __builtin_bit_cast(uint32_t, r);
+    }
+    return out;
+  }
+};
+
 // One run (tokens t .. t+n-1 at offsets off .. off+n-1 of one page) of one
-// head, keys or values, by the whole workgroup.  The run stays in registers
-// between its maximum and its codes.
-template <bool BF16, bool VALUES, int D, int R>
+// head, keys or values, by the whole workgroup.  A thread takes 8 channels of
+// the 4 tokens of an aligned quad of the page and keeps them in registers
+// between the run's maximum and its codes: values then leave as words of 4
+// tokens, which LDS turns into whole rows of the transposed page.  Bound by
+// bytes, so the arithmetic is kept to one and a half instructions an element:
+// maxima of bit patterns, two for bf16 at a time, and conversions that take
+// the scale; a run that holds a NaN or an infinity goes the long way.
+template <bool BF16, bool VALUES, int D, int PAGE>
 __device__ __forceinline__ void append_run(const void* __restrict__ x, int64_t stride, int64_t t, int n, int off,
-                                           int page, uint8_t* __restrict__ codes, uint8_t* __restrict__ scale,
-                                           uint8_t* lds, float* red) {
-  constexpr int CH = D / 8;                   // 8-element pieces of a token
-  const int tid = threadIdx.x;
+                                           uint8_t* __restrict__ codes, uint8_t* __restrict__ scale, uint8_t* lds,
+                                           uint32_t* red) {
+  constexpr int CH = D / 8, ITEMS = PAGE / 4 * CH, R = (ITEMS + KV_THREADS - 1) / KV_THREADS, LROW = PAGE + 4;
+  const int tid = threadIdx.x, end = off + n;
   const int old = off ? (int)*scale : 0;
-  float v[R][8];
-  float m = 0.0f;
+  Raw8<BF16> v[R][4];
+  uint32_t m = 0;
 #pragma unroll
   for (int r = 0; r < R; r++) {
-    const int p = r * KV_THREADS + tid;
-    if (p < n * CH) {
-      load8<BF16>(x, (t + p / CH) * stride + (p % CH) * 8, v[r]);
+    const int p = r * KV_THREADS + tid, o = p / CH * 4;            // o: first offset of the quad
 #pragma unroll
-      for (int i = 0; i < 8; i++) {
-        const float a = __builtin_fabsf(v[r][i]);
-        m = a < INFINITY ? __builtin_fmaxf(m, a) : m;
+    for (int i = 0; i < 4; i++) {
+      const bool in = o + i >= off && o + i < end;
+      const uint8_t* from = (const uint8_t*)x + ((t + (in ? o + i - off : 0)) * stride + (p % CH) * 8) * (BF16 ? 2 : 4);
+#pragma unroll
+      for (int e = 0; e < (BF16 ? 1 : 2); e++) {
+        const u32x4_t q = in ? ld16(from + 16 * e) : u32x4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int b = 0; b < 4; b++) v[r][i].w[4 * e + b] = q[b];
       }
     }
   }
-  m = group_max(m, 64);
-  if ((tid & 63) == 0) red[tid >> 6] = m;
-  __syncthreads();
-  m = __builtin_fmaxf(__builtin_fmaxf(red[0], red[1]), __builtin_fmaxf(red[2], red[3]));
+#pragma unroll
+  for (int r = 0; r < R; r++)
+#pragma unroll
+    for (int i = 0; i < 4; i++) m = v[r][i].magnitude(m);
+  if constexpr (BF16) m = (m & 0xFFFFu) > (m >> 16) ? m << 16 : m & 0xFFFF0000u;
+  auto join = [&](uint32_t a) {               // the largest over the workgroup
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const uint32_t b = (uint32_t)__shfl_xor((int)a, o, 64);
+      a = a > b ? a : b;
+    }
+    if ((tid & 63) == 0) red[tid >> 6] = a;
+    __syncthreads();
+    a = red[0] > red[1] ? red[0] : red[1];
+    const uint32_t b = red[2] > red[3] ? red[2] : red[3];
+    return a > b ? a : b;
+  };
+  m = join(m);
+  const bool odd = m >= 0x7F800000u;          // NaN or infinity: the maximum of the others, element by element
+  if (odd) {
+    m = 0;
+#pragma unroll
+    for (int r = 0; r < R; r++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        float f[8];
+        v[r][i].widen(f);
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          const uint32_t a = __float_as_uint(f[e]) & 0x7FFFFFFFu;
+          m = a < 0x7F800000u && a > m ? a : m;
+        }
+      }
+    __syncthreads();
+    m = join(m);
+  }
   const int need = e8m0_cover(m);
   const int c = need > old ? need : old;
   const int moved = off && c > old ? off : 0; // tokens before the run whose codes change
   if (tid == 0 && (!off || c != old)) *scale = (uint8_t)c;
+  const float sc = e8m0_as_scale((uint32_t)c);
 #pragma unroll
   for (int r = 0; r < R; r++) {
-    const int p = r * KV_THREADS + tid;
-    if (p < n * CH) {
-      float q[8];
+    const int p = r * KV_THREADS + tid, o = p / CH * 4, ch = (p % CH) * 8;
+    if (o + 3 < off || o >= end) continue;
+    u32x2_t w[4];
 #pragma unroll
-      for (int i = 0; i < 8; i++) q[i] = __builtin_ldexpf(v[r][i], 127 - c);
-      const u32x2_t w = {e4m3_word(q), e4m3_word(q + 4)};
-      if constexpr (!VALUES) {
-        *reinterpret_cast<u32x2_t*>(codes + (off + p / CH) * D + (p % CH) * 8) = w;
+    for (int i = 0; i < 4; i++) {
+      if (!odd) {
+        w[i] = v[r][i].codes(sc);
       } else {
-        uint8_t* o = lds + (p % CH) * 8 * (page + 4) + off + p / CH;
+        float q[8];
+        v[r][i].widen(q);
 #pragma unroll
-        for (int i = 0; i < 8; i++) o[i * (page + 4)] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+        for (int e = 0; e < 8; e++) q[e] = __builtin_ldexpf(q[e], 127 - c);
+        w[i] = u32x2_t{e4m3_word(q), e4m3_word(q + 4)};
+      }
+    }
+    if constexpr (!VALUES) {
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        if (o + i >= off && o + i < end) *reinterpret_cast<u32x2_t*>(codes + (o + i) * D + ch) = w[i];
+    } else {
+      // 4 tokens x 4 channels at a time: bytes of one channel into one word
+#pragma unroll
+      for (int hf = 0; hf < 2; hf++) {
+        const uint32_t lo01 = __builtin_amdgcn_perm(w[1][hf], w[0][hf], 0x05010400u);
+        const uint32_t hi01 = __builtin_amdgcn_perm(w[1][hf], w[0][hf], 0x07030602u);
+        const uint32_t lo23 = __builtin_amdgcn_perm(w[3][hf], w[2][hf], 0x05010400u);
+        const uint32_t hi23 = __builtin_amdgcn_perm(w[3][hf], w[2][hf], 0x07030602u);
+        uint32_t* l = reinterpret_cast<uint32_t*>(lds + (ch + 4 * hf) * LROW + o);
+        l[0] = __builtin_amdgcn_perm(lo23, lo01, 0x05040100u);
+        l[LROW / 4] = __builtin_amdgcn_perm(lo23, lo01, 0x07060302u);
+        l[2 * (LROW / 4)] = __builtin_amdgcn_perm(hi23, hi01, 0x05040100u);
+        l[3 * (LROW / 4)] = __builtin_amdgcn_perm(hi23, hi01, 0x07060302u);
       }
     }
   }
@@ -237,24 +347,31 @@ __device__ __forceinline__ void append_run(const void* __restrict__ x, int64_t s
     }
   } else {
     __syncthreads();
-    const int w0 = moved ? 0 : off >> 2, words = ((off + n + 3) >> 2) - w0;
-    for (int p = tid; p < D * words; p += KV_THREADS) {
-      const int d = p / words, w = w0 + p % words;
-      uint8_t* g = codes + d * page + 4 * w;
-      const uint32_t fresh = *reinterpret_cast<const uint32_t*>(lds + d * (page + 4) + 4 * w);
-      // bytes [a, z) of the word are this run's
-      const int a = off - 4 * w > 0 ? off - 4 * w : 0, z = off + n - 4 * w < 4 ? off + n - 4 * w : 4;
-      if (a == 0 && z == 4) {
-        *reinterpret_cast<uint32_t*>(g) = fresh;
-      } else if (moved && a > 0) {
-        const uint32_t had = *reinterpret_cast<const uint32_t*>(g);
-        const uint32_t kept = e4m3_word_shifted(had, old - c);
-        uint32_t res = 0;
+    if (n == PAGE) {                          // a whole page: 16-byte stores
+      for (int p = tid; p < D * PAGE / 16; p += KV_THREADS) {
+        const uint32_t* l = reinterpret_cast<const uint32_t*>(lds + p / (PAGE / 16) * LROW + p % (PAGE / 16) * 16);
+        *reinterpret_cast<u32x4_t*>(codes + p * 16) = u32x4_t{l[0], l[1], l[2], l[3]};
+      }
+    } else {
+      const int w0 = moved ? 0 : off >> 2, words = ((end + 3) >> 2) - w0;
+      for (int p = tid; p < D * words; p += KV_THREADS) {
+        const int d = p / words, w = w0 + p % words;
+        uint8_t* g = codes + d * PAGE + 4 * w;
+        // bytes [a, z) of the word are this run's
+        const int a = off - 4 * w > 0 ? off - 4 * w : 0, z = end - 4 * w < 4 ? end - 4 * w : 4;
+        const uint32_t fresh = a < 4 ? *reinterpret_cast<const uint32_t*>(lds + d * LROW + 4 * w) : 0u;
+        if (a == 0 && z == 4) {
+          *reinterpret_cast<uint32_t*>(g) = fresh;
+        } else if (moved && a > 0) {
+          const uint32_t had = *reinterpret_cast<const uint32_t*>(g);
+          const uint32_t kept = e4m3_word_shifted(had, old - c);
+          uint32_t res = 0;
 #pragma unroll
-        for (int b = 0; b < 4; b++) res |= (b < a ? kept : b < z ? fresh : had) & (0xFFu << (8 * b));
-        *reinterpret_cast<uint32_t*>(g) = res;
-      } else {
-        for (int b = a; b < z; b++) g[b] = (uint8_t)(fresh >> (8 * b));
+          for (int b = 0; b < 4; b++) res |= (b < a ? kept : b < z ? fresh : had) & (0xFFu << (8 * b));
+          *reinterpret_cast<uint32_t*>(g) = res;
+        } else {
+          for (int b = a; b < z; b++) g[b] = (uint8_t)(fresh >> (8 * b));
+        }
       }
     }
   }
@@ -262,42 +379,56 @@ __device__ __forceinline__ void append_run(const void* __restrict__ x, int64_t s
 }
 
 // Workgroup (x, head, keys or values) writes the runs that begin in tokens
-// [x * chunk, (x + 1) * chunk).
-template <bool BF16, int D, int R>
+// [x * chunk, (x + 1) * chunk), chunk <= 64.
+template <bool BF16, int D, int PAGE>
 __global__ __launch_bounds__(KV_THREADS) void k_kv_append(
     const void* __restrict__ k, int64_t k_stride, const void* __restrict__ v, int64_t v_stride,
-    const int64_t* __restrict__ slots, int64_t tokens, int chunk, int log_page, int64_t num_pages,
-    uint8_t* __restrict__ k_codes, uint8_t* __restrict__ k_scales, uint8_t* __restrict__ v_codes,
-    uint8_t* __restrict__ v_scales) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[D * (R * KV_THREADS * 8 / D + 4)];
-  __shared__ float red[KV_THREADS / 64];
-  __shared__ unsigned long long follow[2];
-  const int tid = threadIdx.x, head = blockIdx.y, heads = gridDim.y, page = 1 << log_page;
-  const int64_t limit = num_pages << log_page;
-  const int64_t t1 = ((int64_t)blockIdx.x + 1) * chunk < tokens ? ((int64_t)blockIdx.x + 1) * chunk : tokens;
-  for (int64_t t = (int64_t)blockIdx.x * chunk; t < t1; t++) {
-    const int64_t slot = slots[t];
-    const int off = (int)(slot & (page - 1));
-    if (slot < 0 || slot >= limit) continue;
-    if (t > 0 && off && slots[t - 1] == slot - 1) continue;
-    // the run's length: tokens that follow on in the page
-    if (tid < 128) {
-      const bool on = tid < page - off && t + tid < tokens && slots[t + tid] == slot + tid;
-      const unsigned long long b = __ballot(on);
-      if ((tid & 63) == 0) follow[tid >> 6] = b;
+    const int64_t* __restrict__ slots, int64_t tokens, int chunk, int64_t num_pages, uint8_t* __restrict__ k_codes,
+    uint8_t* __restrict__ k_scales, uint8_t* __restrict__ v_codes, uint8_t* __restrict__ v_scales) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[D * (PAGE + 4)];
+  __shared__ uint32_t red[KV_THREADS / 64];
+  const int lane = threadIdx.x & 63, head = blockIdx.y, heads = gridDim.y;
+  const int64_t limit = num_pages * PAGE;
+  const int64_t t0 = (int64_t)blockIdx.x * chunk;
+  // every wave looks at the chunk's slots and those that a run of them may reach
+  auto slot_of = [&](int64_t t) { return t < tokens ? slots[t] : (int64_t)-1; };
+  const int64_t s0 = slot_of(t0 + lane), s1 = slot_of(t0 + 64 + lane);
+  const int64_t before0 = t0 ? slots[t0 - 1] : -1;
+  int64_t before = __shfl_up(s0, 1, 64);
+  before = lane ? before : before0;
+  const bool valid = s0 >= 0 && s0 < limit;
+  const bool begins = valid && lane < chunk && !((s0 & (PAGE - 1)) && before == s0 - 1);
+  unsigned long long runs = __ballot(begins);
+  // follows: the token extends the run of the one before it
+  const int64_t last0 = __shfl(s0, 63, 64), up1 = __shfl_up(s1, 1, 64), before1 = lane ? up1 : last0;
+  const unsigned long long on0 = __ballot((s0 & (PAGE - 1)) && before == s0 - 1);
+  const unsigned long long on1 = __ballot((s1 & (PAGE - 1)) && before1 == s1 - 1);
+  unsigned long long on2 = 0;
+  if constexpr (PAGE == 128) {
+    const int64_t s2 = slot_of(t0 + 128 + lane);
+    const int64_t last1 = __shfl(s1, 63, 64), up2 = __shfl_up(s2, 1, 64), before2 = lane ? up2 : last1;
+    on2 = __ballot((s2 & (PAGE - 1)) && before2 == s2 - 1 && lane < 63);
+  }
+  while (runs) {
+    const int i = __builtin_ctzll(runs);
+    runs &= runs - 1;
+    const int64_t t = t0 + i, slot = __shfl(s0, i, 64);
+    // tokens that follow i without a gap: up to PAGE - 1 of them
+    const unsigned long long a = i < 63 ? ~(on0 >> (i + 1)) : ~0ull;
+    int n = 1 + (a ? __builtin_ctzll(a) : 64);
+    if (n >= 64 - i) {
+      n = 64 - i + (~on1 ? __builtin_ctzll(~on1) : 64);
+      if (PAGE == 128 && n == 128 - i) n += __builtin_ctzll(~on2);   // a page is at most 128 tokens: ~on2 != 0
     }
-    __syncthreads();
-    const unsigned long long b0 = ~follow[0], b1 = ~follow[1];
-    const int n = b0 ? __builtin_ctzll(b0) : 64 + (b1 ? __builtin_ctzll(b1) : 64);
-    const int64_t block = (slot >> log_page) * heads + head;
-    const int64_t size = (int64_t)page * D;
+    const int off = (int)(slot & (PAGE - 1));
+    const int64_t block = slot / PAGE * heads + head;
     const int64_t col = (int64_t)head * D * (BF16 ? 2 : 4);
     if (blockIdx.z == 0)
-      append_run<BF16, false, D, R>((const uint8_t*)k + col, k_stride, t, n, off, page, k_codes + block * size,
-                                    k_scales + block, lds, red);
+      append_run<BF16, false, D, PAGE>((const uint8_t*)k + col, k_stride, t, n, off, k_codes + block * PAGE * D,
+                                       k_scales + block, lds, red);
     else
-      append_run<BF16, true, D, R>((const uint8_t*)v + col, v_stride, t, n, off, page, v_codes + block * size,
-                                   v_scales + block, lds, red);
+      append_run<BF16, true, D, PAGE>((const uint8_t*)v + col, v_stride, t, n, off, v_codes + block * PAGE * D,
+                                      v_scales + block, lds, red);
   }
 }
 
@@ -935,41 +1066,66 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_prompt(const KvArgs A, con
   if (A.lse && h == 0) A.lse[orow] = l == 0.0f ? -INFINITY : (mx + __builtin_log2f(l)) * LN2;
 }
 
-// Joins the splits of 16 rows of one head: thread (row, channels).
+// Joins the splits of 16 rows of one head, a wave taking every fourth row: its
+// lanes hold 4 channels each, and the groups of lanes that this leaves share
+// the splits, 4 of them in flight per lane, since a long context alone in its
+// batch has a hundred splits of few rows.
 template <int D, int R>
 __device__ __forceinline__ void kv_join(const KvArgs& A, const KvPart& part, int64_t slot, int sub, int kvh) {
   if (slot >= part.used[0]) return;
   const KvRec rec = part.rec[slot];
-  constexpr int CH = D / 16;
-  const int row = sub * 16 + threadIdx.x / 16, ch = (threadIdx.x % 16) * CH;
-  if (rec.splits == 0 || row >= rec.rows) return;
+  if (rec.splits == 0) return;
+  constexpr int LANES = D / 4, GROUPS = 64 / LANES, DEEP = 4;
+  const int lane = threadIdx.x & 63, grp = lane / LANES, ch = (lane % LANES) * 4;
   const int64_t step = (int64_t)A.kv_heads * R;
-  const int64_t at = (slot * A.kv_heads + kvh) * R + row;
-  float M = -INFINITY;
-  for (int s = 0; s < rec.splits; s++) M = __builtin_fmaxf(M, part.stats[2 * (at + s * step)]);
-  float L = 0.0f, acc[CH];
+  for (int row = sub * 16 + threadIdx.x / 64; row < sub * 16 + 16 && row < rec.rows; row += KV_THREADS / 64) {
+    const int64_t at = (slot * A.kv_heads + kvh) * R + row;
+    float M = -INFINITY, L = 0.0f;
+    f32x4_t acc = {0, 0, 0, 0};
+    for (int s0 = grp; s0 < rec.splits; s0 += GROUPS * DEEP) {
+      float ms[DEEP], ls[DEEP], top = M;
+      f32x4_t v[DEEP];
 #pragma unroll
-  for (int i = 0; i < CH; i++) acc[i] = 0.0f;
-  for (int s = 0; s < rec.splits; s++) {
-    const int64_t a = at + s * step;
-    const float ms = part.stats[2 * a];
-    const float f = ms == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ms - M);
-    L += f * part.stats[2 * a + 1];
+      for (int u = 0; u < DEEP; u++) {
+        const int sp = s0 + GROUPS * u;
+        const int64_t a = at + (sp < rec.splits ? sp : s0) * step;
+        ms[u] = part.stats[2 * a];
+        ls[u] = part.stats[2 * a + 1];
+        v[u] = *reinterpret_cast<const f32x4_t*>(part.sums + a * D + ch);
+        if (sp >= rec.splits) ms[u] = -INFINITY;
+        top = __builtin_fmaxf(top, ms[u]);
+      }
+      const float keep = M == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(M - top);
+      M = top;
+      L *= keep;
+      acc *= keep;
 #pragma unroll
-    for (int i = 0; i < CH; i += 4) {
-      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(part.sums + a * D + ch + i);
+      for (int u = 0; u < DEEP; u++) {
+        const float f = ms[u] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ms[u] - M);
+        L = __builtin_fmaf(f, ls[u], L);
 #pragma unroll
-      for (int e = 0; e < 4; e++) acc[i + e] = __builtin_fmaf(f, v[e], acc[i + e]);
+        for (int e = 0; e < 4; e++) acc[e] = __builtin_fmaf(f, v[u][e], acc[e]);
+      }
+    }
+#pragma unroll
+    for (int o = LANES; o < 64; o <<= 1) {
+      const float mo = __shfl_xor(M, o, 64), lo = __shfl_xor(L, o, 64), top = __builtin_fmaxf(M, mo);
+      const float a = M == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(M - top);
+      const float b = mo == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mo - top);
+      L = a * L + b * lo;
+#pragma unroll
+      for (int e = 0; e < 4; e++) acc[e] = a * acc[e] + b * __shfl_xor(acc[e], o, 64);
+      M = top;
+    }
+    if (grp == 0) {
+      const int64_t rr = rec.row0 + row;
+      const int64_t orow = rr / A.group * A.q_heads + kvh * A.group + rr % A.group;
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+      *reinterpret_cast<u32x2_t*>(A.out + orow * D + ch) =
+          u32x2_t{pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv)};
+      if (A.lse && ch == 0) A.lse[orow] = L == 0.0f ? -INFINITY : (M + __builtin_log2f(L)) * LN2;
     }
   }
-  const int64_t rr = rec.row0 + row;
-  const int64_t orow = rr / A.group * A.q_heads + kvh * A.group + rr % A.group;
-  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-#pragma unroll
-  for (int i = 0; i < CH; i += 4)
-    *reinterpret_cast<u32x2_t*>(A.out + orow * D + ch + i) =
-        u32x2_t{pack_bf16x2(acc[i] * inv, acc[i + 1] * inv), pack_bf16x2(acc[i + 2] * inv, acc[i + 3] * inv)};
-  if (A.lse && ch == 0) A.lse[orow] = L == 0.0f ? -INFINITY : (M + __builtin_log2f(L)) * LN2;
 }
 
 // Workgroups of the decode slots first, then PROWS / 16 for each prompt slot.
@@ -990,10 +1146,8 @@ template <bool BF16, int D>
 void launch_append(int page, dim3 grid, hipStream_t s, const void* k, int64_t ks, const void* v, int64_t vs,
                    const int64_t* slots, int64_t tokens, int chunk, int64_t num_pages, uint8_t* kc, uint8_t* ksc,
                    uint8_t* vc, uint8_t* vsc) {
-  const int lp = log2_page(page);
-#define WQ_APPEND(PAGE)                                                                                             \
-  k_kv_append<BF16, D, (PAGE * D / 8 + KV_THREADS - 1) / KV_THREADS><<<grid, KV_THREADS, 0, s>>>(                    \
-      k, ks, v, vs, slots, tokens, chunk, lp, num_pages, kc, ksc, vc, vsc)
+#define WQ_APPEND(PAGE) \
+  k_kv_append<BF16, D, PAGE><<<grid, KV_THREADS, 0, s>>>(k, ks, v, vs, slots, tokens, chunk, num_pages, kc, ksc, vc, vsc)
   if (page == 16) WQ_APPEND(16);
   else if (page == 32) WQ_APPEND(32);
   else if (page == 64) WQ_APPEND(64);
