@@ -450,8 +450,11 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_append(
 // Rows of one key/value head are numbered r = query * group + head in group:
 // the `group` query heads that share a key/value head share its tiles.
 constexpr int TILE = 64;                      // tokens per step
-constexpr int DROWS = 16;                     // rows of a decode tile
 constexpr int PROWS = 128;                    // rows of a prompt tile
+// Requests of at most this many rows go through the decode kernel beside
+// prompts: its tiles of 32 read K and V once each, the prompt kernel once for
+// 128, but a prompt tile costs its 128 rows' arithmetic however few there are.
+constexpr int SHORT_ROWS = 64;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 struct KvArgs {
@@ -460,14 +463,13 @@ struct KvArgs {
   const int32_t* cu_q;
   const int32_t* kv_lens;
   int64_t batch, tokens;
-  int q_heads, kv_heads, group;
+  int q_heads, kv_heads, group, window;
   const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
   int log_page;
   int64_t num_pages;
   const int32_t* table;
   int64_t max_blocks;
   float sm_scale, softcap;
-  int64_t window;
   uint16_t* out;
   float* lse;
 };
@@ -477,11 +479,11 @@ struct KvArgs {
 // in the entry of the first split, with the number of splits that follow.
 struct KvRec {
   int32_t splits;                             // 0 in the entries of the other splits
-  int32_t rows;
-  int64_t row0;                               // query row of the tensors times group, plus head in group
+  int32_t rows, query0, head0;                // the first row: query row of the tensors, head in its group
 };
 struct KvPart {
   int64_t splits;                             // aim: items per head, over which the tiles are spread
+  int64_t slots;                              // room in the arrays below: nothing is written past it, whatever cu_q holds
   int min_tiles;                              // no split is shorter
   int64_t* used;
   KvRec* rec;
@@ -489,15 +491,15 @@ struct KvPart {
   float* stats;
 };
 
-// Which requests a launch takes: all of them, those whose rows fit one decode
-// tile, or the others.
+// Which requests a launch takes: all of them, those of at most SHORT_ROWS rows,
+// or the others.
 enum { REQ_ALL, REQ_SHORT, REQ_LONG };
 
-// One item of work: rows [r0, r0 + rows) of a request, tiles of its share.
+// One item of work: rows [r0, r0 + rows) of a request, a share of their tiles.
+// Uniform over the workgroup (read from one lane, so it lives in scalar registers).
 struct KvItem {
-  int64_t request, q0, n, len;                // first query row, queries, tokens in the cache
-  int64_t r0;
-  int rows, splits, split;
+  int request, q0, n, len;                    // first query row, queries, tokens in the cache
+  int r0, rows, splits, split;
   int64_t slot;                               // partial slot, where splits > 1
 };
 
@@ -506,6 +508,14 @@ __device__ __forceinline__ int64_t wave_sum(int64_t v) {
   for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
   return v;
 }
+__device__ __forceinline__ int lane32(int v, int src) { return __builtin_amdgcn_readlane(v, src); }
+__device__ __forceinline__ int64_t lane64(int64_t v, int src) {
+  return (int64_t)(((uint64_t)(uint32_t)lane32((int)(v >> 32), src) << 32) | (uint32_t)lane32((int)v, src));
+}
+
+// The request's limits in the cache: positions from `first` on, tokens [0, len).
+// Token j is visible to position p when p - window < j <= p.
+__device__ __forceinline__ int kv_lowest(int pos, int window) { return window > 0 && pos >= window ? pos - window + 1 : 0; }
 
 // Every wave finds its item itself, from the lengths: the tiles of all
 // requests are spread evenly over about part.splits items, a request of
@@ -515,84 +525,102 @@ __device__ __forceinline__ int64_t wave_sum(int64_t v) {
 template <int R, int WHICH>
 __device__ __forceinline__ bool kv_find(const KvArgs& A, const KvPart& part, int64_t item, bool count_all, KvItem& it) {
   const int lane = threadIdx.x & 63;
-  const int64_t cap = A.max_blocks << A.log_page;
-  auto request = [&](int64_t i, int64_t& q0, int64_t& n, int64_t& len, int64_t& tiles, int64_t& row_tiles) {
+  const int cap = (int)(A.max_blocks << A.log_page);
+  auto request = [&](int64_t i, int& q0, int& n, int& len, int& tiles, int& row_tiles) {
     q0 = n = len = 0;
     if (i < A.batch) {
-      int64_t a = A.cu_q[i], z = A.cu_q[i + 1];
+      int a = A.cu_q[i], z = A.cu_q[i + 1];
       len = A.kv_lens[i];
       a = a < 0 ? 0 : a;
-      z = z > A.tokens ? A.tokens : z;
+      z = z > A.tokens ? (int)A.tokens : z;
       q0 = a;
       n = z > a ? z - a : 0;
       len = len < 0 ? 0 : len > cap ? cap : len;
     }
-    const int64_t rows = n * A.group;
-    if (WHICH == REQ_SHORT ? rows > DROWS : WHICH == REQ_LONG ? rows <= DROWS : false) n = 0;
-    row_tiles = n > 0 ? (rows + R - 1) / R : 0;
-    const int64_t first = len - n - A.window + 1;      // lowest token any query sees
-    const int64_t lo = A.window > 0 && first > 0 ? first : 0;
-    tiles = len > 0 ? ((len - 1) / TILE) - lo / TILE + 1 : 0;
+    const int rows = n * A.group;             // below 2^31, as tokens * group is
+    if (WHICH == REQ_SHORT ? rows > SHORT_ROWS : WHICH == REQ_LONG ? rows <= SHORT_ROWS : false) n = 0;
+    row_tiles = n > 0 ? (int)(((int64_t)rows + R - 1) / R) : 0;
+    tiles = len > 0 ? (len - 1) / TILE - kv_lowest(len - n, A.window) / TILE + 1 : 0;
   };
-  int64_t q0, n, len, tiles, row_tiles, total = 0;
+  int q0, n, len, tiles, row_tiles;
+  int64_t total = 0;
   for (int64_t base = 0; base < A.batch; base += 64) {
     request(base + lane, q0, n, len, tiles, row_tiles);
-    total += tiles * row_tiles;
+    total += (int64_t)tiles * row_tiles;
   }
-  total = wave_sum(total);
+  total = lane64(wave_sum(total), 0);
   int64_t share = (total + part.splits - 1) / part.splits;
   share = share < part.min_tiles ? part.min_tiles : share;
+  const int per = share > 0x7FFFFFFF ? 0x7FFFFFFF : (int)share;
   int64_t items = 0, slots = 0;
   bool found = false;
   for (int64_t base = 0; base < A.batch; base += 64) {
     if (A.batch > 64) request(base + lane, q0, n, len, tiles, row_tiles);
-    const int64_t splits = tiles > share ? (tiles + share - 1) / share : 1;
-    const int64_t own = row_tiles * splits, part_own = splits > 1 ? own : 0;
+    const int splits = tiles > per ? (int)(((int64_t)tiles + per - 1) / per) : 1;
+    const int64_t own = (int64_t)row_tiles * splits, part_own = splits > 1 ? own : 0;
     const int64_t end = items + wave_scan(own, lane), part_end = slots + wave_scan(part_own, lane);
     const unsigned long long at = __ballot(end > item);
     if (at && !found) {
       const int src = __builtin_ctzll(at);
-      const int64_t s = __shfl(splits, src, 64), idx = item - __shfl(end - own, src, 64);
-      it.request = base + src;
-      it.q0 = __shfl(q0, src, 64);
-      it.n = __shfl(n, src, 64);
-      it.len = __shfl(len, src, 64);
-      it.splits = (int)s;
-      it.split = (int)(idx % s);
-      it.r0 = (__shfl(row_tiles, src, 64) - 1 - idx / s) * R;      // the longest rows first
-      const int64_t left = it.n * A.group - it.r0;
-      it.rows = left < R ? (int)left : R;
-      it.slot = __shfl(part_end - part_own, src, 64) + idx;
+      const int idx = (int)(item - lane64(end - own, src));
+      it.splits = lane32(splits, src);
+      it.split = idx % it.splits;
+      it.request = (int)base + src;
+      it.q0 = lane32(q0, src);
+      it.n = lane32(n, src);
+      it.len = lane32(len, src);
+      it.r0 = (lane32(row_tiles, src) - 1 - idx / it.splits) * R;  // the longest rows first
+      const int left = it.n * A.group - it.r0;
+      it.rows = left < R ? left : R;
+      it.slot = lane64(part_end - part_own, src) + idx;
       found = true;
     }
     if (found && !count_all) return true;
-    items = __shfl(end, 63, 64);
-    slots = __shfl(part_end, 63, 64);
+    items = lane64(end, 63);
+    slots = lane64(part_end, 63);
   }
-  if (count_all && threadIdx.x == 0) part.used[0] = slots;
+  if (count_all && threadIdx.x == 0) part.used[0] = slots < part.slots ? slots : part.slots;
   return found;
 }
 
-// Tiles [t0, t1) of the item: the tokens its rows see, cut into it.splits shares.
-__device__ __forceinline__ void kv_tiles(const KvArgs& A, const KvItem& it, int64_t& lo, int64_t& hi, int64_t& t0,
-                                         int64_t& t1) {
-  const int64_t p0 = it.len - it.n + it.r0 / A.group, p1 = it.len - it.n + (it.r0 + it.rows - 1) / A.group;
-  hi = p1 + 1 < 0 ? 0 : p1 + 1;               // one behind the last token seen
-  lo = A.window > 0 && p0 - A.window + 1 > 0 ? p0 - A.window + 1 : 0;
+// Queries of the item's rows: row r0 is query `first` of the request and head
+// `head0` of the group; row r0 + i is i rows on.
+struct KvRows {
+  int first, head0, pos0;                     // pos0: position of query `first`
+  __device__ __forceinline__ KvRows(const KvArgs& A, const KvItem& it)
+      : first((int)((uint32_t)it.r0 / (uint32_t)A.group)), head0((int)((uint32_t)it.r0 % (uint32_t)A.group)),
+        pos0(it.len - it.n + first) {}
+  __device__ __forceinline__ int query(const KvArgs& A, int i) const { return (int)((uint32_t)(head0 + i) / (uint32_t)A.group); }
+  __device__ __forceinline__ int head(const KvArgs& A, int i) const { return (int)((uint32_t)(head0 + i) % (uint32_t)A.group); }
+};
+
+// Tokens [lo, hi) that the item's rows see between them, and its tiles [t0, t1).
+__device__ __forceinline__ void kv_tiles(const KvArgs& A, const KvItem& it, const KvRows& rows, int& lo, int& hi,
+                                         int& t0, int& t1) {
+  const int last = rows.pos0 + rows.query(A, it.rows - 1);
+  hi = last < 0 ? 0 : last + 1;
+  lo = kv_lowest(rows.pos0, A.window);
   lo = lo < hi ? lo : hi;
-  const int64_t a = lo / TILE, n = hi > lo ? (hi + TILE - 1) / TILE - a : 0;
-  t0 = a + n * it.split / it.splits;
-  t1 = a + n * (it.split + 1) / it.splits;
+  const int a = lo / TILE, n = hi > lo ? (hi - 1) / TILE + 1 - a : 0;
+  t0 = a + (int)((int64_t)n * it.split / it.splits);
+  t1 = a + (int)((int64_t)n * (it.split + 1) / it.splits);
 }
 
-// cap * tanh(s / cap): 1 - 2 / (e^2x + 1), and below .2, where that cancels,
-// the series up to x^7 (the next term is under 6e-8 of the result there).
-__device__ __forceinline__ float kv_softcap(float s, float cap, float inv_cap) {
-  const float x = __builtin_fabsf(s * inv_cap), y = x * x;
-  const float big = 1.0f - 2.0f * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x * (2.0f * LOG2E)) + 1.0f);
-  const float small = x + x * y * (-1.0f / 3.0f + y * (2.0f / 15.0f + y * (-17.0f / 315.0f)));
-  return __builtin_copysignf(cap * (x < 0.2f ? small : big), s);
-}
+// The scores enter as fma(s, mul, add), to base 2.  Capped scores:
+// cap * tanh(x) = cap - 2 cap / (e^2x + 1), so that s is 1 / (e^2x + 1) there,
+// larger scores being smaller values; off by at most cap * 2^-22.
+template <bool CAP>
+struct KvScore {
+  float mul, add, to2x;
+  __device__ __forceinline__ explicit KvScore(const KvArgs& A)
+      : mul(CAP ? -2.0f * A.softcap * LOG2E : A.sm_scale * LOG2E), add(CAP ? A.softcap * LOG2E : 0.0f),
+        to2x(CAP ? 2.0f * LOG2E * A.sm_scale / A.softcap : 0.0f) {}
+  __device__ __forceinline__ float cap(float dot) const {
+    return CAP ? __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(dot * to2x) + 1.0f) : dot;
+  }
+  static constexpr float NONE = CAP ? INFINITY : -INFINITY;
+  __device__ __forceinline__ static float top(float a, float b) { return CAP ? __builtin_fminf(a, b) : __builtin_fmaxf(a, b); }
+};
 
 // Eight E4M3 bytes with E8M0 scale operand -> eight bf16.
 __device__ __forceinline__ bf16x8_t e4m3_bf16x8(uint32_t a, uint32_t b, float scale) {
@@ -604,9 +632,9 @@ __device__ __forceinline__ bf16x8_t e4m3_bf16x8(uint32_t a, uint32_t b, float sc
 }
 
 // Keeps the bytes of tokens [lo, hi) of a 16-byte piece that begins at token j.
-__device__ __forceinline__ u32x4_t keep_tokens(u32x4_t v, int64_t j, int64_t lo, int64_t hi) {
-  const int a = lo > j ? (lo - j < 16 ? (int)(lo - j) : 16) : 0;
-  const int z = hi > j ? (hi - j < 16 ? (int)(hi - j) : 16) : 0;
+__device__ __forceinline__ u32x4_t keep_tokens(u32x4_t v, int j, int lo, int hi) {
+  const int a = lo > j ? (lo - j < 16 ? lo - j : 16) : 0;
+  const int z = hi > j ? (hi - j < 16 ? hi - j : 16) : 0;
 #pragma unroll
   for (int w = 0; w < 4; w++) {
     const int aw = a - 4 * w < 0 ? 0 : a - 4 * w > 4 ? 4 : a - 4 * w;
@@ -616,9 +644,9 @@ __device__ __forceinline__ u32x4_t keep_tokens(u32x4_t v, int64_t j, int64_t lo,
   return v;
 }
 
-// Decode: 16 rows (the query heads of a group, for one token or a few drafted
-// ones) per workgroup; its 4 waves take the item's tiles in turn, each with
-// its own running maximum and sums, which are joined in LDS at the end.
+// Decode: 16 or 32 rows (the query heads of a group, for one token or a few
+// drafted ones) per workgroup; its 4 waves take the item's tiles in turn, each
+// with its own running maximum and sums, which are joined in LDS at the end.
 // Bound by the bytes of K and V: they go from HBM straight into the registers
 // that feed v_mfma_f32_16x16x32_bf16, the next tile's K loads leaving as soon
 // as this tile's scores are done and its V loads after its sums, so that a
@@ -626,213 +654,237 @@ __device__ __forceinline__ u32x4_t keep_tokens(u32x4_t v, int64_t j, int64_t lo,
 //
 // Lane l = 16 g + m.  K tile a (of 4): operand row m is token
 // 16 (m / 4) + 4 a + m % 4, result rows 4 g + i are then tokens 16 g + 4 a + i.
-template <int D, bool CAP, int WHICH>
+template <int D, bool CAP, int WHICH, int NR>
 __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, const KvPart part) {
-  constexpr int KP = D / 64, DT = D / 16;
-  __shared__ __attribute__((aligned(16))) float so[4][DROWS][D + 4];
-  __shared__ float sm[4][DROWS], sl[4][DROWS];
-  const int64_t item = blockIdx.x / A.kv_heads;
-  const int kvh = (int)(blockIdx.x % A.kv_heads);
+  constexpr int KP = D / 64, DT = D / 16, R = 16 * NR;
+  __shared__ __attribute__((aligned(16))) float so[4][R][D + 4];
+  __shared__ float sm[4][R], sl[4][R];
+  const int64_t item = blockIdx.x / (unsigned)A.kv_heads;
+  const int kvh = (int)(blockIdx.x % (unsigned)A.kv_heads);
   KvItem it;
-  if (!kv_find<DROWS, WHICH>(A, part, item, blockIdx.x == 0, it)) return;
+  if (!kv_find<R, WHICH>(A, part, item, blockIdx.x == 0, it)) return;
+  if (it.splits > 1 && it.slot >= part.slots) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, g = lane >> 4;
-  int64_t lo, hi, t0, t1;
-  kv_tiles(A, it, lo, hi, t0, t1);
+  const KvRows rows(A, it);
+  int lo, hi, t0, t1;
+  kv_tiles(A, it, rows, lo, hi, t0, t1);
 
-  // query fragments: columns m of q^T; row m's limits
-  bf16x8_t qf[KP][2];
-  const bool live = m < it.rows;
-  const int64_t r = it.r0 + (live ? m : 0), qrow = it.q0 + r / A.group;
-  const int64_t pos = it.len - it.n + r / A.group;
-  const int64_t rlo = A.window > 0 && pos - A.window + 1 > 0 ? pos - A.window + 1 : 0;
-  {
-    const uint16_t* qp = A.q + qrow * A.q_stride + (kvh * A.group + r % A.group) * D;
-#pragma unroll
-    for (int p = 0; p < KP; p++)
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
-        u32x4_t w = ld16(qp + 64 * p + 16 * g + 8 * h);
-        if (!live) w = u32x4_t{0, 0, 0, 0};
-        qf[p][h] = __builtin_bit_cast(bf16x8_t, w);
-      }
-  }
-  const int64_t row_min = it.len - it.n + it.r0 / A.group;         // position of the tile's first row
-  const int64_t row_max = it.len - it.n + (it.r0 + it.rows - 1) / A.group;
-  const int64_t lo_max = A.window > 0 && row_max - A.window + 1 > 0 ? row_max - A.window + 1 : 0;
-  const int32_t* tab = A.table + it.request * A.max_blocks;
-  const int64_t page_bytes = (int64_t)D << A.log_page;
+  const int32_t* tab = A.table + (int64_t)it.request * A.max_blocks;
+  const int last_col = (int)A.max_blocks - 1;
+  const uint32_t head_bytes = (uint32_t)D << A.log_page, page_bytes = head_bytes * A.kv_heads;
   const int in_page = (1 << A.log_page) - 1;
-  const int64_t last_col = A.max_blocks - 1;
+  const uint8_t* kbase = A.k_codes + (int64_t)kvh * head_bytes;
+  const uint8_t* vbase = A.v_codes + (int64_t)kvh * head_bytes;
+  const uint8_t *ksb = A.k_scales + kvh, *vsb = A.v_scales + kvh;
 
   u32x4_t kr[4][KP], vr[DT];
   uint32_t ksc, vsc;
-  bool kok, vok;
+  bool vok;
   int idk, idv;                               // page ids of the next tile to load
-  auto load_ids = [&](int64_t t) {
-    const int64_t j = t * TILE;
-    const int64_t ck = (j + 16 * (m >> 2)) >> A.log_page, cv = (j + 16 * g) >> A.log_page;
+  auto load_ids = [&](int t) {
+    const int ck = (t * TILE + 16 * (m >> 2)) >> A.log_page, cv = (t * TILE + 16 * g) >> A.log_page;
     idk = tab[ck < last_col ? ck : last_col];
     idv = tab[cv < last_col ? cv : last_col];
   };
-  auto load_k = [&](int64_t t) {
-    kok = idk >= 0 && idk < A.num_pages;
-    const int64_t block = (int64_t)(kok ? idk : 0) * A.kv_heads + kvh;
-    ksc = A.k_scales[block];
-    const uint8_t* p = A.k_codes + block * page_bytes +
-                       (((t * TILE + 16 * (m >> 2)) & in_page) + (m & 3)) * D + 16 * g;
+  auto load_k = [&](int t) {
+    const uint32_t id = idk >= 0 && idk < A.num_pages ? idk : 0;
+    ksc = ksb[(uint64_t)id * (uint32_t)A.kv_heads];
+    const uint8_t* p = kbase + ((uint64_t)id * page_bytes + (((t * TILE + 16 * (m >> 2)) & in_page) + (m & 3)) * D + 16 * g);
 #pragma unroll
     for (int a = 0; a < 4; a++)
 #pragma unroll
       for (int h = 0; h < KP; h++) kr[a][h] = ld16(p + 4 * a * D + 64 * h);
   };
-  auto load_v = [&](int64_t t) {
+  auto load_v = [&](int t) {
     vok = idv >= 0 && idv < A.num_pages;
-    const int64_t block = (int64_t)(vok ? idv : 0) * A.kv_heads + kvh;
-    vsc = A.v_scales[block];
-    const uint8_t* p = A.v_codes + block * page_bytes + ((int64_t)m << A.log_page) + ((t * TILE + 16 * g) & in_page);
+    const uint32_t id = vok ? idv : 0;
+    vsc = vsb[(uint64_t)id * (uint32_t)A.kv_heads];
+    const uint8_t* p = vbase + ((uint64_t)id * page_bytes + (m << A.log_page) + ((t * TILE + 16 * g) & in_page));
 #pragma unroll
-    for (int d = 0; d < DT; d++) vr[d] = ld16(p + ((int64_t)(16 * d) << A.log_page));
+    for (int d = 0; d < DT; d++) vr[d] = ld16(p + ((16 * d) << A.log_page));
   };
-
-  f32x4_t o[DT];
-#pragma unroll
-  for (int d = 0; d < DT; d++) o[d] = f32x4_t{0, 0, 0, 0};
-  float mx = -INFINITY, l = 0.0f;
-  const float c = CAP ? LOG2E : A.sm_scale * LOG2E;
-  const float inv_cap = CAP ? A.sm_scale / A.softcap : 0.0f;
-  int64_t t = t0 + wave;
+  int t = t0 + wave;
   if (t < t1) {
     load_ids(t);
     load_k(t);
     load_v(t);
     if (t + 4 < t1) load_ids(t + 4);
   }
+
+  // query fragments: columns m of q^T; row m's limits
+  bf16x8_t qf[NR][KP][2];
+  int pos[NR], rlo[NR];
+#pragma unroll
+  for (int c = 0; c < NR; c++) {
+    const bool live = 16 * c + m < it.rows;
+    const int i = live ? 16 * c + m : 0, query = rows.query(A, i);
+    pos[c] = rows.pos0 + query;
+    rlo[c] = kv_lowest(pos[c], A.window);
+    const uint16_t* qp = A.q + (int64_t)(it.q0 + rows.first + query) * A.q_stride + (kvh * A.group + rows.head(A, i)) * D;
+#pragma unroll
+    for (int p = 0; p < KP; p++)
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        u32x4_t w = ld16(qp + 64 * p + 16 * g + 8 * h);
+        if (!live) w = u32x4_t{0, 0, 0, 0};
+        qf[c][p][h] = __builtin_bit_cast(bf16x8_t, w);
+      }
+  }
+  const int lo_max = kv_lowest(rows.pos0 + rows.query(A, it.rows - 1), A.window);
+
+  f32x4_t o[NR][DT];
+  float mx[NR], l[NR];
+#pragma unroll
+  for (int c = 0; c < NR; c++) {
+#pragma unroll
+    for (int d = 0; d < DT; d++) o[c][d] = f32x4_t{0, 0, 0, 0};
+    mx[c] = -INFINITY;
+    l[c] = 0.0f;
+  }
+  const KvScore<CAP> sc(A);
   for (; t < t1; t += 4) {
-    const int64_t j0 = t * TILE + 16 * g;     // this lane's 16 tokens in scores and V^T
+    const int j0 = t * TILE + 16 * g;         // this lane's 16 tokens in scores and V^T
     const bool more = t + 4 < t1;
-    f32x4_t s[4];
+    f32x4_t s[NR][4];
     const float ks = e8m0_as_scale(ksc);
 #pragma unroll
     for (int a = 0; a < 4; a++) {
-      s[a] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int c = 0; c < NR; c++) s[c][a] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
       for (int p = 0; p < KP; p++) {
         const u32x4_t w = kr[a][p];
-        s[a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e4m3_bf16x8(w[0], w[1], ks), qf[p][0], s[a], 0, 0, 0);
-        s[a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e4m3_bf16x8(w[2], w[3], ks), qf[p][1], s[a], 0, 0, 0);
+        const bf16x8_t k0 = e4m3_bf16x8(w[0], w[1], ks), k1 = e4m3_bf16x8(w[2], w[3], ks);
+#pragma unroll
+        for (int c = 0; c < NR; c++) {
+          s[c][a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, qf[c][p][0], s[c][a], 0, 0, 0);
+          s[c][a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, qf[c][p][1], s[c][a], 0, 0, 0);
+        }
       }
     }
     if (more) load_k(t + 4);
-    if constexpr (CAP) {
-#pragma unroll
-      for (int a = 0; a < 4; a++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) s[a][i] = kv_softcap(s[a][i], A.softcap, inv_cap);
-    }
-    // tokens outside a row's limits, and bytes of V that no row may see
     float vs = e8m0_as_scale(vsc);
-    if (t * TILE + TILE - 1 > row_min || t * TILE < lo_max || __any(!vok)) {
-#pragma unroll
-      for (int a = 0; a < 4; a++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const int64_t j = j0 + 4 * a + i;
-          s[a][i] = j <= pos && j >= rlo && vok ? s[a][i] : -INFINITY;
-        }
-      const int64_t a = vok ? lo : 0, z = vok ? hi : 0;
+    const bool edge = t * TILE + TILE - 1 > rows.pos0 || t * TILE < lo_max || __any(!vok);
+    if (edge) {                               // bytes of V that no row may see
+      const int a = vok ? lo : 0, z = vok ? hi : 0;
       if (j0 + 16 <= a || j0 >= z) vs = 1.0f;
 #pragma unroll
       for (int d = 0; d < DT; d++) vr[d] = keep_tokens(vr[d], j0, a, z);
     }
-    float mt = -INFINITY;
+    bf16x8_t p0[NR], p1[NR];
 #pragma unroll
-    for (int a = 0; a < 4; a++)
+    for (int c = 0; c < NR; c++) {
+      if constexpr (CAP) {
 #pragma unroll
-      for (int i = 0; i < 4; i++) mt = __builtin_fmaxf(mt, s[a][i]);
-    mt = __builtin_fmaxf(mt, __shfl_xor(mt, 16, 64));
-    mt = __builtin_fmaxf(mt, __shfl_xor(mt, 32, 64)) * c;
-    if (__any(mt > mx)) {
-      const float mn = __builtin_fmaxf(mx, mt);
-      const float f = mx == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx - mn);
-      mx = mn;
-      l *= f;
+        for (int a = 0; a < 4; a++)
 #pragma unroll
-      for (int d = 0; d < DT; d++) o[d] *= f;
-    }
-    const float off = mx == -INFINITY ? 0.0f : mx;
-    uint32_t pw[8];
-#pragma unroll
-    for (int a = 0; a < 4; a++) {
-      float p[4];
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[a][i], c, -off));
-        l += p[i];
+          for (int i = 0; i < 4; i++) s[c][a][i] = sc.cap(s[c][a][i]);
       }
-      // bf16 for the matrix cores: half a step of 2^-8 per probability, the sum l keeps fp32
-      pw[2 * a] = pack_bf16x2(p[0], p[1]);
-      pw[2 * a + 1] = pack_bf16x2(p[2], p[3]);
+      if (edge) {                             // tokens outside the row's limits
+        const int z = vok ? pos[c] - j0 : -1, b = rlo[c] - j0;
+#pragma unroll
+        for (int a = 0; a < 4; a++)
+#pragma unroll
+          for (int i = 0; i < 4; i++) s[c][a][i] = 4 * a + i <= z && 4 * a + i >= b ? s[c][a][i] : sc.NONE;
+      }
+      float mt = sc.NONE;
+#pragma unroll
+      for (int a = 0; a < 4; a++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) mt = sc.top(mt, s[c][a][i]);
+      mt = sc.top(mt, __shfl_xor(mt, 16, 64));
+      mt = __builtin_fmaf(sc.top(mt, __shfl_xor(mt, 32, 64)), sc.mul, sc.add);
+      if (__any(mt > mx[c])) {
+        const float mn = __builtin_fmaxf(mx[c], mt);
+        const float f = mx[c] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx[c] - mn);
+        mx[c] = mn;
+        l[c] *= f;
+#pragma unroll
+        for (int d = 0; d < DT; d++) o[c][d] *= f;
+      }
+      const float off = sc.add - (mx[c] == -INFINITY ? 0.0f : mx[c]);
+      uint32_t pw[8];
+#pragma unroll
+      for (int a = 0; a < 4; a++) {
+        float p[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[c][a][i], sc.mul, off));
+          l[c] += p[i];
+        }
+        // bf16 for the matrix cores: half a step of 2^-8 per probability, the sum l keeps fp32
+        pw[2 * a] = pack_bf16x2(p[0], p[1]);
+        pw[2 * a + 1] = pack_bf16x2(p[2], p[3]);
+      }
+      p0[c] = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[0], pw[1], pw[2], pw[3]}));
+      p1[c] = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[4], pw[5], pw[6], pw[7]}));
     }
-    const bf16x8_t p0 = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[0], pw[1], pw[2], pw[3]}));
-    const bf16x8_t p1 = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[4], pw[5], pw[6], pw[7]}));
 #pragma unroll
     for (int d = 0; d < DT; d++) {
-      o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e4m3_bf16x8(vr[d][0], vr[d][1], vs), p0, o[d], 0, 0, 0);
-      o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e4m3_bf16x8(vr[d][2], vr[d][3], vs), p1, o[d], 0, 0, 0);
+      const bf16x8_t v0 = e4m3_bf16x8(vr[d][0], vr[d][1], vs), v1 = e4m3_bf16x8(vr[d][2], vr[d][3], vs);
+#pragma unroll
+      for (int c = 0; c < NR; c++) {
+        o[c][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, p0[c], o[c][d], 0, 0, 0);
+        o[c][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, p1[c], o[c][d], 0, 0, 0);
+      }
     }
     if (more) {
       load_v(t + 4);
       if (t + 8 < t1) load_ids(t + 8);
     }
   }
-  l += __shfl_xor(l, 16, 64);
-  l += __shfl_xor(l, 32, 64);
-  if (g == 0) {
-    sm[wave][m] = mx;
-    sl[wave][m] = l;
-  }
 #pragma unroll
-  for (int d = 0; d < DT; d++) *reinterpret_cast<f32x4_t*>(&so[wave][m][16 * d + 4 * g]) = o[d];
+  for (int c = 0; c < NR; c++) {
+    l[c] += __shfl_xor(l[c], 16, 64);
+    l[c] += __shfl_xor(l[c], 32, 64);
+    if (g == 0) {
+      sm[wave][16 * c + m] = mx[c];
+      sl[wave][16 * c + m] = l[c];
+    }
+#pragma unroll
+    for (int d = 0; d < DT; d++) *reinterpret_cast<f32x4_t*>(&so[wave][16 * c + m][16 * d + 4 * g]) = o[c][d];
+  }
   __syncthreads();
 
   // join the waves: thread (row, channels)
   constexpr int CH = D / 16;
-  const int row = tid / 16, ch = (tid % 16) * CH;
-  if (row >= it.rows) return;
-  float M = sm[0][row];
+  const int ch = (tid % 16) * CH;
+  if (it.splits > 1 && tid == 0 && kvh == 0)
+    part.rec[it.slot] = KvRec{it.split ? 0 : it.splits, it.rows, it.q0 + rows.first, rows.head0};
+  for (int row = tid / 16; row < it.rows; row += 16) {
+    float M = sm[0][row];
 #pragma unroll
-  for (int w = 1; w < 4; w++) M = __builtin_fmaxf(M, sm[w][row]);
-  float L = 0.0f, acc[CH];
+    for (int w = 1; w < 4; w++) M = __builtin_fmaxf(M, sm[w][row]);
+    float L = 0.0f, acc[CH];
 #pragma unroll
-  for (int i = 0; i < CH; i++) acc[i] = 0.0f;
+    for (int i = 0; i < CH; i++) acc[i] = 0.0f;
 #pragma unroll
-  for (int w = 0; w < 4; w++) {
-    const float f = sm[w][row] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(sm[w][row] - M);
-    L += f * sl[w][row];
+    for (int w = 0; w < 4; w++) {
+      const float f = sm[w][row] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(sm[w][row] - M);
+      L += f * sl[w][row];
 #pragma unroll
-    for (int i = 0; i < CH; i++) acc[i] = __builtin_fmaf(f, so[w][row][ch + i], acc[i]);
-  }
-  const int64_t rr = it.r0 + row;
-  if (it.splits > 1) {
-    const int64_t at = (it.slot * A.kv_heads + kvh) * DROWS + row;
-#pragma unroll
-    for (int i = 0; i < CH; i += 4)
-      *reinterpret_cast<f32x4_t*>(part.sums + at * D + ch + i) = f32x4_t{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
-    if (ch == 0) {
-      part.stats[2 * at] = M;
-      part.stats[2 * at + 1] = L;
+      for (int i = 0; i < CH; i++) acc[i] = __builtin_fmaf(f, so[w][row][ch + i], acc[i]);
     }
-    if (tid == 0 && kvh == 0) part.rec[it.slot] = KvRec{it.split ? 0 : it.splits, it.rows, it.q0 * A.group + it.r0};
-    return;
-  }
-  const int64_t orow = (it.q0 + rr / A.group) * A.q_heads + kvh * A.group + rr % A.group;
-  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-  uint32_t w[CH / 2];
+    if (it.splits > 1) {
+      const int64_t at = (it.slot * A.kv_heads + kvh) * R + row;
 #pragma unroll
-  for (int i = 0; i < CH / 2; i++) w[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-  if constexpr (CH == 8) *reinterpret_cast<u32x4_t*>(A.out + orow * D + ch) = u32x4_t{w[0], w[1], w[2], w[3]};
-  else *reinterpret_cast<u32x2_t*>(A.out + orow * D + ch) = u32x2_t{w[0], w[1]};
-  if (A.lse && ch == 0) A.lse[orow] = L == 0.0f ? -INFINITY : (M + __builtin_log2f(L)) * LN2;
+      for (int i = 0; i < CH; i += 4)
+        *reinterpret_cast<f32x4_t*>(part.sums + at * D + ch + i) = f32x4_t{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
+      if (ch == 0) {
+        part.stats[2 * at] = M;
+        part.stats[2 * at + 1] = L;
+      }
+      continue;
+    }
+    const int64_t orow = (int64_t)(it.q0 + rows.first + rows.query(A, row)) * A.q_heads + kvh * A.group + rows.head(A, row);
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    uint32_t w[CH / 2];
+#pragma unroll
+    for (int i = 0; i < CH / 2; i++) w[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    if constexpr (CH == 8) *reinterpret_cast<u32x4_t*>(A.out + orow * D + ch) = u32x4_t{w[0], w[1], w[2], w[3]};
+    else *reinterpret_cast<u32x2_t*>(A.out + orow * D + ch) = u32x2_t{w[0], w[1]};
+    if (A.lse && ch == 0) A.lse[orow] = L == 0.0f ? -INFINITY : (M + __builtin_log2f(L)) * LN2;
+  }
 }
 
 // Prompts and chunks: 128 rows per workgroup, 32 per wave.  Bound by the
@@ -851,22 +903,23 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_prompt(const KvArgs A, con
   constexpr int XK = D == 128 ? 1 : 2;
   __shared__ __attribute__((aligned(16))) uint8_t sk[2][TILE * D * 2], sv[2][TILE * D * 2];
   __shared__ int sok[2][4];
-  const int64_t item = blockIdx.x / A.kv_heads;
-  const int kvh = (int)(blockIdx.x % A.kv_heads);
+  const int64_t item = blockIdx.x / (unsigned)A.kv_heads;
+  const int kvh = (int)(blockIdx.x % (unsigned)A.kv_heads);
   KvItem it;
   if (!kv_find<PROWS, REQ_LONG>(A, part, item, blockIdx.x == 0, it)) return;
+  if (it.splits > 1 && it.slot >= part.slots) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 31, h = lane >> 5;
-  int64_t lo, hi, t0, t1;
-  kv_tiles(A, it, lo, hi, t0, t1);
+  const KvRows rows(A, it);
+  int lo, hi, t0, t1;
+  kv_tiles(A, it, rows, lo, hi, t0, t1);
 
   const int wrow = wave * 32;                 // first row of the wave in the tile
   const bool live = wrow + m < it.rows;
-  const int64_t r = it.r0 + (live ? wrow + m : 0), qrow = it.q0 + r / A.group;
-  const int64_t pos = it.len - it.n + r / A.group;
-  const int64_t rlo = A.window > 0 && pos - A.window + 1 > 0 ? pos - A.window + 1 : 0;
+  const int ri = live ? wrow + m : 0, query = rows.query(A, ri), rhead = kvh * A.group + rows.head(A, ri);
+  const int pos = rows.pos0 + query, rlo = kv_lowest(pos, A.window);
   bf16x8_t qf[KS];
   {
-    const uint16_t* qp = A.q + qrow * A.q_stride + (kvh * A.group + r % A.group) * D;
+    const uint16_t* qp = A.q + (int64_t)(it.q0 + rows.first + query) * A.q_stride + rhead * D;
 #pragma unroll
     for (int k = 0; k < KS; k++) {
       u32x4_t w = ld16(qp + 16 * k + 8 * h);
@@ -874,15 +927,17 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_prompt(const KvArgs A, con
       qf[k] = __builtin_bit_cast(bf16x8_t, w);
     }
   }
-  const int64_t w_last = wrow + 31 < it.rows ? wrow + 31 : it.rows - 1;      // below wrow: an idle wave
-  const int64_t w_min = it.len - it.n + (it.r0 + wrow) / A.group;
-  const int64_t w_max = it.len - it.n + (it.r0 + w_last) / A.group;
-  const int64_t w_lo_min = A.window > 0 && w_min - A.window + 1 > 0 ? w_min - A.window + 1 : 0;
-  const int64_t w_lo_max = A.window > 0 && w_max - A.window + 1 > 0 ? w_max - A.window + 1 : 0;
-  const int32_t* tab = A.table + it.request * A.max_blocks;
-  const int64_t page_bytes = (int64_t)D << A.log_page;
+  // limits of the wave's rows; a wave without rows computes nothing
+  const int w_rows = it.rows - wrow < 32 ? it.rows - wrow : 32;
+  const int w_min = rows.pos0 + rows.query(A, wrow), w_max = rows.pos0 + rows.query(A, wrow + (w_rows > 0 ? w_rows - 1 : 0));
+  const int w_lo_min = kv_lowest(w_min, A.window), w_lo_max = kv_lowest(w_max, A.window);
+  const int32_t* tab = A.table + (int64_t)it.request * A.max_blocks;
+  const int last_col = (int)A.max_blocks - 1;
+  const uint32_t head_bytes = (uint32_t)D << A.log_page, page_bytes = head_bytes * A.kv_heads;
   const int in_page = (1 << A.log_page) - 1;
-  const int64_t last_col = A.max_blocks - 1;
+  const uint8_t* kbase = A.k_codes + (int64_t)kvh * head_bytes;
+  const uint8_t* vbase = A.v_codes + (int64_t)kvh * head_bytes;
+  const uint8_t *ksb = A.k_scales + kvh, *vsb = A.v_scales + kvh;
 
   // staging: piece x = tid + 256 i is K token x / KS, channels 16 (x % KS)..,
   // and V^T channel x / 4, tokens 16 (x % 4)..
@@ -890,33 +945,34 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_prompt(const KvArgs A, con
   uint32_t ksc[ST], vsc;
   bool vok;
   int idk[ST], idv;
-  auto load_ids = [&](int64_t t) {
+  auto load_ids = [&](int t) {                // past t1 a tile of the item again: loaded, never used
+    t = t < t1 ? t : t1 - 1;
 #pragma unroll
     for (int i = 0; i < ST; i++) {
-      const int64_t c = (t * TILE + (tid + KV_THREADS * i) / KS) >> A.log_page;
+      const int c = (t * TILE + (tid + KV_THREADS * i) / KS) >> A.log_page;
       idk[i] = tab[c < last_col ? c : last_col];
     }
-    const int64_t c = (t * TILE + 16 * (tid & 3)) >> A.log_page;
+    const int c = (t * TILE + 16 * (tid & 3)) >> A.log_page;
     idv = tab[c < last_col ? c : last_col];
   };
-  auto load = [&](int64_t t) {
+  auto load = [&](int t) {
 #pragma unroll
     for (int i = 0; i < ST; i++) {
       const int x = tid + KV_THREADS * i, tok = x / KS;
-      const int64_t block = (int64_t)(idk[i] >= 0 && idk[i] < A.num_pages ? idk[i] : 0) * A.kv_heads + kvh;
-      ksc[i] = A.k_scales[block];
-      kr[i] = ld16(A.k_codes + block * page_bytes + ((t * TILE + tok) & in_page) * D + 16 * (x % KS));
+      const uint32_t id = idk[i] >= 0 && idk[i] < A.num_pages ? idk[i] : 0;
+      ksc[i] = ksb[(uint64_t)id * (uint32_t)A.kv_heads];
+      kr[i] = ld16(kbase + ((uint64_t)id * page_bytes + ((t * TILE + tok) & in_page) * D + 16 * (x % KS)));
     }
     vok = idv >= 0 && idv < A.num_pages;
-    const int64_t block = (int64_t)(vok ? idv : 0) * A.kv_heads + kvh;
-    vsc = A.v_scales[block];
+    const uint32_t id = vok ? idv : 0;
+    vsc = vsb[(uint64_t)id * (uint32_t)A.kv_heads];
 #pragma unroll
     for (int i = 0; i < ST; i++) {
       const int d = (tid + KV_THREADS * i) / 4;
-      vr[i] = ld16(A.v_codes + block * page_bytes + ((int64_t)d << A.log_page) + ((t * TILE + 16 * (tid & 3)) & in_page));
+      vr[i] = ld16(vbase + ((uint64_t)id * page_bytes + (d << A.log_page) + ((t * TILE + 16 * (tid & 3)) & in_page)));
     }
   };
-  auto store = [&](int64_t t, int buf) {
+  auto store = [&](int t, int buf) {
 #pragma unroll
     for (int i = 0; i < ST; i++) {
       const int x = tid + KV_THREADS * i, tok = x / KS, k = x % KS, u = tok >> 5, th = (tok >> 4) & 1, tr = tok & 15;
@@ -927,7 +983,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_prompt(const KvArgs A, con
       *reinterpret_cast<bf16x8_t*>(p + 32 * 16) = e4m3_bf16x8(kr[i][2], kr[i][3], s);
     }
     const int tg = tid & 3;
-    const int64_t j = t * TILE + 16 * tg;
+    const int j = t * TILE + 16 * tg;
     float s = e8m0_as_scale(vsc);
     const bool edge = !vok || j < lo || j + 16 > hi;
     if (!vok || j + 16 <= lo || j >= hi) s = 1.0f;
@@ -949,8 +1005,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_prompt(const KvArgs A, con
 #pragma unroll
     for (int i = 0; i < 16; i++) o[d][i] = 0.0f;
   float mx = -INFINITY, l = 0.0f;
-  const float c = CAP ? LOG2E : A.sm_scale * LOG2E;
-  const float inv_cap = CAP ? A.sm_scale / A.softcap : 0.0f;
+  const KvScore<CAP> sc(A);
   if (t0 < t1) {
     load_ids(t0);
     load(t0);
@@ -960,15 +1015,15 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_prompt(const KvArgs A, con
     load_ids(t0 + 2);
   }
   __syncthreads();
-  for (int64_t t = t0; t < t1; t++) {
-    const int buf = (int)(t - t0) & 1;
+  for (int t = t0; t < t1; t++) {
+    const int buf = (t - t0) & 1;
     if (t + 1 < t1) {
       store(t + 1, buf ^ 1);
-      load(t + 2);                            // past t1: a clamped column, not used
+      load(t + 2);
       load_ids(t + 3);
     }
-    const int64_t j0 = t * TILE;
-    if (w_last >= wrow && j0 <= w_max && j0 + TILE > w_lo_min) {
+    const int j0 = t * TILE;
+    if (w_rows > 0 && j0 <= w_max && j0 + TILE > w_lo_min) {
       f32x16_t s[2];
 #pragma unroll
       for (int u = 0; u < 2; u++) {
@@ -984,24 +1039,23 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_prompt(const KvArgs A, con
 #pragma unroll
         for (int u = 0; u < 2; u++)
 #pragma unroll
-          for (int i = 0; i < 16; i++) s[u][i] = kv_softcap(s[u][i], A.softcap, inv_cap);
+          for (int i = 0; i < 16; i++) s[u][i] = sc.cap(s[u][i]);
       }
       const bool ok0 = sok[buf][h], ok1 = sok[buf][2 + h];
       if (j0 + TILE - 1 > w_min || j0 < w_lo_max || __any(!ok0 || !ok1)) {
 #pragma unroll
-        for (int u = 0; u < 2; u++)
+        for (int u = 0; u < 2; u++) {
+          const int j = j0 + 32 * u + 16 * h, z = (u ? ok1 : ok0) ? pos - j : -1, b = rlo - j;
 #pragma unroll
-          for (int i = 0; i < 16; i++) {
-            const int64_t j = j0 + 32 * u + 16 * h + i;
-            s[u][i] = j <= pos && j >= rlo && (u ? ok1 : ok0) ? s[u][i] : -INFINITY;
-          }
+          for (int i = 0; i < 16; i++) s[u][i] = i <= z && i >= b ? s[u][i] : sc.NONE;
+        }
       }
-      float mt = -INFINITY;
+      float mt = sc.NONE;
 #pragma unroll
       for (int u = 0; u < 2; u++)
 #pragma unroll
-        for (int i = 0; i < 16; i++) mt = __builtin_fmaxf(mt, s[u][i]);
-      mt = __builtin_fmaxf(mt, __shfl_xor(mt, 32, 64)) * c;
+        for (int i = 0; i < 16; i++) mt = sc.top(mt, s[u][i]);
+      mt = __builtin_fmaf(sc.top(mt, __shfl_xor(mt, 32, 64)), sc.mul, sc.add);
       if (__any(mt > mx)) {
         const float mn = __builtin_fmaxf(mx, mt);
         const float f = mx == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx - mn);
@@ -1010,14 +1064,14 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_prompt(const KvArgs A, con
 #pragma unroll
         for (int d = 0; d < DT; d++) o[d] *= f;
       }
-      const float off = mx == -INFINITY ? 0.0f : mx;
+      const float off = sc.add - (mx == -INFINITY ? 0.0f : mx);
 #pragma unroll
       for (int u = 0; u < 2; u++) {
         uint32_t pw[8];
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-          const float a = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][2 * i], c, -off));
-          const float b = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][2 * i + 1], c, -off));
+          const float a = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][2 * i], sc.mul, off));
+          const float b = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][2 * i + 1], sc.mul, off));
           l += a + b;
           pw[i] = pack_bf16x2(a, b);          // half a step of 2^-8 per probability, l keeps fp32
         }
@@ -1038,7 +1092,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_prompt(const KvArgs A, con
   l += __shfl_xor(l, 32, 64);
   const bool split = it.splits > 1;
   if (split && tid == 0 && kvh == 0)
-    part.rec[it.slot] = KvRec{it.split ? 0 : it.splits, it.rows, it.q0 * A.group + it.r0};
+    part.rec[it.slot] = KvRec{it.split ? 0 : it.splits, it.rows, it.q0 + rows.first, rows.head0};
   if (!live) return;
   if (split) {
     const int64_t at = (it.slot * A.kv_heads + kvh) * PROWS + wrow + m;
@@ -1054,7 +1108,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_prompt(const KvArgs A, con
     }
     return;
   }
-  const int64_t orow = qrow * A.q_heads + kvh * A.group + r % A.group;
+  const int64_t orow = (int64_t)(it.q0 + rows.first + query) * A.q_heads + rhead;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
   for (int d = 0; d < DT; d++)
@@ -1074,7 +1128,7 @@ template <int D, int R>
 __device__ __forceinline__ void kv_join(const KvArgs& A, const KvPart& part, int64_t slot, int sub, int kvh) {
   if (slot >= part.used[0]) return;
   const KvRec rec = part.rec[slot];
-  if (rec.splits == 0) return;
+  if (rec.splits == 0 || slot + rec.splits > part.slots) return;
   constexpr int LANES = D / 4, GROUPS = 64 / LANES, DEEP = 4;
   const int lane = threadIdx.x & 63, grp = lane / LANES, ch = (lane % LANES) * 4;
   const int64_t step = (int64_t)A.kv_heads * R;
@@ -1118,8 +1172,8 @@ __device__ __forceinline__ void kv_join(const KvArgs& A, const KvPart& part, int
       M = top;
     }
     if (grp == 0) {
-      const int64_t rr = rec.row0 + row;
-      const int64_t orow = rr / A.group * A.q_heads + kvh * A.group + rr % A.group;
+      const uint32_t rr = rec.head0 + row, group = A.group;
+      const int64_t orow = (int64_t)(rec.query0 + rr / group) * A.q_heads + kvh * group + rr % group;
       const float inv = L == 0.0f ? 0.0f : 1.0f / L;
       *reinterpret_cast<u32x2_t*>(A.out + orow * D + ch) =
           u32x2_t{pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv)};
@@ -1128,14 +1182,14 @@ __device__ __forceinline__ void kv_join(const KvArgs& A, const KvPart& part, int
   }
 }
 
-// Workgroups of the decode slots first, then PROWS / 16 for each prompt slot.
-template <int D>
+// Workgroups of the decode slots first (NR each), then PROWS / 16 for each prompt slot.
+template <int D, int NR>
 __global__ __launch_bounds__(KV_THREADS) void k_kv_join(const KvArgs A, const KvPart dec, const KvPart pro,
                                                         int64_t dec_slots) {
-  const int kvh = (int)(blockIdx.x % A.kv_heads);
-  const int64_t x = blockIdx.x / A.kv_heads;
-  if (x < dec_slots) kv_join<D, DROWS>(A, dec, x, 0, kvh);
-  else kv_join<D, PROWS>(A, pro, (x - dec_slots) / (PROWS / 16), (int)((x - dec_slots) % (PROWS / 16)), kvh);
+  const int kvh = (int)(blockIdx.x % (unsigned)A.kv_heads);
+  const int64_t x = blockIdx.x / (unsigned)A.kv_heads;
+  if (x < dec_slots * NR) kv_join<D, 16 * NR>(A, dec, x / NR, (int)(x % NR), kvh);
+  else kv_join<D, PROWS>(A, pro, (x - dec_slots * NR) / (PROWS / 16), (int)((x - dec_slots * NR) % (PROWS / 16)), kvh);
 }
 
 int log2_page(int page) {
@@ -1227,7 +1281,8 @@ constexpr int DEC_MIN = 4, PRO_MIN = 4;
 // most splits + row tiles; slots (items of requests with two splits or more)
 // at most 2 * splits, and no more than the tiles of the table's width allow.
 struct KvPlan {
-  bool decode, prompt, join;
+  bool prompt, join;
+  int nr;                                     // 16-row columns of a decode tile
   int64_t dec_splits, dec_items, dec_slots, pro_splits, pro_items, pro_slots;
   size_t dec_rec, dec_sums, dec_stats, pro_used, pro_rec, pro_sums, pro_stats, bytes;
 };
@@ -1237,11 +1292,13 @@ KvPlan kv_plan(int64_t batch, int64_t tokens, int64_t max_q, int q_heads, int kv
   KvPlan p = {};
   const int64_t group = q_heads / kv_heads, reqs = batch < tokens ? batch : tokens;
   const int64_t tiles = (max_blocks * page + TILE - 1) / TILE;
-  p.decode = true;
-  p.prompt = !(max_q > 0 && max_q * group <= DROWS) && tokens * group > DROWS;
+  const int64_t most_q = max_q > 0 && max_q < tokens ? max_q : tokens;
+  p.prompt = most_q * group > SHORT_ROWS;
+  p.nr = most_q * group <= 16 ? 1 : 2;
+  const int drows = 16 * p.nr;
   p.dec_splits = (DEC_ITEMS + kv_heads - 1) / kv_heads;
   p.pro_splits = (PRO_ITEMS + kv_heads - 1) / kv_heads;
-  const int64_t dec_rows = p.prompt ? reqs : tokens * group / DROWS + reqs;
+  const int64_t dec_rows = (p.prompt ? (reqs < tokens * group / drows ? reqs : tokens * group / drows) : tokens * group / drows) + reqs;
   const int64_t pro_rows = p.prompt ? tokens * group / PROWS + reqs : 0;
   p.dec_items = dec_rows + p.dec_splits;
   p.pro_items = p.prompt ? pro_rows + p.pro_splits : 0;
@@ -1261,8 +1318,8 @@ KvPlan kv_plan(int64_t batch, int64_t tokens, int64_t max_q, int q_heads, int kv
   };
   take(8);
   p.dec_rec = take(p.dec_slots * sizeof(KvRec));
-  p.dec_sums = take((size_t)p.dec_slots * kv_heads * DROWS * head_dim * 4);
-  p.dec_stats = take((size_t)p.dec_slots * kv_heads * DROWS * 8);
+  p.dec_sums = take((size_t)p.dec_slots * kv_heads * drows * head_dim * 4);
+  p.dec_stats = take((size_t)p.dec_slots * kv_heads * drows * 8);
   p.pro_used = take(8);
   p.pro_rec = take(p.pro_slots * sizeof(KvRec));
   p.pro_sums = take((size_t)p.pro_slots * kv_heads * PROWS * head_dim * 4);
@@ -1275,7 +1332,7 @@ bool kv_sizes_ok(int64_t batch, int64_t tokens, int64_t max_q, int32_t q_heads, 
                  int64_t max_blocks) {
   return batch >= 0 && batch <= 0x7FFFFFFF && tokens >= 0 && tokens <= 0x7FFFFFFF && max_q >= 0 &&
          max_q <= 0x7FFFFFFF && kv_heads >= 1 && q_heads >= kv_heads && q_heads % kv_heads == 0 && q_heads <= 65535 &&
-         max_blocks >= 1 && max_blocks <= 0x7FFFFFFF / page;
+         tokens * (q_heads / kv_heads) <= 0x7FFFFFFF - PROWS && max_blocks >= 1 && max_blocks <= 0x7FFFFF00 / page;
 }
 
 template <int D, bool CAP>
@@ -1283,13 +1340,16 @@ void launch_attention(const KvArgs& A, const KvPlan& p, const KvPart& dec, const
   const unsigned h = (unsigned)A.kv_heads;
   if (p.prompt) {
     k_kv_prompt<D, CAP><<<(unsigned)p.pro_items * h, KV_THREADS, 0, s>>>(A, pro);
-    k_kv_decode<D, CAP, REQ_SHORT><<<(unsigned)p.dec_items * h, KV_THREADS, 0, s>>>(A, dec);
+    k_kv_decode<D, CAP, REQ_SHORT, 2><<<(unsigned)p.dec_items * h, KV_THREADS, 0, s>>>(A, dec);
+  } else if (p.nr == 2) {
+    k_kv_decode<D, CAP, REQ_ALL, 2><<<(unsigned)p.dec_items * h, KV_THREADS, 0, s>>>(A, dec);
   } else {
-    k_kv_decode<D, CAP, REQ_ALL><<<(unsigned)p.dec_items * h, KV_THREADS, 0, s>>>(A, dec);
+    k_kv_decode<D, CAP, REQ_ALL, 1><<<(unsigned)p.dec_items * h, KV_THREADS, 0, s>>>(A, dec);
   }
-  if (p.join)
-    k_kv_join<D><<<(unsigned)((p.dec_slots + p.pro_slots * (PROWS / 16)) * h), KV_THREADS, 0, s>>>(A, dec, pro,
-                                                                                               p.dec_slots);
+  if (!p.join) return;
+  const unsigned groups = (unsigned)((p.dec_slots * p.nr + p.pro_slots * (PROWS / 16)) * h);
+  if (p.nr == 2) k_kv_join<D, 2><<<groups, KV_THREADS, 0, s>>>(A, dec, pro, p.dec_slots);
+  else k_kv_join<D, 1><<<groups, KV_THREADS, 0, s>>>(A, dec, pro, p.dec_slots);
 }
 
 }  // namespace
@@ -1328,12 +1388,12 @@ wq_status wq_kv_attention(const void* q_bf16, int64_t q_stride, const int32_t* c
   if (ws_bytes < p.bytes || !workspace) return WQ_EINVAL;
   if ((p.pro_items > p.dec_items ? p.pro_items : p.dec_items) * kv_heads > 0x7FFFFFFF / KV_THREADS) return WQ_EINVAL;
   const KvArgs A = {(const uint16_t*)q_bf16, q_stride, cu_q, kv_lens, batch, tokens, q_heads, kv_heads,
-                    q_heads / kv_heads, k_codes, k_scales, v_codes, v_scales, log2_page(page), num_pages, block_table,
-                    max_blocks, sm_scale, softcap, window, out, lse};
+                    q_heads / kv_heads, (int)(window < 0x7FFFFFFF ? window : 0), k_codes, k_scales, v_codes, v_scales, log2_page(page), num_pages, block_table,
+                    max_blocks, sm_scale, softcap, out, lse};
   uint8_t* ws = (uint8_t*)workspace;
-  const KvPart dec = {p.dec_splits, DEC_MIN, (int64_t*)ws, (KvRec*)(ws + p.dec_rec), (float*)(ws + p.dec_sums),
+  const KvPart dec = {p.dec_splits, p.dec_slots, DEC_MIN, (int64_t*)ws, (KvRec*)(ws + p.dec_rec), (float*)(ws + p.dec_sums),
                       (float*)(ws + p.dec_stats)};
-  const KvPart pro = {p.pro_splits, PRO_MIN, (int64_t*)(ws + p.pro_used), (KvRec*)(ws + p.pro_rec),
+  const KvPart pro = {p.pro_splits, p.pro_slots, PRO_MIN, (int64_t*)(ws + p.pro_used), (KvRec*)(ws + p.pro_rec),
                       (float*)(ws + p.pro_sums), (float*)(ws + p.pro_stats)};
   hipStream_t s = (hipStream_t)stream;
   if (head_dim == 128) {
