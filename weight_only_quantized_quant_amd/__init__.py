@@ -405,8 +405,12 @@ def wq_moe_gemm_w4a8(x8: torch.Tensor, a_scale: torch.Tensor, row_token, offsets
 # ---------------------------------------------------------------------------
 # These calls are made once per layer of a decode step, where the host's time is the
 # operator's time: one look at a tensor that is as it should be, the words only when it is not.
-def _on(t, dev, dtype, name):
-    """A contiguous tensor of `dtype` on GPU `dev`."""
+_u8, _i32t, _i64t, _bf16 = torch.uint8, torch.int32, torch.int64, torch.bfloat16
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+
+
+def _ptr(t, dev, dtype, name):
+    """The address of a contiguous tensor of `dtype` on GPU `dev`."""
     if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous():
         _dev(t, name)
         if t.dtype != dtype:
@@ -415,34 +419,28 @@ def _on(t, dev, dtype, name):
     return t.data_ptr()
 
 
-def _index(t, dev, dtype, shape, name):
+def _shaped(t, dev, dtype, shape, name):
     """The same, of a given shape."""
-    ptr = _on(t, dev, dtype, name)
+    ptr = _ptr(t, dev, dtype, name)
     if t.shape != shape:
         raise ValueError(f"{name} must be of shape {shape}, not {tuple(t.shape)}")
     return ptr
 
 
-class _Launch:
+def _launch(fn, dev, where, *args):
     """The launch goes to the tensors' device, whichever is current, and to its current stream."""
-
-    def __init__(self, dev):
-        self.dev = dev
-
-    def __enter__(self):
-        self.back = torch.cuda.current_device()
-        if self.back != self.dev:
-            torch.cuda.set_device(self.dev)
-        return torch._C._cuda_getCurrentRawStream(self.dev)
-
-    def __exit__(self, *exc):
-        if self.back != self.dev:
-            torch.cuda.set_device(self.back)
-        return False
+    back = _current_device()
+    if back == dev:
+        status = fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _raw_stream(dev))
+    if status:
+        _check(status, where)
 
 
 def _token_rows(t, name):
-    """Elements between the tokens of a [tokens, heads, dim] tensor whose rows are dense
+    """(device, tokens, heads, head_dim, elements between tokens) of a tensor whose rows are dense
     (a slice of a fused projection's output may have a larger stride)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA (HIP) tensor")
@@ -452,13 +450,13 @@ def _token_rows(t, name):
     sn, sh, sd = t.stride()
     if sd != 1 or (sh != d and h > 1):
         raise ValueError(f"the heads of a token of {name} must be dense")
-    return sn if n > 1 else h * d
+    return t.get_device(), n, h, d, sn if n > 1 else h * d
 
 
 def _kv_cache(k_codes, k_scales, v_codes, v_scales, dev):
     """(num_pages, heads, page, head_dim) of a cache and the addresses of its four tensors."""
-    kc, ks = _on(k_codes, dev, torch.uint8, "k_codes"), _on(k_scales, dev, torch.uint8, "k_scales")
-    vc, vs = _on(v_codes, dev, torch.uint8, "v_codes"), _on(v_scales, dev, torch.uint8, "v_scales")
+    kc, ks = _ptr(k_codes, dev, _u8, "k_codes"), _ptr(k_scales, dev, _u8, "k_scales")
+    vc, vs = _ptr(v_codes, dev, _u8, "v_codes"), _ptr(v_scales, dev, _u8, "v_scales")
     if k_codes.dim() != 4:
         raise ValueError("k_codes must be [num_pages, heads, page, head_dim]")
     n, h, p, d = k_codes.shape
@@ -477,28 +475,27 @@ def wq_kv_blocks(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: tor
     cu_new int32 [B + 1], kv_lens int32 [B], state int32 [2]: the next cursor and the number of
     refused requests)."""
     _dev(ctx_lens, "ctx_lens")
-    dev = ctx_lens.get_device()
-    if ctx_lens.dtype != torch.int32 or ctx_lens.dim() != 1:
+    dev, (B, *rest) = ctx_lens.get_device(), ctx_lens.shape or (0, 0)
+    if ctx_lens.dtype is not _i32t or rest:
         raise ValueError("ctx_lens must be int32 [batch]")
-    B = ctx_lens.shape[0]
-    nl = _index(new_lens, dev, torch.int32, (B,), "new_lens")
-    free = _on(free_pages, dev, torch.int32, "free_pages")
-    table = _on(block_table, dev, torch.int32, "block_table")
+    new = _shaped(new_lens, dev, _i32t, (B,), "new_lens")
+    free = _ptr(free_pages, dev, _i32t, "free_pages")
+    table = _ptr(block_table, dev, _i32t, "block_table")
     if free_pages.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("free_pages must be [pages] and block_table [batch, max_blocks]")
     cur = None
     if cursor is not None:
-        cur = _on(cursor, dev, torch.int32, "cursor")
+        cur = _ptr(cursor, dev, _i32t, "cursor")
         if cursor.numel() < 1:
             raise ValueError("cursor must have an element")
     if tokens < 0:
         raise ValueError("tokens must not be negative")
-    with _Launch(dev) as stream:
-        slots = ctx_lens.new_empty(tokens, dtype=torch.int64)
-        positions, cu_new, kv_lens, state = ctx_lens.new_empty(tokens + 2 * B + 3).split((tokens, B + 1, B, 2))
-        _check(lib.wq_kv_blocks(ctx_lens.data_ptr(), nl, B, free, free_pages.shape[0], cur, page, table,
-                                block_table.shape[1], tokens, slots.data_ptr(), positions.data_ptr(),
-                                cu_new.data_ptr(), kv_lens.data_ptr(), state.data_ptr(), stream), "wq_kv_blocks")
+    slots = ctx_lens.new_empty(tokens, dtype=_i64t)
+    positions, cu_new, kv_lens, state = torch.split_with_sizes(ctx_lens.new_empty(tokens + 2 * B + 3),
+                                                               (tokens, B + 1, B, 2))
+    _launch(lib.wq_kv_blocks, dev, "wq_kv_blocks", ctx_lens.data_ptr(), new, B, free, free_pages.shape[0], cur, page,
+            table, block_table.shape[1], tokens, slots.data_ptr(), positions.data_ptr(), cu_new.data_ptr(), kv_lens.data_ptr(),
+            state.data_ptr())
     return slots, positions, cu_new, kv_lens, state
 
 
@@ -507,16 +504,14 @@ def wq_kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_codes:
     """Quantize k, v (bf16/fp32 [tokens, heads, head_dim], tokens may be strided) into their slots
     (int64 [tokens], negative: skipped) of the cache: codes uint8 [N, heads, page, head_dim] and
     [N, heads, head_dim, page], E8M0 scales uint8 [N, heads]."""
-    k_stride, v_stride = _token_rows(k, "k"), _token_rows(v, "v")
-    dev = k.get_device()
+    dev, T, heads, hd, k_stride = _token_rows(k, "k")
+    v_stride = _token_rows(v, "v")[4]
     n, h, p, dim, kc, ks, vc, vs = _kv_cache(k_codes, k_scales, v_codes, v_scales, dev)
-    T = k.shape[0]
-    if k.shape != (T, h, dim) or v.shape != k.shape or v.dtype != k.dtype or v.get_device() != dev:
+    if heads != h or hd != dim or v.shape != k.shape or v.dtype is not k.dtype or v.get_device() != dev:
         raise ValueError(f"k and v must be [tokens, {h}, {dim}] of one dtype on one device")
-    sp = _index(slots, dev, torch.int64, (T,), "slots")
-    with _Launch(dev) as stream:
-        _check(lib.wq_kv_append(k.data_ptr(), k_stride, v.data_ptr(), v_stride, _x_dtype(k), sp, T, h, dim, p, n, kc,
-                                ks, vc, vs, stream), "wq_kv_append")
+    sp = _shaped(slots, dev, _i64t, (T,), "slots")
+    _launch(lib.wq_kv_append, dev, "wq_kv_append", k.data_ptr(), k_stride, v.data_ptr(), v_stride, _x_dtype(k), sp, T,
+            h, dim, p, n, kc, ks, vc, vs)
 
 
 def wq_kv_attention_workspace_size(batch: int, tokens: int, max_q: int, q_heads: int, kv_heads: int, head_dim: int,
@@ -533,36 +528,33 @@ def wq_kv_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tens
     cu_q int32 [B + 1], kv_lens int32 [B], block_table int32 [B, W].  sm_scale defaults to
     head_dim ** -0.5; max_q: the largest number of queries of one request if known.  Returns out
     bf16 [tokens, q_heads, head_dim] (and lse fp32 [tokens, q_heads])."""
-    q_stride = _token_rows(q, "q")
-    dev = q.get_device()
+    dev, T, hq, qd, q_stride = _token_rows(q, "q")
     n, h, p, dim, kc, ks, vc, vs = _kv_cache(k_codes, k_scales, v_codes, v_scales, dev)
-    T, hq, qd = q.shape
-    if q.dtype is not torch.bfloat16 or qd != dim:
+    if q.dtype is not _bf16 or qd != dim:
         raise ValueError(f"q must be bfloat16 [tokens, q_heads, {dim}]")
-    table = _on(block_table, dev, torch.int32, "block_table")
+    table = _ptr(block_table, dev, _i32t, "block_table")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [batch, max_blocks]")
     B, width = block_table.shape
-    cu = _index(cu_q, dev, torch.int32, (B + 1,), "cu_q")
-    kl = _index(kv_lens, dev, torch.int32, (B,), "kv_lens")
+    cu = _shaped(cu_q, dev, _i32t, (B + 1,), "cu_q")
+    kl = _shaped(kv_lens, dev, _i32t, (B,), "kv_lens")
     if sm_scale is None:
         sm_scale = dim ** -0.5
-    with _Launch(dev) as stream:
-        if out is None:
-            out = q.new_empty((T, hq, dim))
-        else:
-            _index(out, dev, torch.bfloat16, (T, hq, dim), "out")
-        lse = q.new_empty((T, hq), dtype=torch.float32) if return_lse else None
-        if workspace is None:
-            ws_bytes = lib.wq_kv_attention_workspace_size(B, T, max_q, hq, h, dim, p, width)
-            workspace = q.new_empty(ws_bytes, dtype=torch.uint8)
-        else:
-            _on(workspace, dev, workspace.dtype, "workspace")
-            ws_bytes = workspace.numel() * workspace.element_size()
-        _check(lib.wq_kv_attention(q.data_ptr(), q_stride, cu, kl, B, T, max_q, hq, h, dim, kc, ks, vc, vs, p, n,
-                                   table, width, sm_scale, softcap, window, out.data_ptr(),
-                                   lse.data_ptr() if return_lse else None, workspace.data_ptr(), ws_bytes, stream),
-               "wq_kv_attention")
+    if out is None:
+        out = q.new_empty((T, hq, dim))
+        op = out.data_ptr()
+    else:
+        op = _shaped(out, dev, _bf16, (T, hq, dim), "out")
+    lse = q.new_empty((T, hq), dtype=torch.float32) if return_lse else None
+    if workspace is None:
+        ws_bytes = lib.wq_kv_attention_workspace_size(B, T, max_q, hq, h, dim, p, width)
+        workspace = q.new_empty(ws_bytes, dtype=_u8)
+    else:
+        _ptr(workspace, dev, workspace.dtype, "workspace")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _launch(lib.wq_kv_attention, dev, "wq_kv_attention", q.data_ptr(), q_stride, cu, kl, B, T, max_q, hq, h, dim, kc,
+            ks, vc, vs, p, n, table, width, sm_scale, softcap, window, op, lse.data_ptr() if return_lse else None,
+            workspace.data_ptr(), ws_bytes)
     return (out, lse) if return_lse else out
 
 
