@@ -450,10 +450,10 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_append(
 // Rows of one key/value head are numbered r = query * group + head in group:
 // the `group` query heads that share a key/value head share its tiles.
 constexpr int TILE = 64;                      // tokens per step
-constexpr int PROWS = 128;                    // rows of a prompt tile
+constexpr int PROWS = 128, PTHREADS = 256;    // rows of a prompt tile, threads of its workgroup
 // Requests of at most this many rows go through the decode kernel beside
 // prompts: its tiles of 32 read K and V once each, the prompt kernel once for
-// 128, but a prompt tile costs its 128 rows' arithmetic however few there are.
+// 128, but a prompt tile's staging and barriers cost the same however few there are.
 constexpr int SHORT_ROWS = 64;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
@@ -794,7 +794,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
         for (int i = 0; i < 4; i++) mt = sc.top(mt, s[c][a][i]);
       mt = sc.top(mt, __shfl_xor(mt, 16, 64));
       mt = __builtin_fmaf(sc.top(mt, __shfl_xor(mt, 32, 64)), sc.mul, sc.add);
-      if (__any(mt > mx[c])) {
+      if (__any(mt > mx[c] + 8.0f)) {
         const float mn = __builtin_fmaxf(mx[c], mt);
         const float f = mx[c] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx[c] - mn);
         mx[c] = mn;
@@ -888,38 +888,139 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
 }
 
 // Prompts and chunks: 128 rows per workgroup, 32 per wave.  Bound by the
-// matrix cores and the exponentials: a tile of 64 tokens is converted to bf16
-// once per workgroup, on its way from registers (loaded a step ahead) to LDS,
-// where it lies in operand order (each fragment 1 KB contiguous, its 16-byte
-// units permuted by an xor so that neither the writes nor the reads conflict),
-// and feeds v_mfma_f32_32x32x16_bf16.
+// vector instructions of the softmax and the matrix cores alike, so the loop
+// is arranged for the two to overlap: half a tile's scores (32 tokens) are
+// multiplied while those of the half before are exponentiated.  A tile of 64 tokens is
+// converted to bf16 once per workgroup, on its way from registers (loaded a
+// step ahead) to LDS, where it lies in operand order (each fragment 1 KB
+// contiguous, its 16-byte units permuted by an xor so that neither the writes
+// nor the reads conflict), and feeds v_mfma_f32_32x32x16_bf16.
 //
 // Lane l = 32 h + m.  Within a 32-token half u of the tile, operand row
 // 8 (r / 4) + 4 h + r % 4 is token 32 u + 16 h + r: result register r of lane
 // half h is that token.
 template <int D, bool CAP>
-__global__ __launch_bounds__(KV_THREADS, 2) void k_kv_prompt(const KvArgs A, const KvPart part) {
-  constexpr int KS = D / 16, DT = D / 32, ST = D / 64;             // k steps, channel tiles, 16-byte pieces a thread
+__global__ __launch_bounds__(PTHREADS, 2) void k_kv_prompt(const KvArgs A, const KvPart part) {
+  constexpr int KS = D / 16, DT = D / 32;     // k steps, channel tiles
   constexpr int XK = D == 128 ? 1 : 2;
-  __shared__ __attribute__((aligned(16))) uint8_t sk[2][TILE * D * 2], sv[2][TILE * D * 2];
-  __shared__ int sok[2][4];
+  constexpr int ST = D / 64;                  // 16-byte pieces of K, and of V^T, a thread
+  __shared__ __attribute__((aligned(16))) uint8_t sk[3][TILE * D * 2], sv[2][TILE * D * 2];
   const int64_t item = blockIdx.x / (unsigned)A.kv_heads;
   const int kvh = (int)(blockIdx.x % (unsigned)A.kv_heads);
   KvItem it;
   if (!kv_find<PROWS, REQ_LONG>(A, part, item, blockIdx.x == 0, it)) return;
   if (it.splits > 1 && it.slot >= part.slots) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 31, h = lane >> 5;
+  const int tid = threadIdx.x, lane = tid & 63, m = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const KvRows rows(A, it);
   int lo, hi, t0, t1;
   kv_tiles(A, it, rows, lo, hi, t0, t1);
+  const bool split = it.splits > 1;
+  if (split && tid == 0 && kvh == 0)
+    part.rec[it.slot] = KvRec{it.split ? 0 : it.splits, it.rows, it.q0 + rows.first, rows.head0};
 
   const int wrow = wave * 32;                 // first row of the wave in the tile
   const bool live = wrow + m < it.rows;
-  const int ri = live ? wrow + m : 0, query = rows.query(A, ri), rhead = kvh * A.group + rows.head(A, ri);
+  const int ri = live ? wrow + m : 0, query = rows.query(A, ri), head = kvh * A.group + rows.head(A, ri);
   const int pos = rows.pos0 + query, rlo = kv_lowest(pos, A.window);
   bf16x8_t qf[KS];
+  // limits of the wave's rows; a wave without rows computes nothing
+  const int w_rows = it.rows - wrow < 32 ? it.rows - wrow : 32;
+  const int w_min = rows.pos0 + rows.query(A, wrow), w_max = rows.pos0 + rows.query(A, wrow + (w_rows > 0 ? w_rows - 1 : 0));
+  const int w_lo_max = kv_lowest(w_max, A.window);
+  const int32_t* tab = A.table + (int64_t)it.request * A.max_blocks;
+  const int last_col = (int)A.max_blocks - 1;
+  const uint32_t head_bytes = (uint32_t)D << A.log_page, page_bytes = head_bytes * A.kv_heads;
+  const int in_page = (1 << A.log_page) - 1;
+  const uint8_t *ksb = A.k_scales + kvh, *vsb = A.v_scales + kvh;
+
+  // staging: K piece x is token x / KS, channels 16 (x % KS)..; V^T piece x is
+  // channel x / 4, tokens 16 (x % 4)..; a thread's pieces are 256 apart, so that
+  // they differ by 256 / KS tokens and by 64 channels
+  const int ktok = tid / KS, vtok = 16 * (tid & 3);
+  const uint8_t* kbase = A.k_codes + (int64_t)kvh * head_bytes + 16 * (tid % KS);
+  const uint8_t* vbase = A.v_codes + (int64_t)kvh * head_bytes + ((tid >> 2) << A.log_page);
+  uint8_t *kdst[ST], *vdst[ST];
+#pragma unroll
+  for (int i = 0; i < ST; i++) {
+    const int tok = ktok + PTHREADS / KS * i, k = tid % KS, u = tok >> 5, th = (tok >> 4) & 1, tr = tok & 15;
+    const int row = 8 * (tr >> 2) + 4 * th + (tr & 3);
+    kdst[i] = sk[0] + ((u * KS + k) * 64 + (row ^ (XK * k))) * 16;
+    const int d = (tid >> 2) + 64 * i, tg = tid & 3;
+    vdst[i] = sv[0] + (((d >> 5) * 4 + 2 * (tg >> 1)) * 64 + 32 * (tg & 1) + ((d & 31) ^ (2 * tg))) * 16;
+  }
+  constexpr int BUF = TILE * D * 2;
+  u32x4_t kr[ST], vr[ST];
+  uint32_t ksc[ST], vsc;
+  bool vok;
+  int idk[ST], idv;
+  auto page_id = [&](int t, int tok) {        // past t1 the last tile again: loaded, never used
+    const int c = ((t < t1 ? t : t1 - 1) * TILE + tok) >> A.log_page;
+    return tab[c < last_col ? c : last_col];
+  };
+  auto ids_k = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < ST; i++) idk[i] = page_id(t, ktok + PTHREADS / KS * i);
+  };
+  auto ids_v = [&](int t) { idv = page_id(t, vtok); };
+  int idm[2], idn[2];                         // pages of this lane's scores in tiles t and t + 1
+  auto ids_m = [&](int t) {
+#pragma unroll
+    for (int u = 0; u < 2; u++) idn[u] = page_id(t, 32 * u + 16 * h);
+  };
+  auto load_k = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < ST; i++) {
+      const uint32_t id = idk[i] >= 0 && idk[i] < A.num_pages ? idk[i] : 0;
+      ksc[i] = ksb[(uint64_t)id * (uint32_t)A.kv_heads];
+      kr[i] = ld16(kbase + ((uint64_t)id * page_bytes + ((t * TILE + ktok + PTHREADS / KS * i) & in_page) * D));
+    }
+  };
+  auto load_v = [&](int t) {
+    vok = idv >= 0 && idv < A.num_pages;
+    const uint32_t id = vok ? idv : 0;
+    vsc = vsb[(uint64_t)id * (uint32_t)A.kv_heads];
+    const uint8_t* p = vbase + ((uint64_t)id * page_bytes + ((t * TILE + vtok) & in_page));
+#pragma unroll
+    for (int i = 0; i < ST; i++) vr[i] = ld16(p + ((64 * i) << A.log_page));
+  };
+  auto store_k = [&](int at) {
+#pragma unroll
+    for (int i = 0; i < ST; i++) {
+      const float s = e8m0_as_scale(ksc[i]);
+      *reinterpret_cast<bf16x8_t*>(kdst[i] + at) = e4m3_bf16x8(kr[i][0], kr[i][1], s);
+      *reinterpret_cast<bf16x8_t*>(kdst[i] + at + 32 * 16) = e4m3_bf16x8(kr[i][2], kr[i][3], s);
+    }
+  };
+  auto store_v = [&](int t, int buf) {        // without the bytes that no row may see
+    const int j = t * TILE + vtok;
+    float s = e8m0_as_scale(vsc);
+    if (!vok || j < lo || j + 16 > hi) {
+      const int a = vok ? lo : 0, z = vok ? hi : 0;
+      if (j + 16 <= a || j >= z) s = 1.0f;
+#pragma unroll
+      for (int i = 0; i < ST; i++) vr[i] = keep_tokens(vr[i], j, a, z);
+    }
+#pragma unroll
+    for (int i = 0; i < ST; i++) {
+      *reinterpret_cast<bf16x8_t*>(vdst[i] + buf * BUF) = e4m3_bf16x8(vr[i][0], vr[i][1], s);
+      *reinterpret_cast<bf16x8_t*>(vdst[i] + buf * BUF + 64 * 16) = e4m3_bf16x8(vr[i][2], vr[i][3], s);
+    }
+  };
+  if (t0 < t1) {
+    ids_k(t0);
+    ids_v(t0);
+    ids_m(t0);
+    idm[0] = idn[0];
+    idm[1] = idn[1];
+    ids_m(t0 + 1);
+    load_k(t0);
+    load_v(t0);
+    ids_k(t0 + 1);
+    ids_v(t0 + 1);
+  }
   {
-    const uint16_t* qp = A.q + (int64_t)(it.q0 + rows.first + query) * A.q_stride + rhead * D;
+    const uint16_t* qp = A.q + (int64_t)(it.q0 + rows.first + query) * A.q_stride + head * D;
 #pragma unroll
     for (int k = 0; k < KS; k++) {
       u32x4_t w = ld16(qp + 16 * k + 8 * h);
@@ -927,77 +1028,6 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_prompt(const KvArgs A, con
       qf[k] = __builtin_bit_cast(bf16x8_t, w);
     }
   }
-  // limits of the wave's rows; a wave without rows computes nothing
-  const int w_rows = it.rows - wrow < 32 ? it.rows - wrow : 32;
-  const int w_min = rows.pos0 + rows.query(A, wrow), w_max = rows.pos0 + rows.query(A, wrow + (w_rows > 0 ? w_rows - 1 : 0));
-  const int w_lo_min = kv_lowest(w_min, A.window), w_lo_max = kv_lowest(w_max, A.window);
-  const int32_t* tab = A.table + (int64_t)it.request * A.max_blocks;
-  const int last_col = (int)A.max_blocks - 1;
-  const uint32_t head_bytes = (uint32_t)D << A.log_page, page_bytes = head_bytes * A.kv_heads;
-  const int in_page = (1 << A.log_page) - 1;
-  const uint8_t* kbase = A.k_codes + (int64_t)kvh * head_bytes;
-  const uint8_t* vbase = A.v_codes + (int64_t)kvh * head_bytes;
-  const uint8_t *ksb = A.k_scales + kvh, *vsb = A.v_scales + kvh;
-
-  // staging: piece x = tid + 256 i is K token x / KS, channels 16 (x % KS)..,
-  // and V^T channel x / 4, tokens 16 (x % 4)..
-  u32x4_t kr[ST], vr[ST];
-  uint32_t ksc[ST], vsc;
-  bool vok;
-  int idk[ST], idv;
-  auto load_ids = [&](int t) {                // past t1 a tile of the item again: loaded, never used
-    t = t < t1 ? t : t1 - 1;
-#pragma unroll
-    for (int i = 0; i < ST; i++) {
-      const int c = (t * TILE + (tid + KV_THREADS * i) / KS) >> A.log_page;
-      idk[i] = tab[c < last_col ? c : last_col];
-    }
-    const int c = (t * TILE + 16 * (tid & 3)) >> A.log_page;
-    idv = tab[c < last_col ? c : last_col];
-  };
-  auto load = [&](int t) {
-#pragma unroll
-    for (int i = 0; i < ST; i++) {
-      const int x = tid + KV_THREADS * i, tok = x / KS;
-      const uint32_t id = idk[i] >= 0 && idk[i] < A.num_pages ? idk[i] : 0;
-      ksc[i] = ksb[(uint64_t)id * (uint32_t)A.kv_heads];
-      kr[i] = ld16(kbase + ((uint64_t)id * page_bytes + ((t * TILE + tok) & in_page) * D + 16 * (x % KS)));
-    }
-    vok = idv >= 0 && idv < A.num_pages;
-    const uint32_t id = vok ? idv : 0;
-    vsc = vsb[(uint64_t)id * (uint32_t)A.kv_heads];
-#pragma unroll
-    for (int i = 0; i < ST; i++) {
-      const int d = (tid + KV_THREADS * i) / 4;
-      vr[i] = ld16(vbase + ((uint64_t)id * page_bytes + (d << A.log_page) + ((t * TILE + 16 * (tid & 3)) & in_page)));
-    }
-  };
-  auto store = [&](int t, int buf) {
-#pragma unroll
-    for (int i = 0; i < ST; i++) {
-      const int x = tid + KV_THREADS * i, tok = x / KS, k = x % KS, u = tok >> 5, th = (tok >> 4) & 1, tr = tok & 15;
-      const int row = 8 * (tr >> 2) + 4 * th + (tr & 3);
-      const float s = e8m0_as_scale(ksc[i]);
-      uint8_t* p = sk[buf] + ((u * KS + k) * 64 + (row ^ (XK * k))) * 16;
-      *reinterpret_cast<bf16x8_t*>(p) = e4m3_bf16x8(kr[i][0], kr[i][1], s);
-      *reinterpret_cast<bf16x8_t*>(p + 32 * 16) = e4m3_bf16x8(kr[i][2], kr[i][3], s);
-    }
-    const int tg = tid & 3;
-    const int j = t * TILE + 16 * tg;
-    float s = e8m0_as_scale(vsc);
-    const bool edge = !vok || j < lo || j + 16 > hi;
-    if (!vok || j + 16 <= lo || j >= hi) s = 1.0f;
-#pragma unroll
-    for (int i = 0; i < ST; i++) {
-      const int d = (tid + KV_THREADS * i) / 4;
-      u32x4_t w = vr[i];
-      if (edge) w = keep_tokens(w, j, vok ? lo : 0, vok ? hi : 0);
-      uint8_t* p = sv[buf] + (((d >> 5) * 4 + 2 * (tg >> 1)) * 64 + 32 * (tg & 1) + ((d & 31) ^ (2 * tg))) * 16;
-      *reinterpret_cast<bf16x8_t*>(p) = e4m3_bf16x8(w[0], w[1], s);
-      *reinterpret_cast<bf16x8_t*>(p + 64 * 16) = e4m3_bf16x8(w[2], w[3], s);
-    }
-    if (tid < 4) sok[buf][tid] = vok;
-  };
 
   f32x16_t o[DT];
 #pragma unroll
@@ -1006,93 +1036,116 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_prompt(const KvArgs A, con
     for (int i = 0; i < 16; i++) o[d][i] = 0.0f;
   float mx = -INFINITY, l = 0.0f;
   const KvScore<CAP> sc(A);
+  const uint8_t* kfrag = sk[0] + (32 * h) * 16;
+  const uint8_t* vfrag[2];
+#pragma unroll
+  for (int u = 0; u < 2; u++) vfrag[u] = sv[0] + (128 * u + 32 * h + (m ^ (2 * (2 * u + h)))) * 16;
+  auto scores = [&](int at, int u) {          // of half u of the tile whose K begins at `at`
+    f32x16_t z;
+#pragma unroll
+    for (int i = 0; i < 16; i++) z[i] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < KS; k++) {
+      const bf16x8_t a = *reinterpret_cast<const bf16x8_t*>(kfrag + at + (u * KS + k) * 1024 + (m ^ (XK * k)) * 16);
+      z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, qf[k], z, 0, 0, 0);
+    }
+    return z;
+  };
+  // caps and masks the scores of half u of tile t and moves the running
+  // maximum: only when a score passes it by 2^8, for the sums hold that and
+  // the result is the same
+  auto settle = [&](int t, int u, f32x16_t& s) {
+    const int j0 = t * TILE + 32 * u;
+    if constexpr (CAP) {
+#pragma unroll
+      for (int i = 0; i < 16; i++) s[i] = sc.cap(s[i]);
+    }
+    const bool ok = idm[u] >= 0 && idm[u] < A.num_pages;
+    if (j0 + 31 > w_min || j0 < w_lo_max || __any(!ok)) {
+      const int j = j0 + 16 * h, z = ok ? pos - j : -1, b = rlo - j;
+#pragma unroll
+      for (int i = 0; i < 16; i++) s[i] = i <= z && i >= b ? s[i] : sc.NONE;
+    }
+    float mt = sc.NONE;
+#pragma unroll
+    for (int i = 0; i < 16; i++) mt = sc.top(mt, s[i]);
+    mt = __builtin_fmaf(sc.top(mt, __shfl_xor(mt, 32, 64)), sc.mul, sc.add);
+    if (__any(mt > mx + 8.0f)) {
+      const float mn = __builtin_fmaxf(mx, mt);
+      const float f = mx == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx - mn);
+      mx = mn;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < DT; d++) o[d] *= f;
+    }
+  };
+  auto weigh = [&](int buf, int u, const f32x16_t& s) {            // probabilities, and their sums of V
+    const float off = sc.add - (mx == -INFINITY ? 0.0f : mx);
+    uint32_t pw[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const float a = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * i], sc.mul, off));
+      const float b = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * i + 1], sc.mul, off));
+      l += a + b;
+      pw[i] = pack_bf16x2(a, b);              // half a step of 2^-8 per probability, l keeps fp32
+    }
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+      const bf16x8_t p = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[4 * e], pw[4 * e + 1], pw[4 * e + 2], pw[4 * e + 3]}));
+#pragma unroll
+      for (int d = 0; d < DT; d++) {
+        const bf16x8_t a = *reinterpret_cast<const bf16x8_t*>(vfrag[u] + buf * BUF + d * 4096 + e * 1024);
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, p, o[d], 0, 0, 0);
+      }
+    }
+  };
+  // at the top of a step: first half of tile t settled, K of t and t + 1 and
+  // V^T of t in LDS, K of t + 2 and V^T of t + 1 on their way to registers
+  f32x16_t s0, s1;
+  int k0 = 0, k1 = BUF, k2 = 2 * BUF;         // K of t, t + 1, t + 2
   if (t0 < t1) {
-    load_ids(t0);
-    load(t0);
-    load_ids(t0 + 1);
-    store(t0, 0);
-    load(t0 + 1);
-    load_ids(t0 + 2);
+    store_k(k0);
+    store_v(t0, 0);
+    load_k(t0 + 1);
+    load_v(t0 + 1);
+    ids_k(t0 + 2);
+    ids_v(t0 + 2);
+    store_k(k1);
+    load_k(t0 + 2);
+    ids_k(t0 + 3);
+    tile_barrier();
+    if (w_rows > 0) {
+      s0 = scores(k0, 0);
+      settle(t0, 0, s0);
+    }
   }
-  __syncthreads();
   for (int t = t0; t < t1; t++) {
     const int buf = (t - t0) & 1;
-    if (t + 1 < t1) {
-      store(t + 1, buf ^ 1);
-      load(t + 2);
-      load_ids(t + 3);
+    if (w_rows > 0) {
+      s1 = scores(k0, 1);
+      weigh(buf, 0, s0);
+      settle(t, 1, s1);
+      s0 = scores(k1, 0);                     // behind the last tile: not used
+      weigh(buf, 1, s1);
     }
-    const int j0 = t * TILE;
-    if (w_rows > 0 && j0 <= w_max && j0 + TILE > w_lo_min) {
-      f32x16_t s[2];
-#pragma unroll
-      for (int u = 0; u < 2; u++) {
-#pragma unroll
-        for (int i = 0; i < 16; i++) s[u][i] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < KS; k++) {
-          const bf16x8_t a = *reinterpret_cast<const bf16x8_t*>(sk[buf] + ((u * KS + k) * 64 + 32 * h + (m ^ (XK * k))) * 16);
-          s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, qf[k], s[u], 0, 0, 0);
-        }
-      }
-      if constexpr (CAP) {
-#pragma unroll
-        for (int u = 0; u < 2; u++)
-#pragma unroll
-          for (int i = 0; i < 16; i++) s[u][i] = sc.cap(s[u][i]);
-      }
-      const bool ok0 = sok[buf][h], ok1 = sok[buf][2 + h];
-      if (j0 + TILE - 1 > w_min || j0 < w_lo_max || __any(!ok0 || !ok1)) {
-#pragma unroll
-        for (int u = 0; u < 2; u++) {
-          const int j = j0 + 32 * u + 16 * h, z = (u ? ok1 : ok0) ? pos - j : -1, b = rlo - j;
-#pragma unroll
-          for (int i = 0; i < 16; i++) s[u][i] = i <= z && i >= b ? s[u][i] : sc.NONE;
-        }
-      }
-      float mt = sc.NONE;
-#pragma unroll
-      for (int u = 0; u < 2; u++)
-#pragma unroll
-        for (int i = 0; i < 16; i++) mt = sc.top(mt, s[u][i]);
-      mt = __builtin_fmaf(sc.top(mt, __shfl_xor(mt, 32, 64)), sc.mul, sc.add);
-      if (__any(mt > mx)) {
-        const float mn = __builtin_fmaxf(mx, mt);
-        const float f = mx == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx - mn);
-        mx = mn;
-        l *= f;
-#pragma unroll
-        for (int d = 0; d < DT; d++) o[d] *= f;
-      }
-      const float off = sc.add - (mx == -INFINITY ? 0.0f : mx);
-#pragma unroll
-      for (int u = 0; u < 2; u++) {
-        uint32_t pw[8];
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-          const float a = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][2 * i], sc.mul, off));
-          const float b = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][2 * i + 1], sc.mul, off));
-          l += a + b;
-          pw[i] = pack_bf16x2(a, b);          // half a step of 2^-8 per probability, l keeps fp32
-        }
-#pragma unroll
-        for (int e = 0; e < 2; e++) {
-          const bf16x8_t p = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[4 * e], pw[4 * e + 1], pw[4 * e + 2], pw[4 * e + 3]}));
-#pragma unroll
-          for (int d = 0; d < DT; d++) {
-            const bf16x8_t a = *reinterpret_cast<const bf16x8_t*>(
-                sv[buf] + ((d * 4 + 2 * u + e) * 64 + 32 * h + (m ^ (2 * (2 * u + h)))) * 16);
-            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, p, o[d], 0, 0, 0);
-          }
-        }
-      }
-    }
-    __syncthreads();
+    if (t + 1 == t1) break;
+    store_k(k2);
+    store_v(t + 1, buf ^ 1);
+    load_k(t + 3);
+    load_v(t + 2);
+    ids_k(t + 4);
+    ids_v(t + 3);
+    tile_barrier();
+    idm[0] = idn[0];
+    idm[1] = idn[1];
+    ids_m(t + 2);
+    if (w_rows > 0) settle(t + 1, 0, s0);
+    const int k = k0;
+    k0 = k1;
+    k1 = k2;
+    k2 = k;
   }
   l += __shfl_xor(l, 32, 64);
-  const bool split = it.splits > 1;
-  if (split && tid == 0 && kvh == 0)
-    part.rec[it.slot] = KvRec{it.split ? 0 : it.splits, it.rows, it.q0 + rows.first, rows.head0};
   if (!live) return;
   if (split) {
     const int64_t at = (it.slot * A.kv_heads + kvh) * PROWS + wrow + m;
@@ -1108,7 +1161,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_prompt(const KvArgs A, con
     }
     return;
   }
-  const int64_t orow = (int64_t)(it.q0 + rows.first + query) * A.q_heads + rhead;
+  const int64_t orow = (int64_t)(it.q0 + rows.first + query) * A.q_heads + head;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
   for (int d = 0; d < DT; d++)
@@ -1339,7 +1392,7 @@ template <int D, bool CAP>
 void launch_attention(const KvArgs& A, const KvPlan& p, const KvPart& dec, const KvPart& pro, hipStream_t s) {
   const unsigned h = (unsigned)A.kv_heads;
   if (p.prompt) {
-    k_kv_prompt<D, CAP><<<(unsigned)p.pro_items * h, KV_THREADS, 0, s>>>(A, pro);
+    k_kv_prompt<D, CAP><<<(unsigned)p.pro_items * h, PTHREADS, 0, s>>>(A, pro);
     k_kv_decode<D, CAP, REQ_SHORT, 2><<<(unsigned)p.dec_items * h, KV_THREADS, 0, s>>>(A, dec);
   } else if (p.nr == 2) {
     k_kv_decode<D, CAP, REQ_ALL, 2><<<(unsigned)p.dec_items * h, KV_THREADS, 0, s>>>(A, dec);
@@ -1386,7 +1439,7 @@ wq_status wq_kv_attention(const void* q_bf16, int64_t q_stride, const int32_t* c
   if (batch == 0 || tokens == 0) return WQ_OK;
   const KvPlan p = kv_plan(batch, tokens, max_q, q_heads, kv_heads, head_dim, page, max_blocks);
   if (ws_bytes < p.bytes || !workspace) return WQ_EINVAL;
-  if ((p.pro_items > p.dec_items ? p.pro_items : p.dec_items) * kv_heads > 0x7FFFFFFF / KV_THREADS) return WQ_EINVAL;
+  if ((p.pro_items > p.dec_items ? p.pro_items : p.dec_items) * kv_heads > 0x7FFFFFFF / PTHREADS) return WQ_EINVAL;
   const KvArgs A = {(const uint16_t*)q_bf16, q_stride, cu_q, kv_lens, batch, tokens, q_heads, kv_heads,
                     q_heads / kv_heads, (int)(window < 0x7FFFFFFF ? window : 0), k_codes, k_scales, v_codes, v_scales, log2_page(page), num_pages, block_table,
                     max_blocks, sm_scale, softcap, out, lse};
