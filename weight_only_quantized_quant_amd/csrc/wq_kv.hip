@@ -899,7 +899,11 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
 // Lane l = 32 h + m.  Within a 32-token half u of the tile, operand row
 // 8 (r / 4) + 4 h + r % 4 is token 32 u + 16 h + r: result register r of lane
 // half h is that token.
-template <int D, bool CAP>
+//
+// BIG: pages of 64 tokens and more, so that a tile lies in one page: its id,
+// scales and addresses are scalars, which takes a fifth of the loop's vector
+// instructions away.
+template <int D, bool CAP, bool BIG>
 __global__ __launch_bounds__(PTHREADS, 2) void k_kv_prompt(const KvArgs A, const KvPart part) {
   constexpr int KS = D / 16, DT = D / 32;     // k steps, channel tiles
   constexpr int XK = D == 128 ? 1 : 2;
@@ -928,7 +932,9 @@ __global__ __launch_bounds__(PTHREADS, 2) void k_kv_prompt(const KvArgs A, const
   const int w_rows = it.rows - wrow < 32 ? it.rows - wrow : 32;
   const int w_min = rows.pos0 + rows.query(A, wrow), w_max = rows.pos0 + rows.query(A, wrow + (w_rows > 0 ? w_rows - 1 : 0));
   const int w_lo_max = kv_lowest(w_max, A.window);
-  const int32_t* tab = A.table + (int64_t)it.request * A.max_blocks;
+  // the table does not change while the kernel runs: scalar loads where the index is uniform
+  const __attribute__((address_space(4))) int32_t* tab =
+      (const __attribute__((address_space(4))) int32_t*)(A.table + (int64_t)it.request * A.max_blocks);
   const int last_col = (int)A.max_blocks - 1;
   const uint32_t head_bytes = (uint32_t)D << A.log_page, page_bytes = head_bytes * A.kv_heads;
   const int in_page = (1 << A.log_page) - 1;
@@ -938,8 +944,9 @@ __global__ __launch_bounds__(PTHREADS, 2) void k_kv_prompt(const KvArgs A, const
   // channel x / 4, tokens 16 (x % 4)..; a thread's pieces are 256 apart, so that
   // they differ by 256 / KS tokens and by 64 channels
   const int ktok = tid / KS, vtok = 16 * (tid & 3);
-  const uint8_t* kbase = A.k_codes + (int64_t)kvh * head_bytes + 16 * (tid % KS);
-  const uint8_t* vbase = A.v_codes + (int64_t)kvh * head_bytes + ((tid >> 2) << A.log_page);
+  const uint8_t* kbase = A.k_codes + (int64_t)kvh * head_bytes;
+  const uint8_t* vbase = A.v_codes + (int64_t)kvh * head_bytes;
+  const uint32_t koff = ktok * D + 16 * (tid % KS), voff = ((tid >> 2) << A.log_page) + vtok;
   uint8_t *kdst[ST], *vdst[ST];
 #pragma unroll
   for (int i = 0; i < ST; i++) {
@@ -953,41 +960,66 @@ __global__ __launch_bounds__(PTHREADS, 2) void k_kv_prompt(const KvArgs A, const
   u32x4_t kr[ST], vr[ST];
   uint32_t ksc[ST], vsc;
   bool vok;
-  int idk[ST], idv;
+  // page ids on their way: of the next K, V^T and, in score layout, the masks;
+  // with BIG pages of tiles t .. t + 4
+  int idk[ST], idv, idm[2], idn[2], ids[5];
   auto page_id = [&](int t, int tok) {        // past t1 the last tile again: loaded, never used
     const int c = ((t < t1 ? t : t1 - 1) * TILE + tok) >> A.log_page;
     return tab[c < last_col ? c : last_col];
   };
+  auto there = [&](int id) { return id >= 0 && id < A.num_pages; };
   auto ids_k = [&](int t) {
+    if constexpr (!BIG) {
 #pragma unroll
-    for (int i = 0; i < ST; i++) idk[i] = page_id(t, ktok + PTHREADS / KS * i);
-  };
-  auto ids_v = [&](int t) { idv = page_id(t, vtok); };
-  int idm[2], idn[2];                         // pages of this lane's scores in tiles t and t + 1
-  auto ids_m = [&](int t) {
-#pragma unroll
-    for (int u = 0; u < 2; u++) idn[u] = page_id(t, 32 * u + 16 * h);
-  };
-  auto load_k = [&](int t) {
-#pragma unroll
-    for (int i = 0; i < ST; i++) {
-      const uint32_t id = idk[i] >= 0 && idk[i] < A.num_pages ? idk[i] : 0;
-      ksc[i] = ksb[(uint64_t)id * (uint32_t)A.kv_heads];
-      kr[i] = ld16(kbase + ((uint64_t)id * page_bytes + ((t * TILE + ktok + PTHREADS / KS * i) & in_page) * D));
+      for (int i = 0; i < ST; i++) idk[i] = page_id(t, ktok + PTHREADS / KS * i);
     }
   };
-  auto load_v = [&](int t) {
-    vok = idv >= 0 && idv < A.num_pages;
-    const uint32_t id = vok ? idv : 0;
-    vsc = vsb[(uint64_t)id * (uint32_t)A.kv_heads];
-    const uint8_t* p = vbase + ((uint64_t)id * page_bytes + ((t * TILE + vtok) & in_page));
+  auto ids_v = [&](int t) {
+    if constexpr (!BIG) idv = page_id(t, vtok);
+  };
+  auto ids_m = [&](int t) {
+    if constexpr (!BIG) {
 #pragma unroll
-    for (int i = 0; i < ST; i++) vr[i] = ld16(p + ((64 * i) << A.log_page));
+      for (int u = 0; u < 2; u++) idn[u] = page_id(t, 32 * u + 16 * h);
+    }
+  };
+  auto load_k = [&](int t, int id) {
+    if constexpr (BIG) {
+      const uint64_t block = (uint64_t)(uint32_t)(there(id) ? id : 0);
+      const uint8_t* p = kbase + (block * page_bytes + (uint32_t)((t * TILE) & in_page) * D);
+      ksc[0] = ksb[block * (uint32_t)A.kv_heads];
+#pragma unroll
+      for (int i = 0; i < ST; i++) kr[i] = ld16(p + (koff + PTHREADS / KS * D * i));
+    } else {
+#pragma unroll
+      for (int i = 0; i < ST; i++) {
+        const uint32_t k = there(idk[i]) ? idk[i] : 0;
+        ksc[i] = ksb[(uint64_t)k * (uint32_t)A.kv_heads];
+        kr[i] = ld16(kbase + ((uint64_t)k * page_bytes + ((t * TILE + ktok + PTHREADS / KS * i) & in_page) * D + 16 * (tid % KS)));
+      }
+    }
+  };
+  auto load_v = [&](int t, int id) {
+    if constexpr (BIG) {
+      vok = there(id);
+      const uint64_t block = (uint64_t)(uint32_t)(vok ? id : 0);
+      const uint8_t* p = vbase + (block * page_bytes + (uint32_t)((t * TILE) & in_page));
+      vsc = vsb[block * (uint32_t)A.kv_heads];
+#pragma unroll
+      for (int i = 0; i < ST; i++) vr[i] = ld16(p + (voff + ((64u * i) << A.log_page)));
+    } else {
+      vok = there(idv);
+      const uint32_t v = vok ? idv : 0;
+      vsc = vsb[(uint64_t)v * (uint32_t)A.kv_heads];
+      const uint8_t* p = vbase + ((uint64_t)v * page_bytes + ((t * TILE + vtok) & in_page) + ((tid >> 2) << A.log_page));
+#pragma unroll
+      for (int i = 0; i < ST; i++) vr[i] = ld16(p + ((64 * i) << A.log_page));
+    }
   };
   auto store_k = [&](int at) {
 #pragma unroll
     for (int i = 0; i < ST; i++) {
-      const float s = e8m0_as_scale(ksc[i]);
+      const float s = e8m0_as_scale(ksc[BIG ? 0 : i]);
       *reinterpret_cast<bf16x8_t*>(kdst[i] + at) = e4m3_bf16x8(kr[i][0], kr[i][1], s);
       *reinterpret_cast<bf16x8_t*>(kdst[i] + at + 32 * 16) = e4m3_bf16x8(kr[i][2], kr[i][3], s);
     }
@@ -1008,16 +1040,22 @@ __global__ __launch_bounds__(PTHREADS, 2) void k_kv_prompt(const KvArgs A, const
     }
   };
   if (t0 < t1) {
+    if constexpr (BIG) {
+#pragma unroll
+      for (int i = 0; i < 5; i++) ids[i] = page_id(t0 + i, 0);
+    }
     ids_k(t0);
     ids_v(t0);
     ids_m(t0);
-    idm[0] = idn[0];
-    idm[1] = idn[1];
-    ids_m(t0 + 1);
-    load_k(t0);
-    load_v(t0);
+    load_k(t0, ids[0]);
+    load_v(t0, ids[0]);
     ids_k(t0 + 1);
     ids_v(t0 + 1);
+    if constexpr (!BIG) {
+      idm[0] = idn[0];
+      idm[1] = idn[1];
+    }
+    ids_m(t0 + 1);
   }
   {
     const uint16_t* qp = A.q + (int64_t)(it.q0 + rows.first + query) * A.q_stride + head * D;
@@ -1060,8 +1098,8 @@ __global__ __launch_bounds__(PTHREADS, 2) void k_kv_prompt(const KvArgs A, const
 #pragma unroll
       for (int i = 0; i < 16; i++) s[i] = sc.cap(s[i]);
     }
-    const bool ok = idm[u] >= 0 && idm[u] < A.num_pages;
-    if (j0 + 31 > w_min || j0 < w_lo_max || __any(!ok)) {
+    const bool ok = there(BIG ? ids[0] : idm[u]);
+    if (j0 + 31 > w_min || j0 < w_lo_max || (BIG ? !ok : __any(!ok))) {
       const int j = j0 + 16 * h, z = ok ? pos - j : -1, b = rlo - j;
 #pragma unroll
       for (int i = 0; i < 16; i++) s[i] = i <= z && i >= b ? s[i] : sc.NONE;
@@ -1069,7 +1107,8 @@ __global__ __launch_bounds__(PTHREADS, 2) void k_kv_prompt(const KvArgs A, const
     float mt = sc.NONE;
 #pragma unroll
     for (int i = 0; i < 16; i++) mt = sc.top(mt, s[i]);
-    mt = __builtin_fmaf(sc.top(mt, __shfl_xor(mt, 32, 64)), sc.mul, sc.add);
+    const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(mt), __float_as_uint(mt), false, false);
+    mt = __builtin_fmaf(sc.top(__uint_as_float(both[0]), __uint_as_float(both[1])), sc.mul, sc.add);
     if (__any(mt > mx + 8.0f)) {
       const float mn = __builtin_fmaxf(mx, mt);
       const float f = mx == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx - mn);
@@ -1106,12 +1145,12 @@ __global__ __launch_bounds__(PTHREADS, 2) void k_kv_prompt(const KvArgs A, const
   if (t0 < t1) {
     store_k(k0);
     store_v(t0, 0);
-    load_k(t0 + 1);
-    load_v(t0 + 1);
+    load_k(t0 + 1, ids[1]);
+    load_v(t0 + 1, ids[1]);
     ids_k(t0 + 2);
     ids_v(t0 + 2);
     store_k(k1);
-    load_k(t0 + 2);
+    load_k(t0 + 2, ids[2]);
     ids_k(t0 + 3);
     tile_barrier();
     if (w_rows > 0) {
@@ -1131,14 +1170,20 @@ __global__ __launch_bounds__(PTHREADS, 2) void k_kv_prompt(const KvArgs A, const
     if (t + 1 == t1) break;
     store_k(k2);
     store_v(t + 1, buf ^ 1);
-    load_k(t + 3);
-    load_v(t + 2);
+    load_k(t + 3, ids[3]);
+    load_v(t + 2, ids[2]);
     ids_k(t + 4);
     ids_v(t + 3);
     tile_barrier();
-    idm[0] = idn[0];
-    idm[1] = idn[1];
-    ids_m(t + 2);
+    if constexpr (BIG) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) ids[i] = ids[i + 1];
+      ids[4] = page_id(t + 5, 0);
+    } else {
+      idm[0] = idn[0];
+      idm[1] = idn[1];
+      ids_m(t + 2);
+    }
     if (w_rows > 0) settle(t + 1, 0, s0);
     const int k = k0;
     k0 = k1;
@@ -1392,7 +1437,9 @@ template <int D, bool CAP>
 void launch_attention(const KvArgs& A, const KvPlan& p, const KvPart& dec, const KvPart& pro, hipStream_t s) {
   const unsigned h = (unsigned)A.kv_heads;
   if (p.prompt) {
-    k_kv_prompt<D, CAP><<<(unsigned)p.pro_items * h, PTHREADS, 0, s>>>(A, pro);
+    const unsigned items = (unsigned)p.pro_items * h;
+    if (A.log_page >= 6) k_kv_prompt<D, CAP, true><<<items, PTHREADS, 0, s>>>(A, pro);
+    else k_kv_prompt<D, CAP, false><<<items, PTHREADS, 0, s>>>(A, pro);
     k_kv_decode<D, CAP, REQ_SHORT, 2><<<(unsigned)p.dec_items * h, KV_THREADS, 0, s>>>(A, dec);
   } else if (p.nr == 2) {
     k_kv_decode<D, CAP, REQ_ALL, 2><<<(unsigned)p.dec_items * h, KV_THREADS, 0, s>>>(A, dec);
