@@ -455,6 +455,7 @@ constexpr int PROWS = 128, PTHREADS = 256;    // rows of a prompt tile, threads 
 // prompts: its tiles of 32 read K and V once each, the prompt kernel once for
 // 128, but a prompt tile's staging and barriers cost the same however few there are.
 constexpr int SHORT_ROWS = 64;
+constexpr int DEC_GROUPS = 512;               // decode workgroups over all heads: two a CU
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 struct KvArgs {
@@ -474,9 +475,10 @@ struct KvArgs {
   float* lse;
 };
 
-// Partial results of split rows: `used[0]` slots are in use; slot s of head h
-// holds rows * D sums and (maximum, sum) pairs.  `rec` names the slot's rows
-// in the entry of the first split, with the number of splits that follow.
+// Partial results of the prompt kernel's split rows: `used[0]` slots are in
+// use; slot s of head h holds PROWS * D sums and (maximum, sum) pairs.  `rec`
+// names the slot's rows in the entry of the first split, with the number of
+// splits that follow.
 struct KvRec {
   int32_t splits;                             // 0 in the entries of the other splits
   int32_t rows, query0, head0;                // the first row: query row of the tensors, head in its group
@@ -487,6 +489,24 @@ struct KvPart {
   int min_tiles;                              // no split is shorter
   int64_t* used;
   KvRec* rec;
+  float* sums;
+  float* stats;
+};
+
+// Partial results of the decode kernel.  Wave x of a head (4 to a workgroup)
+// has two slots: 2 x for a row tile that begins in its share of the work and
+// ends behind it, 2 x + 1 for one that began before.  A workgroup inside one
+// row tile joins its waves first and uses the slots of its first wave alone.
+// chain[x] describes the row tile of slot 2 x; every wave writes its own entry.
+struct KvChain {
+  int32_t rows, query0, head0;                // 0 rows: none
+  int32_t first, last;                        // waves that share the row tile
+  int32_t first_joined, last_joined;          // whether the workgroups of those joined their waves
+  int32_t pad;
+};
+struct KvShare {
+  int groups, rows;                           // workgroups per head, rows of a slot
+  KvChain* chain;
   float* sums;
   float* stats;
 };
@@ -517,18 +537,15 @@ __device__ __forceinline__ int64_t lane64(int64_t v, int src) {
 // Token j is visible to position p when p - window < j <= p.
 __device__ __forceinline__ int kv_lowest(int pos, int window) { return window > 0 && pos >= window ? pos - window + 1 : 0; }
 
-// Every wave finds its item itself, from the lengths: the tiles of all
-// requests are spread evenly over about part.splits items, a request of
-// `tiles` tiles being cut into ceil(tiles / share) splits per row tile.
-// Splits, not tokens, are scanned, so that a long context beside short ones
-// fills the chip as well as equal ones do.  False if there is no such item.
-template <int R, int WHICH>
-__device__ __forceinline__ bool kv_find(const KvArgs& A, const KvPart& part, int64_t item, bool count_all, KvItem& it) {
-  const int lane = threadIdx.x & 63;
-  const int cap = (int)(A.max_blocks << A.log_page);
-  auto request = [&](int64_t i, int& q0, int& n, int& len, int& tiles, int& row_tiles) {
+// Request i (its lengths clamped to what the tensors hold): first query row,
+// queries, tokens, tiles that some query sees, row tiles of R rows.
+struct KvRequest {
+  int q0, n, len, first, tiles, row_tiles;    // first: the first of the tiles
+  template <int R, int WHICH>
+  __device__ __forceinline__ void load(const KvArgs& A, int64_t i) {
     q0 = n = len = 0;
     if (i < A.batch) {
+      const int cap = (int)(A.max_blocks << A.log_page);
       int a = A.cu_q[i], z = A.cu_q[i + 1];
       len = A.kv_lens[i];
       a = a < 0 ? 0 : a;
@@ -540,13 +557,28 @@ __device__ __forceinline__ bool kv_find(const KvArgs& A, const KvPart& part, int
     const int rows = n * A.group;             // below 2^31, as tokens * group is
     if (WHICH == REQ_SHORT ? rows > SHORT_ROWS : WHICH == REQ_LONG ? rows <= SHORT_ROWS : false) n = 0;
     row_tiles = n > 0 ? (int)(((int64_t)rows + R - 1) / R) : 0;
-    tiles = len > 0 ? (len - 1) / TILE - kv_lowest(len - n, A.window) / TILE + 1 : 0;
-  };
-  int q0, n, len, tiles, row_tiles;
+    first = kv_lowest(len - n, A.window) / TILE;
+    tiles = len > 0 ? (len - 1) / TILE - first + 1 : 0;
+  }
+  __device__ __forceinline__ KvRequest from(int src) const {       // another lane's
+    return KvRequest{lane32(q0, src), lane32(n, src), lane32(len, src), lane32(first, src), lane32(tiles, src),
+                     lane32(row_tiles, src)};
+  }
+};
+
+// Every wave finds its item itself, from the lengths: the tiles of all
+// requests are spread evenly over about part.splits items, a request of
+// `tiles` tiles being cut into ceil(tiles / share) splits per row tile.
+// Splits, not tokens, are scanned, so that a long context beside short ones
+// fills the chip as well as equal ones do.  False if there is no such item.
+template <int R, int WHICH>
+__device__ __forceinline__ bool kv_find(const KvArgs& A, const KvPart& part, int64_t item, bool count_all, KvItem& it) {
+  const int lane = threadIdx.x & 63;
+  KvRequest q;
   int64_t total = 0;
   for (int64_t base = 0; base < A.batch; base += 64) {
-    request(base + lane, q0, n, len, tiles, row_tiles);
-    total += (int64_t)tiles * row_tiles;
+    q.load<R, WHICH>(A, base + lane);
+    total += (int64_t)q.tiles * q.row_tiles;
   }
   total = lane64(wave_sum(total), 0);
   int64_t share = (total + part.splits - 1) / part.splits;
@@ -555,9 +587,9 @@ __device__ __forceinline__ bool kv_find(const KvArgs& A, const KvPart& part, int
   int64_t items = 0, slots = 0;
   bool found = false;
   for (int64_t base = 0; base < A.batch; base += 64) {
-    if (A.batch > 64) request(base + lane, q0, n, len, tiles, row_tiles);
-    const int splits = tiles > per ? (int)(((int64_t)tiles + per - 1) / per) : 1;
-    const int64_t own = (int64_t)row_tiles * splits, part_own = splits > 1 ? own : 0;
+    if (A.batch > 64) q.load<R, WHICH>(A, base + lane);
+    const int splits = q.tiles > per ? (int)(((int64_t)q.tiles + per - 1) / per) : 1;
+    const int64_t own = (int64_t)q.row_tiles * splits, part_own = splits > 1 ? own : 0;
     const int64_t end = items + wave_scan(own, lane), part_end = slots + wave_scan(part_own, lane);
     const unsigned long long at = __ballot(end > item);
     if (at && !found) {
@@ -566,10 +598,10 @@ __device__ __forceinline__ bool kv_find(const KvArgs& A, const KvPart& part, int
       it.splits = lane32(splits, src);
       it.split = idx % it.splits;
       it.request = (int)base + src;
-      it.q0 = lane32(q0, src);
-      it.n = lane32(n, src);
-      it.len = lane32(len, src);
-      it.r0 = (lane32(row_tiles, src) - 1 - idx / it.splits) * R;  // the longest rows first
+      it.q0 = lane32(q.q0, src);
+      it.n = lane32(q.n, src);
+      it.len = lane32(q.len, src);
+      it.r0 = (lane32(q.row_tiles, src) - 1 - idx / it.splits) * R;  // the longest rows first
       const int left = it.n * A.group - it.r0;
       it.rows = left < R ? left : R;
       it.slot = lane64(part_end - part_own, src) + idx;
@@ -583,13 +615,13 @@ __device__ __forceinline__ bool kv_find(const KvArgs& A, const KvPart& part, int
   return found;
 }
 
-// Queries of the item's rows: row r0 is query `first` of the request and head
+// Queries of a row tile: row r0 is query `first` of the request and head
 // `head0` of the group; row r0 + i is i rows on.
 struct KvRows {
   int first, head0, pos0;                     // pos0: position of query `first`
-  __device__ __forceinline__ KvRows(const KvArgs& A, const KvItem& it)
-      : first((int)((uint32_t)it.r0 / (uint32_t)A.group)), head0((int)((uint32_t)it.r0 % (uint32_t)A.group)),
-        pos0(it.len - it.n + first) {}
+  __device__ __forceinline__ KvRows(const KvArgs& A, int r0, int n, int len)
+      : first((int)((uint32_t)r0 / (uint32_t)A.group)), head0((int)((uint32_t)r0 % (uint32_t)A.group)),
+        pos0(len - n + first) {}
   __device__ __forceinline__ int query(const KvArgs& A, int i) const { return (int)((uint32_t)(head0 + i) / (uint32_t)A.group); }
   __device__ __forceinline__ int head(const KvArgs& A, int i) const { return (int)((uint32_t)(head0 + i) % (uint32_t)A.group); }
 };
@@ -645,246 +677,343 @@ __device__ __forceinline__ u32x4_t keep_tokens(u32x4_t v, int j, int lo, int hi)
 }
 
 // Decode: 16 or 32 rows (the query heads of a group, for one token or a few
-// drafted ones) per workgroup; its 4 waves take the item's tiles in turn, each
-// with its own running maximum and sums, which are joined in LDS at the end.
-// Bound by the bytes of K and V: they go from HBM straight into the registers
-// that feed v_mfma_f32_16x16x32_bf16, the next tile's K loads leaving as soon
-// as this tile's scores are done and its V loads after its sums, so that a
-// wave always has 8 to 16 KB in flight.
+// drafted ones) per row tile.  Bound by the bytes of K and V: they go from HBM
+// straight into the registers that feed v_mfma_f32_16x16x32_bf16, the next
+// tile's K loads leaving as soon as this tile's scores are done and its V loads
+// after its sums, so that a wave always has 8 to 16 KB in flight.
+//
+// The launch fills the chip once, and the tiles of all row tiles, one after the
+// other, are cut into equal shares, one a wave: no wave waits for another, long
+// contexts and short ones may stand side by side, and the shares differ by
+// one tile at most.  A share that begins or ends inside a row tile leaves
+// partial sums, which k_kv_join puts together; a workgroup whose waves are all
+// inside one row tile joins them in LDS first.  A row tile that sees nothing
+// counts as one tile, so that its rows are written.
 //
 // Lane l = 16 g + m.  K tile a (of 4): operand row m is token
 // 16 (m / 4) + 4 a + m % 4, result rows 4 g + i are then tokens 16 g + 4 a + i.
 template <int D, bool CAP, int WHICH, int NR>
-__global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, const KvPart part) {
+__global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, const KvShare part) {
   constexpr int KP = D / 64, DT = D / 16, R = 16 * NR;
   __shared__ __attribute__((aligned(16))) float so[4][R][D + 4];
   __shared__ float sm[4][R], sl[4][R];
-  const int64_t item = blockIdx.x / (unsigned)A.kv_heads;
-  const int kvh = (int)(blockIdx.x % (unsigned)A.kv_heads);
-  KvItem it;
-  if (!kv_find<R, WHICH>(A, part, item, blockIdx.x == 0, it)) return;
-  if (it.splits > 1 && it.slot >= part.slots) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, g = lane >> 4;
-  const KvRows rows(A, it);
-  int lo, hi, t0, t1;
-  kv_tiles(A, it, rows, lo, hi, t0, t1);
+  const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int group = (int)(blockIdx.x / (unsigned)A.kv_heads), kvh = (int)(blockIdx.x % (unsigned)A.kv_heads);
+  const int x = 4 * group + wave;
+  const KvChain none = {};
 
-  const int32_t* tab = A.table + (int64_t)it.request * A.max_blocks;
+  // all the work, and this wave's share [u0, u1) of it
+  KvRequest lanes;
+  int64_t total = 0;
+  for (int64_t base = 0; base < A.batch; base += 64) {
+    lanes.load<R, WHICH>(A, base + lane);
+    total += (int64_t)(lanes.tiles > 0 ? lanes.tiles : 1) * lanes.row_tiles;
+  }
+  total = lane64(wave_sum(total), 0);
+  const int64_t shares = total < 4 * part.groups ? total : 4 * part.groups;
+  auto share_at = [&](int64_t y) { return y < shares ? y * total / shares : total; };
+  const int64_t u0 = share_at(x), u1 = share_at(x + 1), g0 = share_at(4 * group), g1 = share_at(4 * group + 4);
+  if (g0 >= g1) {                             // an idle workgroup
+    if (kvh == 0 && lane == 0) part.chain[x] = none;
+    return;
+  }
+  // the request that holds unit u, and its first unit
+  KvRequest q = {};
+  int request = 0;
+  int64_t begin = 0;
+  auto find = [&](int64_t u) {
+    int64_t before = 0;
+    for (int64_t base = 0; base < A.batch; base += 64) {
+      if (A.batch > 64) lanes.load<R, WHICH>(A, base + lane);
+      const int64_t own = (int64_t)(lanes.tiles > 0 ? lanes.tiles : 1) * lanes.row_tiles;
+      const int64_t end = before + wave_scan(own, lane);
+      const unsigned long long at = __ballot(end > u);
+      if (at) {
+        const int src = __builtin_ctzll(at);
+        q = lanes.from(src);
+        request = (int)base + src;
+        begin = lane64(end - own, src);
+        return;
+      }
+      before = lane64(end, 63);
+    }
+  };
+  find(g0);
+  auto units = [&]() { return q.tiles > 0 ? q.tiles : 1; };
+  int rt = (int)((g0 - begin) / units());     // row tiles in order of their units, the last rows first
+  const bool joined = g1 <= begin + (int64_t)(rt + 1) * units();
+  if (!joined) {
+    if (u0 >= u1) {
+      if (kvh == 0 && lane == 0) part.chain[x] = none;
+      return;
+    }
+    find(u0);
+    rt = (int)((u0 - begin) / units());
+  }
+  if (q.row_tiles == 0) return;
+
   const int last_col = (int)A.max_blocks - 1;
   const uint32_t head_bytes = (uint32_t)D << A.log_page, page_bytes = head_bytes * A.kv_heads;
   const int in_page = (1 << A.log_page) - 1;
   const uint8_t* kbase = A.k_codes + (int64_t)kvh * head_bytes;
   const uint8_t* vbase = A.v_codes + (int64_t)kvh * head_bytes;
   const uint8_t *ksb = A.k_scales + kvh, *vsb = A.v_scales + kvh;
-
-  u32x4_t kr[4][KP], vr[DT];
-  uint32_t ksc, vsc;
-  bool vok;
-  int idk, idv;                               // page ids of the next tile to load
-  auto load_ids = [&](int t) {
-    const int ck = (t * TILE + 16 * (m >> 2)) >> A.log_page, cv = (t * TILE + 16 * g) >> A.log_page;
-    idk = tab[ck < last_col ? ck : last_col];
-    idv = tab[cv < last_col ? cv : last_col];
-  };
-  auto load_k = [&](int t) {
-    const uint32_t id = idk >= 0 && idk < A.num_pages ? idk : 0;
-    ksc = ksb[(uint64_t)id * (uint32_t)A.kv_heads];
-    const uint8_t* p = kbase + ((uint64_t)id * page_bytes + (((t * TILE + 16 * (m >> 2)) & in_page) + (m & 3)) * D + 16 * g);
-#pragma unroll
-    for (int a = 0; a < 4; a++)
-#pragma unroll
-      for (int h = 0; h < KP; h++) kr[a][h] = ld16(p + 4 * a * D + 64 * h);
-  };
-  auto load_v = [&](int t) {
-    vok = idv >= 0 && idv < A.num_pages;
-    const uint32_t id = vok ? idv : 0;
-    vsc = vsb[(uint64_t)id * (uint32_t)A.kv_heads];
-    const uint8_t* p = vbase + ((uint64_t)id * page_bytes + (m << A.log_page) + ((t * TILE + 16 * g) & in_page));
-#pragma unroll
-    for (int d = 0; d < DT; d++) vr[d] = ld16(p + ((16 * d) << A.log_page));
-  };
-  int t = t0 + wave;
-  if (t < t1) {
-    load_ids(t);
-    load_k(t);
-    load_v(t);
-    if (t + 4 < t1) load_ids(t + 4);
-  }
-
-  // query fragments: columns m of q^T; row m's limits
-  bf16x8_t qf[NR][KP][2];
-  int pos[NR], rlo[NR];
-#pragma unroll
-  for (int c = 0; c < NR; c++) {
-    const bool live = 16 * c + m < it.rows;
-    const int i = live ? 16 * c + m : 0, query = rows.query(A, i);
-    pos[c] = rows.pos0 + query;
-    rlo[c] = kv_lowest(pos[c], A.window);
-    const uint16_t* qp = A.q + (int64_t)(it.q0 + rows.first + query) * A.q_stride + (kvh * A.group + rows.head(A, i)) * D;
-#pragma unroll
-    for (int p = 0; p < KP; p++)
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
-        u32x4_t w = ld16(qp + 64 * p + 16 * g + 8 * h);
-        if (!live) w = u32x4_t{0, 0, 0, 0};
-        qf[c][p][h] = __builtin_bit_cast(bf16x8_t, w);
-      }
-  }
-  const int lo_max = kv_lowest(rows.pos0 + rows.query(A, it.rows - 1), A.window);
-
-  f32x4_t o[NR][DT];
-  float mx[NR], l[NR];
-#pragma unroll
-  for (int c = 0; c < NR; c++) {
-#pragma unroll
-    for (int d = 0; d < DT; d++) o[c][d] = f32x4_t{0, 0, 0, 0};
-    mx[c] = -INFINITY;
-    l[c] = 0.0f;
-  }
   const KvScore<CAP> sc(A);
-  for (; t < t1; t += 4) {
-    const int j0 = t * TILE + 16 * g;         // this lane's 16 tokens in scores and V^T
-    const bool more = t + 4 < t1;
-    f32x4_t s[NR][4];
-    const float ks = e8m0_as_scale(ksc);
-#pragma unroll
-    for (int a = 0; a < 4; a++) {
-#pragma unroll
-      for (int c = 0; c < NR; c++) s[c][a] = f32x4_t{0, 0, 0, 0};
-#pragma unroll
-      for (int p = 0; p < KP; p++) {
-        const u32x4_t w = kr[a][p];
-        const bf16x8_t k0 = e4m3_bf16x8(w[0], w[1], ks), k1 = e4m3_bf16x8(w[2], w[3], ks);
-#pragma unroll
-        for (int c = 0; c < NR; c++) {
-          s[c][a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, qf[c][p][0], s[c][a], 0, 0, 0);
-          s[c][a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, qf[c][p][1], s[c][a], 0, 0, 0);
-        }
-      }
-    }
-    if (more) load_k(t + 4);
-    float vs = e8m0_as_scale(vsc);
-    const bool edge = t * TILE + TILE - 1 > rows.pos0 || t * TILE < lo_max || __any(!vok);
-    if (edge) {                               // bytes of V that no row may see
-      const int a = vok ? lo : 0, z = vok ? hi : 0;
-      if (j0 + 16 <= a || j0 >= z) vs = 1.0f;
-#pragma unroll
-      for (int d = 0; d < DT; d++) vr[d] = keep_tokens(vr[d], j0, a, z);
-    }
-    bf16x8_t p0[NR], p1[NR];
-#pragma unroll
-    for (int c = 0; c < NR; c++) {
-      if constexpr (CAP) {
-#pragma unroll
-        for (int a = 0; a < 4; a++)
-#pragma unroll
-          for (int i = 0; i < 4; i++) s[c][a][i] = sc.cap(s[c][a][i]);
-      }
-      if (edge) {                             // tokens outside the row's limits
-        const int z = vok ? pos[c] - j0 : -1, b = rlo[c] - j0;
-#pragma unroll
-        for (int a = 0; a < 4; a++)
-#pragma unroll
-          for (int i = 0; i < 4; i++) s[c][a][i] = 4 * a + i <= z && 4 * a + i >= b ? s[c][a][i] : sc.NONE;
-      }
-      float mt = sc.NONE;
+  KvChain chain = none;
+
+  for (int64_t u = u0;;) {
+    const int64_t row_begin = begin + (int64_t)rt * units(), row_end = row_begin + units();
+    const int64_t stop = u1 < row_end ? u1 : row_end;
+    const int r0 = (q.row_tiles - 1 - rt) * R;
+    const int n_rows = q.n * A.group - r0 < R ? q.n * A.group - r0 : R;
+    const KvRows rows(A, r0, q.n, q.len);
+    // tokens [lo, hi) that the rows see between them, tiles [t, t1) of this share
+    const int row_max = rows.pos0 + rows.query(A, n_rows - 1);
+    const int hi = row_max < 0 ? 0 : row_max + 1;
+    int lo = kv_lowest(rows.pos0, A.window);
+    lo = lo < hi ? lo : hi;
+    const int lo_max = kv_lowest(row_max, A.window);
+    int t = q.first + (int)(u - row_begin), t1 = q.first + (int)(stop - row_begin);
+    t = t < lo / TILE ? lo / TILE : t;
+    t1 = t1 > (hi + TILE - 1) / TILE ? (hi + TILE - 1) / TILE : t1;
+
+    const int32_t* tab = A.table + (int64_t)request * A.max_blocks;
+    u32x4_t kr[4][KP], vr[DT];
+    uint32_t ksc, vsc;
+    bool vok;
+    int idk, idv;                             // page ids of the next tile to load
+    auto load_ids = [&](int t) {
+      const int ck = (t * TILE + 16 * (m >> 2)) >> A.log_page, cv = (t * TILE + 16 * g) >> A.log_page;
+      idk = tab[ck < last_col ? ck : last_col];
+      idv = tab[cv < last_col ? cv : last_col];
+    };
+    auto load_k = [&](int t) {
+      const uint32_t id = idk >= 0 && idk < A.num_pages ? idk : 0;
+      ksc = ksb[(uint64_t)id * (uint32_t)A.kv_heads];
+      const uint8_t* p = kbase + ((uint64_t)id * page_bytes + (((t * TILE + 16 * (m >> 2)) & in_page) + (m & 3)) * D + 16 * g);
 #pragma unroll
       for (int a = 0; a < 4; a++)
 #pragma unroll
-        for (int i = 0; i < 4; i++) mt = sc.top(mt, s[c][a][i]);
-      mt = sc.top(mt, __shfl_xor(mt, 16, 64));
-      mt = __builtin_fmaf(sc.top(mt, __shfl_xor(mt, 32, 64)), sc.mul, sc.add);
-      if (__any(mt > mx[c] + 8.0f)) {
-        const float mn = __builtin_fmaxf(mx[c], mt);
-        const float f = mx[c] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx[c] - mn);
-        mx[c] = mn;
-        l[c] *= f;
+        for (int h = 0; h < KP; h++) kr[a][h] = ld16(p + 4 * a * D + 64 * h);
+    };
+    auto load_v = [&](int t) {
+      vok = idv >= 0 && idv < A.num_pages;
+      const uint32_t id = vok ? idv : 0;
+      vsc = vsb[(uint64_t)id * (uint32_t)A.kv_heads];
+      const uint8_t* p = vbase + ((uint64_t)id * page_bytes + (m << A.log_page) + ((t * TILE + 16 * g) & in_page));
 #pragma unroll
-        for (int d = 0; d < DT; d++) o[c][d] *= f;
-      }
-      const float off = sc.add - (mx[c] == -INFINITY ? 0.0f : mx[c]);
-      uint32_t pw[8];
+      for (int d = 0; d < DT; d++) vr[d] = ld16(p + ((16 * d) << A.log_page));
+    };
+    if (t < t1) {
+      load_ids(t);
+      load_k(t);
+      load_v(t);
+      if (t + 1 < t1) load_ids(t + 1);
+    }
+
+    // query fragments: columns m of q^T; row m's limits
+    bf16x8_t qf[NR][KP][2];
+    int pos[NR], rlo[NR];
+#pragma unroll
+    for (int c = 0; c < NR; c++) {
+      const bool live = 16 * c + m < n_rows;
+      const int i = live ? 16 * c + m : 0, query = rows.query(A, i);
+      pos[c] = rows.pos0 + query;
+      rlo[c] = kv_lowest(pos[c], A.window);
+      const uint16_t* qp = A.q + (int64_t)(q.q0 + rows.first + query) * A.q_stride + (kvh * A.group + rows.head(A, i)) * D;
+#pragma unroll
+      for (int p = 0; p < KP; p++)
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          u32x4_t w = ld16(qp + 64 * p + 16 * g + 8 * h);
+          if (!live) w = u32x4_t{0, 0, 0, 0};
+          qf[c][p][h] = __builtin_bit_cast(bf16x8_t, w);
+        }
+    }
+
+    f32x4_t o[NR][DT];
+    float mx[NR], l[NR];
+#pragma unroll
+    for (int c = 0; c < NR; c++) {
+#pragma unroll
+      for (int d = 0; d < DT; d++) o[c][d] = f32x4_t{0, 0, 0, 0};
+      mx[c] = -INFINITY;
+      l[c] = 0.0f;
+    }
+    for (; t < t1; t++) {
+      const int j0 = t * TILE + 16 * g;       // this lane's 16 tokens in scores and V^T
+      const bool more = t + 1 < t1;
+      f32x4_t s[NR][4];
+      const float ks = e8m0_as_scale(ksc);
 #pragma unroll
       for (int a = 0; a < 4; a++) {
-        float p[4];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[c][a][i], sc.mul, off));
-          l[c] += p[i];
+        for (int c = 0; c < NR; c++) s[c][a] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int p = 0; p < KP; p++) {
+          const u32x4_t w = kr[a][p];
+          const bf16x8_t k0 = e4m3_bf16x8(w[0], w[1], ks), k1 = e4m3_bf16x8(w[2], w[3], ks);
+#pragma unroll
+          for (int c = 0; c < NR; c++) {
+            s[c][a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, qf[c][p][0], s[c][a], 0, 0, 0);
+            s[c][a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, qf[c][p][1], s[c][a], 0, 0, 0);
+          }
         }
-        // bf16 for the matrix cores: half a step of 2^-8 per probability, the sum l keeps fp32
-        pw[2 * a] = pack_bf16x2(p[0], p[1]);
-        pw[2 * a + 1] = pack_bf16x2(p[2], p[3]);
       }
-      p0[c] = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[0], pw[1], pw[2], pw[3]}));
-      p1[c] = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[4], pw[5], pw[6], pw[7]}));
-    }
+      if (more) load_k(t + 1);
+      float vs = e8m0_as_scale(vsc);
+      const bool edge = t * TILE + TILE - 1 > rows.pos0 || t * TILE < lo_max || __any(!vok);
+      if (edge) {                             // bytes of V that no row may see
+        const int a = vok ? lo : 0, z = vok ? hi : 0;
+        if (j0 + 16 <= a || j0 >= z) vs = 1.0f;
 #pragma unroll
-    for (int d = 0; d < DT; d++) {
-      const bf16x8_t v0 = e4m3_bf16x8(vr[d][0], vr[d][1], vs), v1 = e4m3_bf16x8(vr[d][2], vr[d][3], vs);
+        for (int d = 0; d < DT; d++) vr[d] = keep_tokens(vr[d], j0, a, z);
+      }
+      bf16x8_t p0[NR], p1[NR];
 #pragma unroll
       for (int c = 0; c < NR; c++) {
-        o[c][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, p0[c], o[c][d], 0, 0, 0);
-        o[c][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, p1[c], o[c][d], 0, 0, 0);
+        if constexpr (CAP) {
+#pragma unroll
+          for (int a = 0; a < 4; a++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) s[c][a][i] = sc.cap(s[c][a][i]);
+        }
+        if (edge) {                           // tokens outside the row's limits
+          const int z = vok ? pos[c] - j0 : -1, b = rlo[c] - j0;
+#pragma unroll
+          for (int a = 0; a < 4; a++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) s[c][a][i] = 4 * a + i <= z && 4 * a + i >= b ? s[c][a][i] : sc.NONE;
+        }
+        float mt = sc.NONE;
+#pragma unroll
+        for (int a = 0; a < 4; a++)
+#pragma unroll
+          for (int i = 0; i < 4; i++) mt = sc.top(mt, s[c][a][i]);
+        mt = sc.top(mt, __shfl_xor(mt, 16, 64));
+        mt = __builtin_fmaf(sc.top(mt, __shfl_xor(mt, 32, 64)), sc.mul, sc.add);
+        if (__any(mt > mx[c] + 8.0f)) {       // only past 2^8: the sums hold that, and the result is the same
+          const float mn = __builtin_fmaxf(mx[c], mt);
+          const float f = mx[c] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx[c] - mn);
+          mx[c] = mn;
+          l[c] *= f;
+#pragma unroll
+          for (int d = 0; d < DT; d++) o[c][d] *= f;
+        }
+        const float off = sc.add - (mx[c] == -INFINITY ? 0.0f : mx[c]);
+        uint32_t pw[8];
+#pragma unroll
+        for (int a = 0; a < 4; a++) {
+          float p[4];
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[c][a][i], sc.mul, off));
+            l[c] += p[i];
+          }
+          // bf16 for the matrix cores: half a step of 2^-8 per probability, the sum l keeps fp32
+          pw[2 * a] = pack_bf16x2(p[0], p[1]);
+          pw[2 * a + 1] = pack_bf16x2(p[2], p[3]);
+        }
+        p0[c] = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[0], pw[1], pw[2], pw[3]}));
+        p1[c] = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[4], pw[5], pw[6], pw[7]}));
+      }
+#pragma unroll
+      for (int d = 0; d < DT; d++) {
+        const bf16x8_t v0 = e4m3_bf16x8(vr[d][0], vr[d][1], vs), v1 = e4m3_bf16x8(vr[d][2], vr[d][3], vs);
+#pragma unroll
+        for (int c = 0; c < NR; c++) {
+          o[c][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, p0[c], o[c][d], 0, 0, 0);
+          o[c][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, p1[c], o[c][d], 0, 0, 0);
+        }
+      }
+      if (more) {
+        load_v(t + 1);
+        if (t + 2 < t1) load_ids(t + 2);
       }
     }
-    if (more) {
-      load_v(t + 4);
-      if (t + 8 < t1) load_ids(t + 8);
-    }
-  }
 #pragma unroll
-  for (int c = 0; c < NR; c++) {
-    l[c] += __shfl_xor(l[c], 16, 64);
-    l[c] += __shfl_xor(l[c], 32, 64);
-    if (g == 0) {
-      sm[wave][16 * c + m] = mx[c];
-      sl[wave][16 * c + m] = l[c];
+    for (int c = 0; c < NR; c++) {
+      l[c] += __shfl_xor(l[c], 16, 64);
+      l[c] += __shfl_xor(l[c], 32, 64);
     }
-#pragma unroll
-    for (int d = 0; d < DT; d++) *reinterpret_cast<f32x4_t*>(&so[wave][16 * c + m][16 * d + 4 * g]) = o[c][d];
-  }
-  __syncthreads();
 
-  // join the waves: thread (row, channels)
-  constexpr int CH = D / 16;
-  const int ch = (tid % 16) * CH;
-  if (it.splits > 1 && tid == 0 && kvh == 0)
-    part.rec[it.slot] = KvRec{it.split ? 0 : it.splits, it.rows, it.q0 + rows.first, rows.head0};
-  for (int row = tid / 16; row < it.rows; row += 16) {
-    float M = sm[0][row];
-#pragma unroll
-    for (int w = 1; w < 4; w++) M = __builtin_fmaxf(M, sm[w][row]);
-    float L = 0.0f, acc[CH];
-#pragma unroll
-    for (int i = 0; i < CH; i++) acc[i] = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 4; w++) {
-      const float f = sm[w][row] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(sm[w][row] - M);
-      L += f * sl[w][row];
-#pragma unroll
-      for (int i = 0; i < CH; i++) acc[i] = __builtin_fmaf(f, so[w][row][ch + i], acc[i]);
+    // this wave, or the workgroup, has units [from, to) of the row tile's
+    const int64_t from = joined ? g0 : u, to = joined ? g1 : stop;
+    const bool whole = from == row_begin && to == row_end;
+    const int slot = 2 * (joined ? 4 * group : x) + (from == row_begin ? 0 : 1);
+    if (from == row_begin && !whole && (!joined || wave == 0)) {
+      // the last wave: the one whose share holds unit row_end - 1
+      const int64_t last = (row_end * shares - 1) / total;
+      chain = KvChain{n_rows, q.q0 + rows.first, rows.head0, joined ? 4 * group : x, (int)last, joined,
+                      share_at((last | 3) + 1) <= row_end, 0};
     }
-    if (it.splits > 1) {
-      const int64_t at = (it.slot * A.kv_heads + kvh) * R + row;
+    auto put = [&](int row, int ch, const f32x4_t& v, float top, float sum) {      // 4 channels of a row
+      if (!whole) {
+        const int64_t at = ((int64_t)slot * A.kv_heads + kvh) * part.rows + row;
+        *reinterpret_cast<f32x4_t*>(part.sums + at * D + ch) = v;
+        if (ch == 0) {
+          part.stats[2 * at] = top;
+          part.stats[2 * at + 1] = sum;
+        }
+        return;
+      }
+      const int64_t orow = (int64_t)(q.q0 + rows.first + rows.query(A, row)) * A.q_heads + kvh * A.group + rows.head(A, row);
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      *reinterpret_cast<u32x2_t*>(A.out + orow * D + ch) =
+          u32x2_t{pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv)};
+      if (A.lse && ch == 0) A.lse[orow] = sum == 0.0f ? -INFINITY : (top + __builtin_log2f(sum)) * LN2;
+    };
+    if (!joined) {
 #pragma unroll
-      for (int i = 0; i < CH; i += 4)
-        *reinterpret_cast<f32x4_t*>(part.sums + at * D + ch + i) = f32x4_t{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
-      if (ch == 0) {
-        part.stats[2 * at] = M;
-        part.stats[2 * at + 1] = L;
+      for (int c = 0; c < NR; c++)
+        if (16 * c + m < n_rows) {
+#pragma unroll
+          for (int d = 0; d < DT; d++) put(16 * c + m, 16 * d + 4 * g, o[c][d], mx[c], l[c]);
+        }
+      u = stop;
+      if (u >= u1) break;
+      if (++rt == q.row_tiles) {              // on to the next request that has rows
+        begin = row_end;
+        rt = 0;
+        do {
+          request++;
+          q.load<R, WHICH>(A, request);
+          q = q.from(0);
+        } while (q.row_tiles == 0 && request < A.batch);
+        if (q.row_tiles == 0) break;
       }
       continue;
     }
-    const int64_t orow = (int64_t)(it.q0 + rows.first + rows.query(A, row)) * A.q_heads + kvh * A.group + rows.head(A, row);
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-    uint32_t w[CH / 2];
 #pragma unroll
-    for (int i = 0; i < CH / 2; i++) w[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-    if constexpr (CH == 8) *reinterpret_cast<u32x4_t*>(A.out + orow * D + ch) = u32x4_t{w[0], w[1], w[2], w[3]};
-    else *reinterpret_cast<u32x2_t*>(A.out + orow * D + ch) = u32x2_t{w[0], w[1]};
-    if (A.lse && ch == 0) A.lse[orow] = L == 0.0f ? -INFINITY : (M + __builtin_log2f(L)) * LN2;
+    for (int c = 0; c < NR; c++) {
+      if (g == 0) {
+        sm[wave][16 * c + m] = mx[c];
+        sl[wave][16 * c + m] = l[c];
+      }
+#pragma unroll
+      for (int d = 0; d < DT; d++) *reinterpret_cast<f32x4_t*>(&so[wave][16 * c + m][16 * d + 4 * g]) = o[c][d];
+    }
+    __syncthreads();
+    for (int i = tid; i < n_rows * (D / 4); i += KV_THREADS) {
+      const int row = i / (D / 4), ch = i % (D / 4) * 4;
+      float top = sm[0][row], sum = 0.0f;
+#pragma unroll
+      for (int w = 1; w < 4; w++) top = __builtin_fmaxf(top, sm[w][row]);
+      f32x4_t acc = {0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < 4; w++) {
+        const float f = sm[w][row] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(sm[w][row] - top);
+        sum = __builtin_fmaf(f, sl[w][row], sum);
+        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(&so[w][row][ch]);
+#pragma unroll
+        for (int e = 0; e < 4; e++) acc[e] = __builtin_fmaf(f, v[e], acc[e]);
+      }
+      put(row, ch, acc, top, sum);
+    }
+    break;
   }
+  if (kvh == 0 && lane == 0) part.chain[x] = chain;
 }
 
 // Prompts and chunks: 128 rows per workgroup, 32 per wave.  Bound by the
@@ -916,7 +1045,7 @@ __global__ __launch_bounds__(PTHREADS, 2) void k_kv_prompt(const KvArgs A, const
   if (it.splits > 1 && it.slot >= part.slots) return;
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const KvRows rows(A, it);
+  const KvRows rows(A, it.r0, it.n, it.len);
   int lo, hi, t0, t1;
   kv_tiles(A, it, rows, lo, hi, t0, t1);
   const bool split = it.splits > 1;
@@ -1218,33 +1347,30 @@ __global__ __launch_bounds__(PTHREADS, 2) void k_kv_prompt(const KvArgs A, const
   if (A.lse && h == 0) A.lse[orow] = l == 0.0f ? -INFINITY : (mx + __builtin_log2f(l)) * LN2;
 }
 
-// Joins the splits of 16 rows of one head, a wave taking every fourth row: its
-// lanes hold 4 channels each, and the groups of lanes that this leaves share
-// the splits, 4 of them in flight per lane, since a long context alone in its
-// batch has a hundred splits of few rows.
-template <int D, int R>
-__device__ __forceinline__ void kv_join(const KvArgs& A, const KvPart& part, int64_t slot, int sub, int kvh) {
-  if (slot >= part.used[0]) return;
-  const KvRec rec = part.rec[slot];
-  if (rec.splits == 0 || slot + rec.splits > part.slots) return;
+// Joins `parts` partial results of rows [row0, row0 + 16) of one head, a wave
+// taking every fourth row: its lanes hold 4 channels each, and the groups of
+// lanes that this leaves share the parts, 4 of them in flight per lane, since a
+// long context alone in its batch has many parts of few rows.  slot_of(i) is
+// the place of part i among the slots of `room` rows.
+template <int D, typename SLOT>
+__device__ __forceinline__ void kv_join(const KvArgs& A, const float* sums, const float* stats, int room, int kvh,
+                                        int row0, int rows, int query0, int head0, int parts, SLOT slot_of) {
   constexpr int LANES = D / 4, GROUPS = 64 / LANES, DEEP = 4;
   const int lane = threadIdx.x & 63, grp = lane / LANES, ch = (lane % LANES) * 4;
-  const int64_t step = (int64_t)A.kv_heads * R;
-  for (int row = sub * 16 + threadIdx.x / 64; row < sub * 16 + 16 && row < rec.rows; row += KV_THREADS / 64) {
-    const int64_t at = (slot * A.kv_heads + kvh) * R + row;
+  for (int row = row0 + threadIdx.x / 64; row < row0 + 16 && row < rows; row += KV_THREADS / 64) {
     float M = -INFINITY, L = 0.0f;
     f32x4_t acc = {0, 0, 0, 0};
-    for (int s0 = grp; s0 < rec.splits; s0 += GROUPS * DEEP) {
+    for (int s0 = grp; s0 < parts; s0 += GROUPS * DEEP) {
       float ms[DEEP], ls[DEEP], top = M;
       f32x4_t v[DEEP];
 #pragma unroll
       for (int u = 0; u < DEEP; u++) {
         const int sp = s0 + GROUPS * u;
-        const int64_t a = at + (sp < rec.splits ? sp : s0) * step;
-        ms[u] = part.stats[2 * a];
-        ls[u] = part.stats[2 * a + 1];
-        v[u] = *reinterpret_cast<const f32x4_t*>(part.sums + a * D + ch);
-        if (sp >= rec.splits) ms[u] = -INFINITY;
+        const int64_t a = (slot_of(sp < parts ? sp : s0) * A.kv_heads + kvh) * room + row;
+        ms[u] = stats[2 * a];
+        ls[u] = stats[2 * a + 1];
+        v[u] = *reinterpret_cast<const f32x4_t*>(sums + a * D + ch);
+        if (sp >= parts) ms[u] = -INFINITY;
         top = __builtin_fmaxf(top, ms[u]);
       }
       const float keep = M == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(M - top);
@@ -1270,8 +1396,8 @@ __device__ __forceinline__ void kv_join(const KvArgs& A, const KvPart& part, int
       M = top;
     }
     if (grp == 0) {
-      const uint32_t rr = rec.head0 + row, group = A.group;
-      const int64_t orow = (int64_t)(rec.query0 + rr / group) * A.q_heads + kvh * group + rr % group;
+      const uint32_t rr = head0 + row, group = A.group;
+      const int64_t orow = (int64_t)(query0 + rr / group) * A.q_heads + kvh * group + rr % group;
       const float inv = L == 0.0f ? 0.0f : 1.0f / L;
       *reinterpret_cast<u32x2_t*>(A.out + orow * D + ch) =
           u32x2_t{pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv)};
@@ -1280,14 +1406,34 @@ __device__ __forceinline__ void kv_join(const KvArgs& A, const KvPart& part, int
   }
 }
 
-// Workgroups of the decode slots first (NR each), then PROWS / 16 for each prompt slot.
+// Workgroups of the decode kernel's waves first (NR each), then PROWS / 16 for
+// each prompt slot.
 template <int D, int NR>
-__global__ __launch_bounds__(KV_THREADS) void k_kv_join(const KvArgs A, const KvPart dec, const KvPart pro,
-                                                        int64_t dec_slots) {
+__global__ __launch_bounds__(KV_THREADS) void k_kv_join(const KvArgs A, const KvShare dec, const KvPart pro) {
   const int kvh = (int)(blockIdx.x % (unsigned)A.kv_heads);
-  const int64_t x = blockIdx.x / (unsigned)A.kv_heads;
-  if (x < dec_slots * NR) kv_join<D, 16 * NR>(A, dec, x / NR, (int)(x % NR), kvh);
-  else kv_join<D, PROWS>(A, pro, (x - dec_slots * NR) / (PROWS / 16), (int)((x - dec_slots * NR) % (PROWS / 16)), kvh);
+  int64_t x = blockIdx.x / (unsigned)A.kv_heads;
+  const int64_t waves = 4 * (int64_t)dec.groups;
+  if (x < waves * NR) {
+    const KvChain c = dec.chain[x / NR];
+    if (c.rows == 0) return;
+    // parts: the first workgroup's, one for each between, the last workgroup's
+    const int ga = c.first / 4, gz = c.last / 4;
+    const int a = c.first_joined ? 1 : (gz > ga ? 4 * ga + 3 : c.last) - c.first + 1;
+    const int mid = gz > ga ? gz - ga - 1 : 0, z = gz > ga ? (c.last_joined ? 1 : c.last - 4 * gz + 1) : 0;
+    kv_join<D>(A, dec.sums, dec.stats, dec.rows, kvh, (int)(x % NR) * 16, c.rows, c.query0, c.head0, a + mid + z,
+               [&](int i) -> int64_t {
+                 if (i < a) return i == 0 ? 2 * c.first : 2 * (c.first + i) + 1;
+                 return i < a + mid ? 8 * (ga + 1 + i - a) + 1 : 2 * (4 * gz + i - a - mid) + 1;
+               });
+    return;
+  }
+  x -= waves * NR;
+  const int64_t slot = x / (PROWS / 16);
+  if (slot >= pro.used[0]) return;
+  const KvRec rec = pro.rec[slot];
+  if (rec.splits == 0 || slot + rec.splits > pro.slots) return;
+  kv_join<D>(A, pro.sums, pro.stats, PROWS, kvh, (int)(x % (PROWS / 16)) * 16, rec.rows, rec.query0, rec.head0, rec.splits,
+             [&](int i) -> int64_t { return slot + i; });
 }
 
 int log2_page(int page) {
@@ -1371,18 +1517,22 @@ wq_status wq_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v
 
 namespace {
 
-// Splits aimed at, over all key/value heads, and the fewest tiles of a split.
-constexpr int64_t DEC_ITEMS = 1024, PRO_ITEMS = 512;
-constexpr int DEC_MIN = 4, PRO_MIN = 4;
+// Items aimed at for prompts, over all key/value heads, and the fewest tiles
+// of a split.
+constexpr int64_t PRO_ITEMS = 512;
+constexpr int PRO_MIN = 4;
 
-// What a call launches and where its workspace lies.  Items per head are at
-// most splits + row tiles; slots (items of requests with two splits or more)
-// at most 2 * splits, and no more than the tiles of the table's width allow.
+// What a call launches and where its workspace lies.  Prompt items per head are
+// at most splits + row tiles; slots (items of requests with two splits or
+// more) at most 2 * splits, and no more than the tiles of the table's width
+// allow.  The decode kernel has as many workgroups as the chip holds at once
+// (two a CU, as its registers allow), or one a head.
 struct KvPlan {
-  bool prompt, join;
+  bool prompt;
   int nr;                                     // 16-row columns of a decode tile
-  int64_t dec_splits, dec_items, dec_slots, pro_splits, pro_items, pro_slots;
-  size_t dec_rec, dec_sums, dec_stats, pro_used, pro_rec, pro_sums, pro_stats, bytes;
+  int groups, rows;                           // decode workgroups per head, rows of its slots
+  int64_t pro_splits, pro_items, pro_slots;
+  size_t dec_sums, dec_stats, pro_used, pro_rec, pro_sums, pro_stats, bytes;
 };
 
 KvPlan kv_plan(int64_t batch, int64_t tokens, int64_t max_q, int q_heads, int kv_heads, int head_dim, int page,
@@ -1393,31 +1543,26 @@ KvPlan kv_plan(int64_t batch, int64_t tokens, int64_t max_q, int q_heads, int kv
   const int64_t most_q = max_q > 0 && max_q < tokens ? max_q : tokens;
   p.prompt = most_q * group > SHORT_ROWS;
   p.nr = most_q * group <= 16 ? 1 : 2;
-  const int drows = 16 * p.nr;
-  p.dec_splits = (DEC_ITEMS + kv_heads - 1) / kv_heads;
+  const int64_t wgs = DEC_GROUPS / kv_heads;
+  p.groups = (int)(wgs > 1 ? wgs : 1);
+  p.rows = 16 * p.nr;
   p.pro_splits = (PRO_ITEMS + kv_heads - 1) / kv_heads;
-  const int64_t dec_rows = (p.prompt ? (reqs < tokens * group / drows ? reqs : tokens * group / drows) : tokens * group / drows) + reqs;
   const int64_t pro_rows = p.prompt ? tokens * group / PROWS + reqs : 0;
-  p.dec_items = dec_rows + p.dec_splits;
   p.pro_items = p.prompt ? pro_rows + p.pro_splits : 0;
-  auto slots = [&](int64_t rows, int64_t splits, int min_tiles) {
-    if (tiles <= min_tiles) return (int64_t)0;
-    const int64_t most = (tiles + min_tiles - 1) / min_tiles;
-    return rows > 2 * splits / most ? 2 * splits : rows * most;
-  };
-  p.dec_slots = slots(dec_rows, p.dec_splits, DEC_MIN);
-  p.pro_slots = p.prompt ? slots(pro_rows, p.pro_splits, PRO_MIN) : 0;
-  p.join = p.dec_slots + p.pro_slots > 0;
+  if (p.prompt && tiles > PRO_MIN) {
+    const int64_t most = (tiles + PRO_MIN - 1) / PRO_MIN;
+    p.pro_slots = pro_rows > 2 * p.pro_splits / most ? 2 * p.pro_splits : pro_rows * most;
+  }
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t a = at;
     at += (n + 255) & ~(size_t)255;
     return a;
   };
-  take(8);
-  p.dec_rec = take(p.dec_slots * sizeof(KvRec));
-  p.dec_sums = take((size_t)p.dec_slots * kv_heads * drows * head_dim * 4);
-  p.dec_stats = take((size_t)p.dec_slots * kv_heads * drows * 8);
+  const size_t slots = 8 * (size_t)p.groups * kv_heads * p.rows;
+  take(4 * (size_t)p.groups * sizeof(KvChain));
+  p.dec_sums = take(slots * head_dim * 4);
+  p.dec_stats = take(slots * 8);
   p.pro_used = take(8);
   p.pro_rec = take(p.pro_slots * sizeof(KvRec));
   p.pro_sums = take((size_t)p.pro_slots * kv_heads * PROWS * head_dim * 4);
@@ -1434,22 +1579,21 @@ bool kv_sizes_ok(int64_t batch, int64_t tokens, int64_t max_q, int32_t q_heads, 
 }
 
 template <int D, bool CAP>
-void launch_attention(const KvArgs& A, const KvPlan& p, const KvPart& dec, const KvPart& pro, hipStream_t s) {
-  const unsigned h = (unsigned)A.kv_heads;
+void launch_attention(const KvArgs& A, const KvPlan& p, const KvShare& dec, const KvPart& pro, hipStream_t s) {
+  const unsigned h = (unsigned)A.kv_heads, groups = (unsigned)p.groups * h;
   if (p.prompt) {
     const unsigned items = (unsigned)p.pro_items * h;
     if (A.log_page >= 6) k_kv_prompt<D, CAP, true><<<items, PTHREADS, 0, s>>>(A, pro);
     else k_kv_prompt<D, CAP, false><<<items, PTHREADS, 0, s>>>(A, pro);
-    k_kv_decode<D, CAP, REQ_SHORT, 2><<<(unsigned)p.dec_items * h, KV_THREADS, 0, s>>>(A, dec);
+    k_kv_decode<D, CAP, REQ_SHORT, 2><<<groups, KV_THREADS, 0, s>>>(A, dec);
   } else if (p.nr == 2) {
-    k_kv_decode<D, CAP, REQ_ALL, 2><<<(unsigned)p.dec_items * h, KV_THREADS, 0, s>>>(A, dec);
+    k_kv_decode<D, CAP, REQ_ALL, 2><<<groups, KV_THREADS, 0, s>>>(A, dec);
   } else {
-    k_kv_decode<D, CAP, REQ_ALL, 1><<<(unsigned)p.dec_items * h, KV_THREADS, 0, s>>>(A, dec);
+    k_kv_decode<D, CAP, REQ_ALL, 1><<<groups, KV_THREADS, 0, s>>>(A, dec);
   }
-  if (!p.join) return;
-  const unsigned groups = (unsigned)((p.dec_slots * p.nr + p.pro_slots * (PROWS / 16)) * h);
-  if (p.nr == 2) k_kv_join<D, 2><<<groups, KV_THREADS, 0, s>>>(A, dec, pro, p.dec_slots);
-  else k_kv_join<D, 1><<<groups, KV_THREADS, 0, s>>>(A, dec, pro, p.dec_slots);
+  const unsigned joins = 4 * groups * p.nr + (unsigned)(p.pro_slots * (PROWS / 16)) * h;
+  if (p.nr == 2) k_kv_join<D, 2><<<joins, KV_THREADS, 0, s>>>(A, dec, pro);
+  else k_kv_join<D, 1><<<joins, KV_THREADS, 0, s>>>(A, dec, pro);
 }
 
 }  // namespace
@@ -1486,13 +1630,12 @@ wq_status wq_kv_attention(const void* q_bf16, int64_t q_stride, const int32_t* c
   if (batch == 0 || tokens == 0) return WQ_OK;
   const KvPlan p = kv_plan(batch, tokens, max_q, q_heads, kv_heads, head_dim, page, max_blocks);
   if (ws_bytes < p.bytes || !workspace) return WQ_EINVAL;
-  if ((p.pro_items > p.dec_items ? p.pro_items : p.dec_items) * kv_heads > 0x7FFFFFFF / PTHREADS) return WQ_EINVAL;
+  if (p.pro_items * kv_heads > 0x7FFFFFFF / PTHREADS) return WQ_EINVAL;
   const KvArgs A = {(const uint16_t*)q_bf16, q_stride, cu_q, kv_lens, batch, tokens, q_heads, kv_heads,
                     q_heads / kv_heads, (int)(window < 0x7FFFFFFF ? window : 0), k_codes, k_scales, v_codes, v_scales, log2_page(page), num_pages, block_table,
                     max_blocks, sm_scale, softcap, out, lse};
   uint8_t* ws = (uint8_t*)workspace;
-  const KvPart dec = {p.dec_splits, p.dec_slots, DEC_MIN, (int64_t*)ws, (KvRec*)(ws + p.dec_rec), (float*)(ws + p.dec_sums),
-                      (float*)(ws + p.dec_stats)};
+  const KvShare dec = {p.groups, p.rows, (KvChain*)ws, (float*)(ws + p.dec_sums), (float*)(ws + p.dec_stats)};
   const KvPart pro = {p.pro_splits, p.pro_slots, PRO_MIN, (int64_t*)(ws + p.pro_used), (KvRec*)(ws + p.pro_rec),
                       (float*)(ws + p.pro_sums), (float*)(ws + p.pro_stats)};
   hipStream_t s = (hipStream_t)stream;
