@@ -568,7 +568,8 @@ struct KvRequest {
 
 // Every wave finds its item itself, from the lengths: the tiles of all
 // requests are spread evenly over about part.splits items, a request of
-// `tiles` tiles being cut into ceil(tiles / share) splits per row tile.
+// `tiles` tiles being cut into tiles / share splits per row tile, to the
+// nearest (rounding up costs more in partial sums than it evens out).
 // Splits, not tokens, are scanned, so that a long context beside short ones
 // fills the chip as well as equal ones do.  False if there is no such item.
 template <int R, int WHICH>
@@ -588,7 +589,7 @@ __device__ __forceinline__ bool kv_find(const KvArgs& A, const KvPart& part, int
   bool found = false;
   for (int64_t base = 0; base < A.batch; base += 64) {
     if (A.batch > 64) q.load<R, WHICH>(A, base + lane);
-    const int splits = q.tiles > per ? (int)(((int64_t)q.tiles + per - 1) / per) : 1;
+    const int rounded = (int)((2 * (int64_t)q.tiles + per) / (2 * (int64_t)per)), splits = rounded > 1 ? rounded : 1;
     const int64_t own = (int64_t)q.row_tiles * splits, part_own = splits > 1 ? own : 0;
     const int64_t end = items + wave_scan(own, lane), part_end = slots + wave_scan(part_own, lane);
     const unsigned long long at = __ballot(end > item);
@@ -765,6 +766,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
   for (int64_t u = u0;;) {
     const int64_t row_begin = begin + (int64_t)rt * units(), row_end = row_begin + units();
     const int64_t stop = u1 < row_end ? u1 : row_end;
+    const int step = joined ? 4 : 1;          // the waves of a joined workgroup take its tiles in turn
     const int r0 = (q.row_tiles - 1 - rt) * R;
     const int n_rows = q.n * A.group - r0 < R ? q.n * A.group - r0 : R;
     const KvRows rows(A, r0, q.n, q.len);
@@ -774,9 +776,10 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
     int lo = kv_lowest(rows.pos0, A.window);
     lo = lo < hi ? lo : hi;
     const int lo_max = kv_lowest(row_max, A.window);
-    int t = q.first + (int)(u - row_begin), t1 = q.first + (int)(stop - row_begin);
+    int t = q.first + (int)((joined ? g0 : u) - row_begin), t1 = q.first + (int)((joined ? g1 : stop) - row_begin);
     t = t < lo / TILE ? lo / TILE : t;
     t1 = t1 > (hi + TILE - 1) / TILE ? (hi + TILE - 1) / TILE : t1;
+    t += joined ? wave : 0;
 
     const int32_t* tab = A.table + (int64_t)request * A.max_blocks;
     u32x4_t kr[4][KP], vr[DT];
@@ -809,7 +812,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
       load_ids(t);
       load_k(t);
       load_v(t);
-      if (t + 1 < t1) load_ids(t + 1);
+      if (t + step < t1) load_ids(t + step);
     }
 
     // query fragments: columns m of q^T; row m's limits
@@ -841,9 +844,9 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
       mx[c] = -INFINITY;
       l[c] = 0.0f;
     }
-    for (; t < t1; t++) {
+    for (; t < t1; t += step) {
       const int j0 = t * TILE + 16 * g;       // this lane's 16 tokens in scores and V^T
-      const bool more = t + 1 < t1;
+      const bool more = t + step < t1;
       f32x4_t s[NR][4];
       const float ks = e8m0_as_scale(ksc);
 #pragma unroll
@@ -861,7 +864,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
           }
         }
       }
-      if (more) load_k(t + 1);
+      if (more) load_k(t + step);
       float vs = e8m0_as_scale(vsc);
       const bool edge = t * TILE + TILE - 1 > rows.pos0 || t * TILE < lo_max || __any(!vok);
       if (edge) {                             // bytes of V that no row may see
@@ -928,8 +931,8 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
         }
       }
       if (more) {
-        load_v(t + 1);
-        if (t + 2 < t1) load_ids(t + 2);
+        load_v(t + step);
+        if (t + 2 * step < t1) load_ids(t + 2 * step);
       }
     }
 #pragma unroll
