@@ -378,6 +378,99 @@ __device__ __forceinline__ void append_run(const void* __restrict__ x, int64_t s
   __syncthreads();                            // LDS is free for the next run
 }
 
+// Runs of one token each (a decode step): `runs` has the chunk's tokens that
+// begin one, `slot` the slot of token t0 + lane.  D / 8 lanes a token, many
+// tokens at once and no barrier among them; the pages whose scale grew are
+// gone over by the whole workgroup afterwards.
+template <bool BF16, bool VALUES, int D, int PAGE>
+__device__ __forceinline__ void append_ones(const void* __restrict__ x, int64_t stride, int64_t t0, int chunk,
+                                            unsigned long long runs, int64_t slot, int heads, int head,
+                                            uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int* grown) {
+  constexpr int GL = D / 8, AT_ONCE = KV_THREADS / GL;
+  const int tid = threadIdx.x, lane = tid & 63, ch = tid % GL * 8;
+  if (tid < 64) grown[tid] = 0;
+  __syncthreads();
+  for (int base = 0; base < chunk; base += AT_ONCE) {
+    const int i = base + tid / GL;
+    const int64_t sl = __shfl(slot, i & 63, 64);
+    if (i >= chunk || !(runs >> i & 1)) continue;                  // the same for all lanes of a token
+    const int off = (int)(sl & (PAGE - 1));
+    const int64_t block = sl / PAGE * heads + head;
+    const int old = off ? (int)scales[block] : 0;
+    Raw8<BF16> v;
+    const uint8_t* from = (const uint8_t*)x + ((t0 + i) * stride + ch) * (BF16 ? 2 : 4);
+#pragma unroll
+    for (int e = 0; e < (BF16 ? 1 : 2); e++) {
+      const u32x4_t q = ld16(from + 16 * e);
+#pragma unroll
+      for (int b = 0; b < 4; b++) v.w[4 * e + b] = q[b];
+    }
+    auto join = [&](uint32_t a) {
+#pragma unroll
+      for (int o = 1; o < GL; o <<= 1) {
+        const uint32_t b = (uint32_t)__shfl_xor((int)a, o, 64);
+        a = a > b ? a : b;
+      }
+      return a;
+    };
+    uint32_t m = v.magnitude(0);
+    if constexpr (BF16) m = (m & 0xFFFFu) > (m >> 16) ? m << 16 : m & 0xFFFF0000u;
+    m = join(m);
+    const bool odd = m >= 0x7F800000u;        // NaN or infinity
+    float f[8];
+    if (odd) {
+      v.widen(f);
+      m = 0;
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        const uint32_t a = __float_as_uint(f[e]) & 0x7FFFFFFFu;
+        m = a < 0x7F800000u && a > m ? a : m;
+      }
+      m = join(m);
+    }
+    const int need = e8m0_cover(m), c = need > old ? need : old;
+    u32x2_t w;
+    if (!odd) {
+      w = v.codes(e8m0_as_scale((uint32_t)c));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; e++) f[e] = __builtin_ldexpf(f[e], 127 - c);
+      w = u32x2_t{e4m3_word(f), e4m3_word(f + 4)};
+    }
+    uint8_t* p = codes + block * PAGE * D;
+    if constexpr (!VALUES) {
+      *reinterpret_cast<u32x2_t*>(p + off * D + ch) = w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; e++) p[(ch + e) * PAGE + off] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
+    }
+    if (ch == 0 && (!off || c != old)) scales[block] = (uint8_t)c;
+    if (ch == 0 && off && c > old) grown[i] = c - old;
+  }
+  __syncthreads();
+  const int shift = grown[lane];
+  for (unsigned long long todo = __ballot(shift != 0); todo; todo &= todo - 1) {
+    const int i = __builtin_ctzll(todo);
+    const int64_t sl = __shfl(slot, i, 64);
+    const int by = -__shfl(shift, i, 64), off = (int)(sl & (PAGE - 1));
+    uint8_t* p = codes + (sl / PAGE * heads + head) * PAGE * D;
+    if constexpr (!VALUES) {
+      for (int j = tid; j < off * D / 4; j += KV_THREADS) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(p) + j;
+        *w = e4m3_word_shifted(*w, by);
+      }
+    } else {
+      const int words = (off + 3) >> 2;
+      for (int j = tid; j < D * words; j += KV_THREADS) {
+        const int k = j % words;
+        uint32_t* w = reinterpret_cast<uint32_t*>(p + j / words * PAGE) + k;
+        const uint32_t had = *w, keep = off - 4 * k < 4 ? ~0u << (8 * (off - 4 * k)) : 0u;   // bytes from `off` on
+        *w = (had & keep) | (e4m3_word_shifted(had, by) & ~keep);
+      }
+    }
+  }
+}
+
 // Workgroup (x, head, keys or values) writes the runs that begin in tokens
 // [x * chunk, (x + 1) * chunk), chunk <= 64.
 template <bool BF16, int D, int PAGE>
@@ -387,6 +480,7 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_append(
     uint8_t* __restrict__ k_scales, uint8_t* __restrict__ v_codes, uint8_t* __restrict__ v_scales) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[D * (PAGE + 4)];
   __shared__ uint32_t red[KV_THREADS / 64];
+  __shared__ int grown[64];
   const int lane = threadIdx.x & 63, head = blockIdx.y, heads = gridDim.y;
   const int64_t limit = num_pages * PAGE;
   const int64_t t0 = (int64_t)blockIdx.x * chunk;
@@ -403,6 +497,18 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_append(
   const int64_t last0 = __shfl(s0, 63, 64), up1 = __shfl_up(s1, 1, 64), before1 = lane ? up1 : last0;
   const unsigned long long on0 = __ballot((s0 & (PAGE - 1)) && before == s0 - 1);
   const unsigned long long on1 = __ballot((s1 & (PAGE - 1)) && before1 == s1 - 1);
+  const int64_t col = (int64_t)head * D * (BF16 ? 2 : 4);
+  // no token of the chunk, nor the one behind it, goes on in another's run
+  const unsigned long long behind = chunk < 64 ? on0 & ((2ull << chunk) - 2) : (on0 & ~1ull) | (on1 & 1);
+  if (!behind) {
+    if (blockIdx.z == 0)
+      append_ones<BF16, false, D, PAGE>((const uint8_t*)k + col, k_stride, t0, chunk, runs, s0, heads, head, k_codes,
+                                        k_scales, grown);
+    else
+      append_ones<BF16, true, D, PAGE>((const uint8_t*)v + col, v_stride, t0, chunk, runs, s0, heads, head, v_codes,
+                                       v_scales, grown);
+    return;
+  }
   unsigned long long on2 = 0;
   if constexpr (PAGE == 128) {
     const int64_t s2 = slot_of(t0 + 128 + lane);
@@ -422,7 +528,6 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_append(
     }
     const int off = (int)(slot & (PAGE - 1));
     const int64_t block = slot / PAGE * heads + head;
-    const int64_t col = (int64_t)head * D * (BF16 ? 2 : 4);
     if (blockIdx.z == 0)
       append_run<BF16, false, D, PAGE>((const uint8_t*)k + col, k_stride, t, n, off, k_codes + block * PAGE * D,
                                        k_scales + block, lds, red);
@@ -1497,7 +1602,7 @@ wq_status wq_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v
   if (!wq_aligned(k) || !wq_aligned(v) || !wq_aligned(k_codes) || !wq_aligned(v_codes)) return WQ_EALIGN;
   if (tokens == 0) return WQ_OK;
   int chunk = 1;
-  while (chunk < 64 && chunk < page && (tokens + chunk - 1) / chunk * heads * 2 > 4096) chunk *= 2;
+  while (chunk < 64 && chunk < page && (tokens + chunk - 1) / chunk * heads * 2 > 2048) chunk *= 2;
   const dim3 grid((unsigned)((tokens + chunk - 1) / chunk), (unsigned)heads, 2);
   hipStream_t s = (hipStream_t)stream;
   const bool bf = x_dtype == WQ_BF16;
