@@ -155,6 +155,21 @@ def test_append_many_requests_in_steps(W):
     _check_append(W, k, v, slots, _cache(g, N, 2, 16, 64), True)
 
 
+@pytest.mark.parametrize("values", [1, 50])
+def test_append_growing_scales(W, values):
+    """Single tokens whose scale passes their page's, in every place of the page, and runs beside them."""
+    banner("kv append: growing scales", values)
+    g = np.random.default_rng(6)
+    H, D, P = 2, 128, 32
+    ctx = list(range(0, 64)) + [7, 40]
+    new = [1] * 64 + [values, 3]
+    slots, N = _slots(g, ctx, new, P)
+    k, v = (g.standard_normal((len(slots), H, D)).astype(np.float32) * 2.0 ** g.integers(3, 7, (len(slots), H, 1))
+            for _ in range(2))
+    for bf16 in (True, False):
+        _check_append(W, k, v, slots, _cache(g, N, H, P, D), bf16)
+
+
 def test_append_special_values(W):
     banner("kv append: zeros, NaN, infinities, extremes, slots outside the cache")
     g = np.random.default_rng(3)
@@ -373,6 +388,39 @@ def test_attention_one_long_context_beside_short_ones(W):
     banner("kv attention: 20000 tokens beside short contexts")
     q, cu, kv, cache, table = _problem(10, 4, 2, 64, 64, [1, 1, 1, 2], [20000, 3, 900, 5000])
     _check_attention(W, q, cu, kv, cache, table, poison=False)
+
+
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("H,group,most_q,D", [(8, 2, 1, 64), (8, 4, 6, 64), (5, 3, 1, 128), (16, 2, 10, 128), (3, 16, 4, 64)])
+def test_attention_shares_over_requests(W, page, H, group, most_q, D):
+    """Ragged batches whose tiles are cut into shares that begin and end anywhere: several requests to
+    a wave, several waves to a request, requests without rows or without a cache between them."""
+    banner("kv attention: shares over requests", page, H, group, most_q, D)
+    g = np.random.default_rng(H + page)
+    kl = np.exp(g.uniform(0, np.log(3000), 40)).astype(int)
+    ql = g.integers(1, most_q + 1, 40)
+    kl[[3, 17]], ql[[5, 6, 30]], kl[[9, 22]] = 0, 0, [2999, 2048]
+    q, cu, kv, cache, table = _problem(14, H * group, H, D, page, ql, kl, spare_rows=2)
+    for kw in ({}, {"window": 700}):
+        _check_attention(W, q, cu, kv, cache, table, max_q=most_q, **kw)
+
+
+@pytest.mark.parametrize("hint", [0, 1])
+def test_attention_many_short_requests(W, hint):
+    banner("kv attention: 900 requests of a few tokens, 16 key heads", hint)
+    g = np.random.default_rng(15)
+    kl, ql = g.integers(0, 130, 900), g.integers(0, 3, 900)
+    q, cu, kv, cache, table = _problem(15, 16, 16, 64, 16, ql, kl)
+    _check_attention(W, q, cu, kv, cache, table, max_q=2 if hint else 0)
+
+
+@pytest.mark.parametrize("page", [32, 64])
+def test_attention_chunk_of_a_long_prompt(W, page):
+    """Few rows and many tokens: prompt tiles are split over the cache, beside short requests."""
+    banner("kv attention: chunks of 40 and 90 rows on 3000 tokens", page)
+    q, cu, kv, cache, table = _problem(16, 8, 2, 128, page, [40, 1, 90, 5], [3000, 700, 2500, 64])
+    for kw in ({}, {"softcap": 10.0}, {"window": 1500}):
+        _check_attention(W, q, cu, kv, cache, table, **kw)
 
 
 def test_attention_cache_past_32_bits(W):
