@@ -545,7 +545,8 @@ wq_status wq_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v
  * lse -inf.  Rows behind cu_q[batch] stay as they were.
  *
  * q           tokens x q_heads x head_dim bf16; rows of a token q_stride elements
- *             apart (at least q_heads * head_dim, a multiple of 8).
+ *             apart (at least q_heads * head_dim, a multiple of 8); tokens times
+ *             query heads a key/value head below 2^31.
  * cu_q        batch + 1 int32, cu_q[0] = 0, non-decreasing, at most `tokens`.
  * kv_lens     batch int32.
  * block_table batch x max_blocks int32.  These three are device data the host
@@ -555,8 +556,12 @@ wq_status wq_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v
  *             not seen, so that no access leaves the buffers.
  * max_q       the largest number of queries of one request, or 0 if unknown.
  *             Only the choice of kernels depends on it.
- * softcap     >= 0, finite; window >= 0; sm_scale > 0, finite.
- * out         tokens x q_heads x head_dim bf16, dense (output).
+ * sm_scale    > 0, finite; window >= 0.
+ * softcap     0, or 2^-10 to 2^10 (WQ_EUNSUPPORTED outside): a capped score is off
+ *             by at most softcap * 2^-22.
+ * out         tokens x q_heads x head_dim bf16, dense (output); not the queries' own
+ *             memory, since a row's queries are read while others are written
+ *             (an equal pointer is WQ_EINVAL).
  * lse         tokens x q_heads fp32 (output), or NULL.
  * workspace   wq_kv_attention_workspace_size bytes, 16-byte aligned, for this
  *             call alone while it runs; its contents need no preparation and

@@ -49,16 +49,17 @@ def test_append_refusals(lib):
 
 def test_attention_refusals(lib):
     def call(q=P, qs=1024, cu=P, kv=P, batch=2, tokens=4, max_q=0, hq=8, hk=4, dim=128, kc=P, ksc=P, vc=P, vsc=P,
-             page=64, pages=10, table=P, width=4, sm=0.1, cap=0.0, window=0, out=P, lse=None, ws=P, wsb=1 << 40):
+             page=64, pages=10, table=P, width=4, sm=0.1, cap=0.0, window=0, out=P2, lse=None, ws=P, wsb=1 << 40):
         return lib.wq_kv_attention(q, qs, cu, kv, batch, tokens, max_q, hq, hk, dim, kc, ksc, vc, vsc, page, pages,
                                    table, width, sm, cap, window, out, lse, ws, wsb, None)
     assert call(dim=32) == 3 and call(page=20) == 3
+    assert call(cap=2000.0, out=P2) == 3 and call(cap=1e-4, out=P2) == 3
     inf, nan = float("inf"), float("nan")
     for bad in ({"batch": -1}, {"tokens": -1}, {"max_q": -1}, {"hk": 0}, {"hq": 6}, {"hq": 2}, {"pages": 0},
                 {"width": 0}, {"width": 1 << 26}, {"window": -1}, {"sm": 0.0}, {"sm": -1.0}, {"sm": inf}, {"sm": nan},
                 {"cap": -1.0}, {"cap": inf}, {"cap": nan}, {"qs": 1000}, {"qs": 1028}, {"q": None}, {"cu": None},
                 {"kv": None}, {"table": None}, {"out": None}, {"kc": None}, {"ksc": None}, {"vc": None},
-                {"vsc": None}, {"tokens": 1 << 31}, {"pages": 1 << 40}):
+                {"vsc": None}, {"tokens": 1 << 31}, {"tokens": (1 << 31) - 200}, {"pages": 1 << 40}, {"out": P}):
         assert call(**bad) == 1, bad
     for bad in ("q", "out", "kc", "vc", "ws"):
         assert call(**{bad: ODD}) == 2, bad
@@ -70,7 +71,7 @@ def test_attention_workspace_is_asked_for(lib):
     ok = (3, 3, 1, 32, 8, 128, 64, 512)
     need = size(*ok)
     args = lambda wsb, ws=P: lib.wq_kv_attention(P, 4096, P, P, 3, 3, 1, 32, 8, 128, P, P, P, P, 64, 10, P, 512, 0.1,
-                                                 0.0, 0, P, None, ws, wsb, None)
+                                                 0.0, 0, P2, None, ws, wsb, None)
     if need:
         assert args(need - 1) == 1 and args(need, None) == 1
     # sizes the call refuses need nothing

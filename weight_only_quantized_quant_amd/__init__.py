@@ -488,6 +488,7 @@ def wq_kv_blocks(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: tor
         cur = _ptr(cursor, dev, _i32t, "cursor")
         if cursor.numel() < 1:
             raise ValueError("cursor must have an element")
+    tokens = int(tokens)
     if tokens < 0:
         raise ValueError("tokens must not be negative")
     slots = ctx_lens.new_empty(tokens, dtype=_i64t)
@@ -526,7 +527,8 @@ def wq_kv_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tens
     """Causal attention of q (bf16 [tokens, q_heads, head_dim], tokens may be strided; request i has
     rows cu_q[i] .. cu_q[i + 1]) over the cache's kv_lens[i] tokens of the pages block_table[i].
     cu_q int32 [B + 1], kv_lens int32 [B], block_table int32 [B, W].  sm_scale defaults to
-    head_dim ** -0.5; max_q: the largest number of queries of one request if known.  Returns out
+    head_dim ** -0.5; softcap 0 or 2^-10 .. 2^10; max_q: the largest number of queries of one
+    request if known (it only chooses kernels).  Returns out
     bf16 [tokens, q_heads, head_dim] (and lse fp32 [tokens, q_heads])."""
     dev, T, hq, qd, q_stride = _token_rows(q, "q")
     n, h, p, dim, kc, ks, vc, vs = _kv_cache(k_codes, k_scales, v_codes, v_scales, dev)
@@ -538,8 +540,8 @@ def wq_kv_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tens
     B, width = block_table.shape
     cu = _shaped(cu_q, dev, _i32t, (B + 1,), "cu_q")
     kl = _shaped(kv_lens, dev, _i32t, (B,), "kv_lens")
-    if sm_scale is None:
-        sm_scale = dim ** -0.5
+    sm_scale = dim ** -0.5 if sm_scale is None else float(sm_scale)
+    max_q, window = int(max_q), int(window)
     if out is None:
         out = q.new_empty((T, hq, dim))
         op = out.data_ptr()

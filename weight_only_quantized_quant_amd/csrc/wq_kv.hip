@@ -1315,15 +1315,25 @@ __global__ __launch_bounds__(PTHREADS, 2) void k_kv_prompt(const KvArgs A, const
   const uint8_t* vfrag[2];
 #pragma unroll
   for (int u = 0; u < 2; u++) vfrag[u] = sv[0] + (128 * u + 32 * h + (m ^ (2 * (2 * u + h)))) * 16;
+  constexpr int HOLD = 4;                     // fragments read ahead of their use
+  bf16x8_t kf[HOLD];
+  auto frag_k = [&](int at, int u, int k) {
+    return *reinterpret_cast<const bf16x8_t*>(kfrag + at + (u * KS + k) * 1024 + (m ^ (XK * k)) * 16);
+  };
+  auto fetch = [&](int at, int u) {
+#pragma unroll
+    for (int k = 0; k < HOLD; k++) kf[k] = frag_k(at, u, k);
+  };
   auto scores = [&](int at, int u) {          // of half u of the tile whose K begins at `at`
     f32x16_t z;
 #pragma unroll
     for (int i = 0; i < 16; i++) z[i] = 0.0f;
+    bf16x8_t rest[KS > HOLD ? KS - HOLD : 1];
 #pragma unroll
-    for (int k = 0; k < KS; k++) {
-      const bf16x8_t a = *reinterpret_cast<const bf16x8_t*>(kfrag + at + (u * KS + k) * 1024 + (m ^ (XK * k)) * 16);
-      z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, qf[k], z, 0, 0, 0);
-    }
+    for (int k = HOLD; k < KS; k++) rest[k - HOLD] = frag_k(at, u, k);
+    __builtin_amdgcn_sched_barrier(0x47F);    // LDS reads stay where they are
+#pragma unroll
+    for (int k = 0; k < KS; k++) z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k < HOLD ? kf[k] : rest[k - HOLD], qf[k], z, 0, 0, 0);
     return z;
   };
   // caps and masks the scores of half u of tile t and moves the running
@@ -1355,8 +1365,12 @@ __global__ __launch_bounds__(PTHREADS, 2) void k_kv_prompt(const KvArgs A, const
       for (int d = 0; d < DT; d++) o[d] *= f;
     }
   };
-  auto weigh = [&](int buf, int u, const f32x16_t& s) {            // probabilities, and their sums of V
+  auto weigh = [&](int buf, int u, const f32x16_t& s, int at, int un) {   // probabilities, and their sums of V
     const float off = sc.add - (mx == -INFINITY ? 0.0f : mx);
+    bf16x8_t v0[DT], v1[DT];
+#pragma unroll
+    for (int d = 0; d < DT; d++) v0[d] = *reinterpret_cast<const bf16x8_t*>(vfrag[u] + buf * BUF + d * 4096);
+    __builtin_amdgcn_sched_barrier(0x47F);    // LDS reads stay where they are
     uint32_t pw[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) {
@@ -1366,14 +1380,15 @@ __global__ __launch_bounds__(PTHREADS, 2) void k_kv_prompt(const KvArgs A, const
       pw[i] = pack_bf16x2(a, b);              // half a step of 2^-8 per probability, l keeps fp32
     }
 #pragma unroll
-    for (int e = 0; e < 2; e++) {
-      const bf16x8_t p = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[4 * e], pw[4 * e + 1], pw[4 * e + 2], pw[4 * e + 3]}));
+    for (int d = 0; d < DT; d++) v1[d] = *reinterpret_cast<const bf16x8_t*>(vfrag[u] + buf * BUF + d * 4096 + 1024);
+    const bf16x8_t p0 = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[0], pw[1], pw[2], pw[3]}));
+    const bf16x8_t p1 = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[4], pw[5], pw[6], pw[7]}));
 #pragma unroll
-      for (int d = 0; d < DT; d++) {
-        const bf16x8_t a = *reinterpret_cast<const bf16x8_t*>(vfrag[u] + buf * BUF + d * 4096 + e * 1024);
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, p, o[d], 0, 0, 0);
-      }
-    }
+    for (int d = 0; d < DT; d++) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v0[d], p0, o[d], 0, 0, 0);
+    fetch(at, un);
+    __builtin_amdgcn_sched_barrier(0x47F);    // LDS reads stay where they are
+#pragma unroll
+    for (int d = 0; d < DT; d++) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v1[d], p1, o[d], 0, 0, 0);
   };
   // at the top of a step: first half of tile t settled, K of t and t + 1 and
   // V^T of t in LDS, K of t + 2 and V^T of t + 1 on their way to registers
@@ -1391,7 +1406,9 @@ __global__ __launch_bounds__(PTHREADS, 2) void k_kv_prompt(const KvArgs A, const
     ids_k(t0 + 3);
     tile_barrier();
     if (w_rows > 0) {
+      fetch(k0, 0);
       s0 = scores(k0, 0);
+      fetch(k0, 1);
       settle(t0, 0, s0);
     }
   }
@@ -1399,10 +1416,10 @@ __global__ __launch_bounds__(PTHREADS, 2) void k_kv_prompt(const KvArgs A, const
     const int buf = (t - t0) & 1;
     if (w_rows > 0) {
       s1 = scores(k0, 1);
-      weigh(buf, 0, s0);
+      weigh(buf, 0, s0, k1, 0);
       settle(t, 1, s1);
       s0 = scores(k1, 0);                     // behind the last tile: not used
-      weigh(buf, 1, s1);
+      weigh(buf, 1, s1, k1, 1);
     }
     if (t + 1 == t1) break;
     store_k(k2);
@@ -1726,16 +1743,17 @@ wq_status wq_kv_attention(const void* q_bf16, int64_t q_stride, const int32_t* c
   if (!kv_sizes_ok(batch, tokens, max_q, q_heads, kv_heads, page, max_blocks) || num_pages < 1 || window < 0)
     return WQ_EINVAL;
   if (!(sm_scale > 0.0f) || !(sm_scale < INFINITY) || !(softcap >= 0.0f) || !(softcap < INFINITY)) return WQ_EINVAL;
+  if (softcap > 0.0f && (softcap < 0x1p-10f || softcap > 0x1p10f || !(sm_scale / softcap < 0x1p100f))) return WQ_EUNSUPPORTED;
   const int64_t row = (int64_t)q_heads * head_dim;
   if (q_stride < row || q_stride % 8 || q_stride > (int64_t(1) << 40) ||
       !wq_numel_ok(num_pages, (int64_t)kv_heads * head_dim * page) || !wq_numel_ok(tokens ? tokens : 1, row) ||
       !wq_numel_ok(batch ? batch : 1, max_blocks))
     return WQ_EINVAL;
   if (!k_codes || !k_scales || !v_codes || !v_scales) return WQ_EINVAL;
-  if (batch > 0 && tokens > 0 && (!q_bf16 || !cu_q || !kv_lens || !block_table || !out)) return WQ_EINVAL;
+  if (batch > 0 && tokens > 0 && (!q_bf16 || !cu_q || !kv_lens || !block_table || !out || out == q_bf16)) return WQ_EINVAL;
   if (!wq_aligned(q_bf16) || !wq_aligned(out) || !wq_aligned(k_codes) || !wq_aligned(v_codes) || !wq_aligned(workspace))
     return WQ_EALIGN;
-  if (batch == 0 || tokens == 0) return WQ_OK;
+  if (batch == 0 || tokens == 0) return WQ_OK;               // nothing to compute
   const KvPlan p = kv_plan(batch, tokens, max_q, q_heads, kv_heads, head_dim, page, max_blocks);
   if (ws_bytes < p.bytes || !workspace) return WQ_EINVAL;
   if (p.pro_items * kv_heads > 0x7FFFFFFF / PTHREADS) return WQ_EINVAL;
