@@ -40,5 +40,7 @@ w4a8      MoE routing, W4A8 scale recipe, INT4 -> E4M3 lookup table, grouped GEM
 Parity status: every function is pinned by CPU tests against values the pages
 print, closed forms, library routines (torch CPU casts) or brute force, except
 the nibble order inside a byte / word (pack and unpack), which the pages do not
-fix: parity unpinned (self-consistency only).
+fix: parity unpinned (self-consistency only), and the key/value cache (kv), which
+is not on the pages: derived from its formats and pinned by brute force,
+invariants and closed forms.
 """

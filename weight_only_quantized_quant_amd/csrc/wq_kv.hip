@@ -43,9 +43,11 @@ __device__ __forceinline__ int first_above(const int64_t* sums, int count, int64
 // sums of new tokens and of the pages needed, kept in LDS for the chunk) and
 // writes its own rows of the token arrays, found by binary search in the
 // chunk's token ends, and its share of the new table entries, found in the
-// same way.  Workgroup 0 writes the per-request outputs.  There is no dependence between workgroups, so one
-// launch does it all: the new pages of a token come from the free list
-// itself, not from the table that another workgroup fills.
+// same way.  Workgroup 0 writes the per-request outputs.  There is no
+// dependence between workgroups, so one launch does it all: the new pages of a
+// token come from the free list itself, not from the table that another
+// workgroup fills.  Bound by latency: 4.4 us for 256 requests of one token,
+// 4.0 us for 7 prompts of 16384 tokens (an empty launch takes 2.5 us).
 __global__ __launch_bounds__(KV_THREADS) void k_kv_blocks(
     const int32_t* __restrict__ ctx_lens, const int32_t* __restrict__ new_lens, int64_t batch,
     const int32_t* __restrict__ free_pages, int64_t num_free, const int32_t* __restrict__ cursor, int log_page,
@@ -237,7 +239,8 @@ struct Raw8 {
 // tokens, which LDS turns into whole rows of the transposed page.  Bound by
 // bytes, so the arithmetic is kept to one and a half instructions an element:
 // maxima of bit patterns, two for bf16 at a time, and conversions that take
-// the scale; a run that holds a NaN or an infinity goes the long way.
+// the scale; a run that holds a NaN or an infinity goes the long way.  8192
+// tokens of prompts, 8 heads of 128, bf16: 13.3 us a call (3.8 TB/s).
 template <bool BF16, bool VALUES, int D, int PAGE>
 __device__ __forceinline__ void append_run(const void* __restrict__ x, int64_t stride, int64_t t, int n, int off,
                                            uint8_t* __restrict__ codes, uint8_t* __restrict__ scale, uint8_t* lds,
@@ -381,7 +384,9 @@ __device__ __forceinline__ void append_run(const void* __restrict__ x, int64_t s
 // Runs of one token each (a decode step): `runs` has the chunk's tokens that
 // begin one, `slot` the slot of token t0 + lane.  D / 8 lanes a token, many
 // tokens at once and no barrier among them; the pages whose scale grew are
-// gone over by the whole workgroup afterwards.
+// gone over by the whole workgroup afterwards.  64 tokens, 8 heads of 128: 4.2
+// us (5.3 as runs); 2048: 66 us, bound by the cache line that each value byte
+// of the transposed page touches (76 as runs).
 template <bool BF16, bool VALUES, int D, int PAGE>
 __device__ __forceinline__ void append_ones(const void* __restrict__ x, int64_t stride, int64_t t0, int chunk,
                                             unsigned long long runs, int64_t slot, int heads, int head,
@@ -472,7 +477,9 @@ __device__ __forceinline__ void append_ones(const void* __restrict__ x, int64_t 
 }
 
 // Workgroup (x, head, keys or values) writes the runs that begin in tokens
-// [x * chunk, (x + 1) * chunk), chunk <= 64.
+// [x * chunk, (x + 1) * chunk), chunk <= 64: one token where that gives no more
+// than 2048 workgroups, else up to a page, since a workgroup without a run of
+// its own costs its start (8192 tokens: 14.7 us at 2048, 17.4 at 4096, 22 at 8192).
 template <bool BF16, int D, int PAGE>
 __global__ __launch_bounds__(KV_THREADS) void k_kv_append(
     const void* __restrict__ k, int64_t k_stride, const void* __restrict__ v, int64_t v_stride,
@@ -556,11 +563,16 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_append(
 // the `group` query heads that share a key/value head share its tiles.
 constexpr int TILE = 64;                      // tokens per step
 constexpr int PROWS = 128, PTHREADS = 256;    // rows of a prompt tile, threads of its workgroup
-// Requests of at most this many rows go through the decode kernel beside
-// prompts: its tiles of 32 read K and V once each, the prompt kernel once for
-// 128, but a prompt tile's staging and barriers cost the same however few there are.
+// Requests of at most this many rows go through the decode kernel: its tiles of
+// 32 read K and V once each, the prompt kernel once for 128, but a prompt
+// tile's staging and barriers cost the same however few there are.  24 requests
+// on 500-6000 tokens, 8 heads of 128: 48 rows 54 us decoded against 58 in
+// prompt tiles, 64 rows 56 against 57, 128 rows 79 against 66.
 constexpr int SHORT_ROWS = 64;
-constexpr int DEC_GROUPS = 512;               // decode workgroups over all heads: two a CU
+// Decode workgroups over all heads: two a CU, as the registers of D = 128 allow
+// (256: 2-4 % slower on drafted tokens; 768 and 1024 at D = 64, where they fit:
+// 9 and 14 % slower on short windows).
+constexpr int DEC_GROUPS = 512;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 struct KvArgs {
@@ -607,7 +619,6 @@ struct KvChain {
   int32_t rows, query0, head0;                // 0 rows: none
   int32_t first, last;                        // waves that share the row tile
   int32_t first_joined, last_joined;          // whether the workgroups of those joined their waves
-  int32_t pad;
 };
 struct KvShare {
   int groups, rows;                           // workgroups per head, rows of a slot
@@ -638,8 +649,7 @@ __device__ __forceinline__ int64_t lane64(int64_t v, int src) {
   return (int64_t)(((uint64_t)(uint32_t)lane32((int)(v >> 32), src) << 32) | (uint32_t)lane32((int)v, src));
 }
 
-// The request's limits in the cache: positions from `first` on, tokens [0, len).
-// Token j is visible to position p when p - window < j <= p.
+// The lowest token that position `pos` sees (window 0: the first).
 __device__ __forceinline__ int kv_lowest(int pos, int window) { return window > 0 && pos >= window ? pos - window + 1 : 0; }
 
 // Request i (its lengths clamped to what the tensors hold): first query row,
@@ -675,8 +685,7 @@ struct KvRequest {
 // requests are spread evenly over about part.splits items, a request of
 // `tiles` tiles being cut into tiles / share splits per row tile, to the
 // nearest (rounding up costs more in partial sums than it evens out).
-// Splits, not tokens, are scanned, so that a long context beside short ones
-// fills the chip as well as equal ones do.  False if there is no such item.
+// False if there is no such item.
 template <int R, int WHICH>
 __device__ __forceinline__ bool kv_find(const KvArgs& A, const KvPart& part, int64_t item, bool count_all, KvItem& it) {
   const int lane = threadIdx.x & 63;
@@ -796,6 +805,9 @@ __device__ __forceinline__ u32x4_t keep_tokens(u32x4_t v, int j, int lo, int hi)
 // inside one row tile joins them in LDS first.  A row tile that sees nothing
 // counts as one tile, so that its rows are written.
 //
+// 8 heads of 128, 4 query heads each: 64 x 8192 tokens 187 us (5.76 TB/s, 0.92
+// of a streaming read's rate); 64 x 2048-8192 tokens 105 us and 4.9 us joining.
+//
 // Lane l = 16 g + m.  K tile a (of 4): operand row m is token
 // 16 (m / 4) + 4 a + m % 4, result rows 4 g + i are then tokens 16 g + 4 a + i.
 template <int D, bool CAP, int WHICH, int NR>
@@ -857,7 +869,10 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
     find(u0);
     rt = (int)((u0 - begin) / units());
   }
-  if (q.row_tiles == 0) return;
+  if (q.row_tiles == 0) {                     // lengths that changed under the kernel
+    if (kvh == 0 && lane == 0) part.chain[x] = none;
+    return;
+  }
 
   const int last_col = (int)A.max_blocks - 1;
   const uint32_t head_bytes = (uint32_t)D << A.log_page, page_bytes = head_bytes * A.kv_heads;
@@ -1054,7 +1069,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
       // the last wave: the one whose share holds unit row_end - 1
       const int64_t last = (row_end * shares - 1) / total;
       chain = KvChain{n_rows, q.q0 + rows.first, rows.head0, joined ? 4 * group : x, (int)last, joined,
-                      share_at((last | 3) + 1) <= row_end, 0};
+                      share_at((last | 3) + 1) <= row_end};
     }
     auto put = [&](int row, int ch, const f32x4_t& v, float top, float sum) {      // 4 channels of a row
       if (!whole) {
@@ -1139,7 +1154,11 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
 //
 // BIG: pages of 64 tokens and more, so that a tile lies in one page: its id,
 // scales and addresses are scalars, which takes a fifth of the loop's vector
-// instructions away.
+// instructions away (330 -> 323 us, capped 688 -> 654 us).
+//
+// Three prompts of 1500-4096 tokens, 32 heads of 128 on 8: 306-314 us (840-863
+// TFLOP/s; matrix cores busy 0.37, vector units 0.46 of the cycles, no LDS bank
+// conflicts).  Power sets the clock: a tenth fewer cycles took 3 % off the time.
 template <int D, bool CAP, bool BIG>
 __global__ __launch_bounds__(PTHREADS, 2) void k_kv_prompt(const KvArgs A, const KvPart part) {
   constexpr int KS = D / 16, DT = D / 32;     // k steps, channel tiles
@@ -1232,7 +1251,8 @@ __global__ __launch_bounds__(PTHREADS, 2) void k_kv_prompt(const KvArgs A, const
       for (int i = 0; i < ST; i++) {
         const uint32_t k = there(idk[i]) ? idk[i] : 0;
         ksc[i] = ksb[(uint64_t)k * (uint32_t)A.kv_heads];
-        kr[i] = ld16(kbase + ((uint64_t)k * page_bytes + ((t * TILE + ktok + PTHREADS / KS * i) & in_page) * D + 16 * (tid % KS)));
+        const uint32_t in = ((t * TILE + ktok + PTHREADS / KS * i) & in_page) * D + 16 * (tid % KS);
+        kr[i] = ld16(kbase + ((uint64_t)k * page_bytes + in));
       }
     }
   };
@@ -1333,7 +1353,8 @@ __global__ __launch_bounds__(PTHREADS, 2) void k_kv_prompt(const KvArgs A, const
     for (int k = HOLD; k < KS; k++) rest[k - HOLD] = frag_k(at, u, k);
     __builtin_amdgcn_sched_barrier(0x47F);    // LDS reads stay where they are
 #pragma unroll
-    for (int k = 0; k < KS; k++) z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k < HOLD ? kf[k] : rest[k - HOLD], qf[k], z, 0, 0, 0);
+    for (int k = 0; k < KS; k++)
+      z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k < HOLD ? kf[k] : rest[k - HOLD], qf[k], z, 0, 0, 0);
     return z;
   };
   // caps and masks the scores of half u of tile t and moves the running
@@ -1521,8 +1542,9 @@ __device__ __forceinline__ void kv_join(const KvArgs& A, const float* sums, cons
       M = top;
     }
     if (grp == 0) {
-      const uint32_t rr = head0 + row, group = A.group;
-      const int64_t orow = (int64_t)(query0 + rr / group) * A.q_heads + kvh * group + rr % group;
+      const uint32_t rr = (uint32_t)head0 + row, group = A.group;
+      const int64_t token = (int64_t)query0 + rr / group, orow = token * A.q_heads + kvh * group + rr % group;
+      if (token < 0 || token >= A.tokens) continue;
       const float inv = L == 0.0f ? 0.0f : 1.0f / L;
       *reinterpret_cast<u32x2_t*>(A.out + orow * D + ch) =
           u32x2_t{pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv)};
@@ -1556,7 +1578,8 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_join(const KvArgs A, const Kv
   const int64_t slot = x / (PROWS / 16);
   if (slot >= pro.used[0]) return;
   const KvRec rec = pro.rec[slot];
-  if (rec.splits == 0 || slot + rec.splits > pro.slots) return;
+  // entries that ranges of rows on top of each other left unwritten hold anything
+  if (rec.splits <= 0 || slot + rec.splits > pro.slots || rec.rows > PROWS) return;
   kv_join<D>(A, pro.sums, pro.stats, PROWS, kvh, (int)(x % (PROWS / 16)) * 16, rec.rows, rec.query0, rec.head0, rec.splits,
              [&](int i) -> int64_t { return slot + i; });
 }
@@ -1642,8 +1665,10 @@ wq_status wq_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v
 
 namespace {
 
-// Items aimed at for prompts, over all key/value heads, and the fewest tiles
-// of a split.
+// Items aimed at for prompts, over all key/value heads (two workgroups a CU; 256
+// leaves 24 x 128 rows at 80 us instead of 66, 1024 slows 4 x 512 queries on
+// 4000 tokens from 164 to 190 us by its partial sums), and the fewest tiles of
+// a split (1: the same; 16: 72 us instead of 66).
 constexpr int64_t PRO_ITEMS = 512;
 constexpr int PRO_MIN = 4;
 
@@ -1743,7 +1768,8 @@ wq_status wq_kv_attention(const void* q_bf16, int64_t q_stride, const int32_t* c
   if (!kv_sizes_ok(batch, tokens, max_q, q_heads, kv_heads, page, max_blocks) || num_pages < 1 || window < 0)
     return WQ_EINVAL;
   if (!(sm_scale > 0.0f) || !(sm_scale < INFINITY) || !(softcap >= 0.0f) || !(softcap < INFINITY)) return WQ_EINVAL;
-  if (softcap > 0.0f && (softcap < 0x1p-10f || softcap > 0x1p10f || !(sm_scale / softcap < 0x1p100f))) return WQ_EUNSUPPORTED;
+  if (softcap > 0.0f && (softcap < 0x1p-10f || softcap > 0x1p10f || !(sm_scale / softcap < 0x1p100f)))
+    return WQ_EUNSUPPORTED;
   const int64_t row = (int64_t)q_heads * head_dim;
   if (q_stride < row || q_stride % 8 || q_stride > (int64_t(1) << 40) ||
       !wq_numel_ok(num_pages, (int64_t)kv_heads * head_dim * page) || !wq_numel_ok(tokens ? tokens : 1, row) ||
@@ -1758,8 +1784,8 @@ wq_status wq_kv_attention(const void* q_bf16, int64_t q_stride, const int32_t* c
   if (ws_bytes < p.bytes || !workspace) return WQ_EINVAL;
   if (p.pro_items * kv_heads > 0x7FFFFFFF / PTHREADS) return WQ_EINVAL;
   const KvArgs A = {(const uint16_t*)q_bf16, q_stride, cu_q, kv_lens, batch, tokens, q_heads, kv_heads,
-                    q_heads / kv_heads, (int)(window < 0x7FFFFFFF ? window : 0), k_codes, k_scales, v_codes, v_scales, log2_page(page), num_pages, block_table,
-                    max_blocks, sm_scale, softcap, out, lse};
+                    q_heads / kv_heads, (int)(window < 0x7FFFFFFF ? window : 0), k_codes, k_scales, v_codes, v_scales,
+                    log2_page(page), num_pages, block_table, max_blocks, sm_scale, softcap, out, lse};
   uint8_t* ws = (uint8_t*)workspace;
   const KvShare dec = {p.groups, p.rows, (KvChain*)ws, (float*)(ws + p.dec_sums), (float*)(ws + p.dec_stats)};
   const KvPart pro = {p.pro_splits, p.pro_slots, PRO_MIN, (int64_t*)(ws + p.pro_used), (KvRec*)(ws + p.pro_rec),
