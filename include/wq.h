@@ -563,9 +563,9 @@ wq_status wq_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v
  *             memory, since a row's queries are read while others are written
  *             (an equal pointer is WQ_EINVAL).
  * lse         tokens x q_heads fp32 (output), or NULL.
- * workspace   wq_kv_attention_workspace_size bytes, 16-byte aligned, for this
- *             call alone while it runs; its contents need no preparation and
- *             mean nothing afterwards.
+ * workspace   wq_kv_attention_workspace_size bytes (NULL if that is 0), 16-byte
+ *             aligned, for this call alone while it runs; its contents need no
+ *             preparation and mean nothing afterwards.
  * Keys with NaN codes make the rows that see them NaN.  A NaN value code may
  * reach every row of its request: it is outside the contract.
  */
@@ -576,9 +576,10 @@ wq_status wq_kv_attention(const void* q_bf16, int64_t q_stride, const int32_t* c
                           int64_t max_blocks, float sm_scale, float softcap, int64_t window, uint16_t* out,
                           float* lse, void* workspace, size_t ws_bytes, void* stream);
 
-/* Bytes of workspace wq_kv_attention needs for this problem (0 for sizes it refuses). */
+/* Bytes of workspace wq_kv_attention needs for this problem: 0 where nothing is
+ * split, and for sizes it refuses. */
 size_t wq_kv_attention_workspace_size(int64_t batch, int64_t tokens, int64_t max_q, int32_t q_heads, int32_t kv_heads,
-                                      int32_t head_dim, int32_t page, int64_t max_blocks);
+                                      int32_t head_dim, int32_t page, int64_t max_blocks, int64_t window);
 
 #ifdef __cplusplus
 }

@@ -535,10 +535,11 @@ def test_serving_steps(W):
             assert (np.abs(got - want) <= 2 * 2.0 ** -4 * np.abs(want) + 2 * 2.0 ** -10 * unit).all()
 
 
-def test_decode_step_in_a_graph(W):
+@pytest.mark.parametrize("width", [6, 100])                # 100: wide enough that contexts are split
+def test_decode_step_in_a_graph(W, width):
     """One decode step captured once and replayed: every replay equals the eager step on the same state."""
-    banner("kv: graph replays of blocks, append and attention")
-    B, H, G, D, P, width = 5, 2, 4, 64, 16, 6
+    banner("kv: graph replays of blocks, append and attention", width)
+    B, H, G, D, P = 5, 2, 4, 64, 16
     gen = torch.Generator("cuda").manual_seed(1)
     N = B * width
     start = torch.tensor([0, 15, 16, 40, 70], dtype=torch.int32, device="cuda")

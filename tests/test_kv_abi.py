@@ -68,16 +68,16 @@ def test_attention_refusals(lib):
 
 def test_attention_workspace_is_asked_for(lib):
     size = lib.wq_kv_attention_workspace_size
-    ok = (3, 3, 1, 32, 8, 128, 64, 512)
+    ok = (3, 3, 1, 32, 8, 128, 64, 512, 0)
     need = size(*ok)
     args = lambda wsb, ws=P: lib.wq_kv_attention(P, 4096, P, P, 3, 3, 1, 32, 8, 128, P, P, P, P, 64, 10, P, 512, 0.1,
                                                  0.0, 0, P2, None, ws, wsb, None)
-    if need:
-        assert args(need - 1) == 1 and args(need, None) == 1
+    assert need > 0 and args(need - 1) == 1 and args(need, None) == 1
+    assert size(*ok[:7], 8, 0) == 0 and size(*ok[:8], 300) == 0        # short contexts and windows are not split
     # sizes the call refuses need nothing
-    for bad in ((-1, 3, 1, 32, 8, 128, 64, 512), (3, -3, 1, 32, 8, 128, 64, 512), (3, 3, 1, 30, 8, 128, 64, 512),
-                (3, 3, 1, 32, 0, 128, 64, 512), (3, 3, 1, 32, 8, 100, 64, 512), (3, 3, 1, 32, 8, 128, 7, 512),
-                (3, 3, 1, 32, 8, 128, 64, 0)):
+    for bad in ((-1, 3, 1, 32, 8, 128, 64, 512, 0), (3, -3, 1, 32, 8, 128, 64, 512, 0), (3, 3, 1, 30, 8, 128, 64, 512, 0),
+                (3, 3, 1, 32, 0, 128, 64, 512, 0), (3, 3, 1, 32, 8, 100, 64, 512, 0), (3, 3, 1, 32, 8, 128, 7, 512, 0),
+                (3, 3, 1, 32, 8, 128, 64, 0, 0), (3, 3, 1, 32, 8, 128, 64, 512, -1)):
         assert size(*bad) == 0, bad
 
 

@@ -58,7 +58,7 @@ _SIGS = {
                      ctypes.c_int),
     "wq_kv_attention": ([_vp, _i64, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i64, _vp,
                          _i64, ctypes.c_float, ctypes.c_float, _i64, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
-    "wq_kv_attention_workspace_size": ([_i64, _i64, _i64, _i32, _i32, _i32, _i32, _i64], _sz),
+    "wq_kv_attention_workspace_size": ([_i64, _i64, _i64, _i32, _i32, _i32, _i32, _i64, _i64], _sz),
     "wq_util_stream_read": ([_vp, _i64, ctypes.c_uint32, _vp, _vp], ctypes.c_int),
     "wq_util_spin": ([_i64, ctypes.c_uint32, _vp, _vp], ctypes.c_int),
     "wq_util_clock": ([_i64, _vp, _vp], ctypes.c_int),
@@ -516,8 +516,9 @@ def wq_kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_codes:
 
 
 def wq_kv_attention_workspace_size(batch: int, tokens: int, max_q: int, q_heads: int, kv_heads: int, head_dim: int,
-                                   page: int, max_blocks: int) -> int:
-    return int(lib.wq_kv_attention_workspace_size(batch, tokens, max_q, q_heads, kv_heads, head_dim, page, max_blocks))
+                                   page: int, max_blocks: int, window: int = 0) -> int:
+    return int(lib.wq_kv_attention_workspace_size(batch, tokens, max_q, q_heads, kv_heads, head_dim, page, max_blocks,
+                                                  window))
 
 
 def wq_kv_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
@@ -549,14 +550,15 @@ def wq_kv_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tens
         op = _shaped(out, dev, _bf16, (T, hq, dim), "out")
     lse = q.new_empty((T, hq), dtype=torch.float32) if return_lse else None
     if workspace is None:
-        ws_bytes = lib.wq_kv_attention_workspace_size(B, T, max_q, hq, h, dim, p, width)
-        workspace = q.new_empty(ws_bytes, dtype=_u8)
+        ws_bytes = lib.wq_kv_attention_workspace_size(B, T, max_q, hq, h, dim, p, width, window)
+        workspace = q.new_empty(ws_bytes, dtype=_u8) if ws_bytes else None
+        ws = workspace.data_ptr() if ws_bytes else None
     else:
-        _ptr(workspace, dev, workspace.dtype, "workspace")
+        ws = _ptr(workspace, dev, workspace.dtype, "workspace")
         ws_bytes = workspace.numel() * workspace.element_size()
     _launch(lib.wq_kv_attention, dev, "wq_kv_attention", q.data_ptr(), q_stride, cu, kl, B, T, max_q, hq, h, dim, kc,
             ks, vc, vs, p, n, table, width, sm_scale, softcap, window, op, lse.data_ptr() if return_lse else None,
-            workspace.data_ptr(), ws_bytes)
+            ws, ws_bytes)
     return (out, lse) if return_lse else out
 
 

@@ -573,6 +573,12 @@ constexpr int SHORT_ROWS = 64;
 // (256: 2-4 % slower on drafted tokens; 768 and 1024 at D = 64, where they fit:
 // 9 and 14 % slower on short windows).
 constexpr int DEC_GROUPS = 512;
+// A workgroup a row tile where no request can have more tiles than this (few row
+// tiles, enough of them for half the CUs) and they fit the chip twice over.  8
+// heads of 128, calls back to back: 1 x 700 tokens 12.8 us against 18.0 in
+// shares and a join, 1 x 2000 17 against 16; 16 x 2000 18.5 against 21.8, 16 x
+// 4000 30 against 31.
+constexpr int SOLO_TILES = 20, SOLO_TILES_MANY = 40;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 struct KvArgs {
@@ -621,7 +627,7 @@ struct KvChain {
   int32_t first_joined, last_joined;          // whether the workgroups of those joined their waves
 };
 struct KvShare {
-  int groups, rows;                           // workgroups per head, rows of a slot
+  int groups, rows;                           // workgroups per head (0: one a row tile), rows of a slot
   KvChain* chain;
   float* sums;
   float* stats;
@@ -803,7 +809,9 @@ __device__ __forceinline__ u32x4_t keep_tokens(u32x4_t v, int j, int lo, int hi)
 // one tile at most.  A share that begins or ends inside a row tile leaves
 // partial sums, which k_kv_join puts together; a workgroup whose waves are all
 // inside one row tile joins them in LDS first.  A row tile that sees nothing
-// counts as one tile, so that its rows are written.
+// counts as one tile, so that its rows are written.  Where no request has more
+// than a few tiles and the row tiles fit the chip, each gets a workgroup
+// instead (`solo`): the join's launch costs more than the tiles in turn do.
 //
 // 8 heads of 128, 4 query heads each: 64 x 8192 tokens 187 us (5.76 TB/s, 0.92
 // of a streaming read's rate); 64 x 2048-8192 tokens 105 us and 4.9 us joining.
@@ -821,19 +829,21 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
   const int x = 4 * group + wave;
   const KvChain none = {};
 
-  // all the work, and this wave's share [u0, u1) of it
+  // all the work, in tiles or in row tiles, and this wave's share [u0, u1) of it
+  const bool solo = part.groups == 0;
+  auto units_of = [&](const KvRequest& r) { return solo || r.tiles <= 0 ? 1 : r.tiles; };
   KvRequest lanes;
   int64_t total = 0;
   for (int64_t base = 0; base < A.batch; base += 64) {
     lanes.load<R, WHICH>(A, base + lane);
-    total += (int64_t)(lanes.tiles > 0 ? lanes.tiles : 1) * lanes.row_tiles;
+    total += (int64_t)units_of(lanes) * lanes.row_tiles;
   }
   total = lane64(wave_sum(total), 0);
-  const int64_t shares = total < 4 * part.groups ? total : 4 * part.groups;
-  auto share_at = [&](int64_t y) { return y < shares ? y * total / shares : total; };
+  const int64_t shares = solo ? 4 * total : total < 4 * part.groups ? total : 4 * part.groups;
+  auto share_at = [&](int64_t y) { return y >= shares ? total : solo ? y / 4 : y * total / shares; };
   const int64_t u0 = share_at(x), u1 = share_at(x + 1), g0 = share_at(4 * group), g1 = share_at(4 * group + 4);
   if (g0 >= g1) {                             // an idle workgroup
-    if (kvh == 0 && lane == 0) part.chain[x] = none;
+    if (!solo && kvh == 0 && lane == 0) part.chain[x] = none;
     return;
   }
   // the request that holds unit u, and its first unit
@@ -844,7 +854,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
     int64_t before = 0;
     for (int64_t base = 0; base < A.batch; base += 64) {
       if (A.batch > 64) lanes.load<R, WHICH>(A, base + lane);
-      const int64_t own = (int64_t)(lanes.tiles > 0 ? lanes.tiles : 1) * lanes.row_tiles;
+      const int64_t own = (int64_t)units_of(lanes) * lanes.row_tiles;
       const int64_t end = before + wave_scan(own, lane);
       const unsigned long long at = __ballot(end > u);
       if (at) {
@@ -858,9 +868,9 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
     }
   };
   find(g0);
-  auto units = [&]() { return q.tiles > 0 ? q.tiles : 1; };
+  auto units = [&]() { return units_of(q); };
   int rt = (int)((g0 - begin) / units());     // row tiles in order of their units, the last rows first
-  const bool joined = g1 <= begin + (int64_t)(rt + 1) * units();
+  const bool joined = g1 <= begin + (int64_t)(rt + 1) * units();   // always so if solo
   if (!joined) {
     if (u0 >= u1) {
       if (kvh == 0 && lane == 0) part.chain[x] = none;
@@ -870,7 +880,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
     rt = (int)((u0 - begin) / units());
   }
   if (q.row_tiles == 0) {                     // lengths that changed under the kernel
-    if (kvh == 0 && lane == 0) part.chain[x] = none;
+    if (!solo && kvh == 0 && lane == 0) part.chain[x] = none;
     return;
   }
 
@@ -896,7 +906,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
     int lo = kv_lowest(rows.pos0, A.window);
     lo = lo < hi ? lo : hi;
     const int lo_max = kv_lowest(row_max, A.window);
-    int t = q.first + (int)((joined ? g0 : u) - row_begin), t1 = q.first + (int)((joined ? g1 : stop) - row_begin);
+    int t = q.first + (int)((joined ? g0 : u) - row_begin), t1 = q.first + (solo ? q.tiles : (int)((joined ? g1 : stop) - row_begin));
     t = t < lo / TILE ? lo / TILE : t;
     t1 = t1 > (hi + TILE - 1) / TILE ? (hi + TILE - 1) / TILE : t1;
     t += joined ? wave : 0;
@@ -1136,7 +1146,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
     }
     break;
   }
-  if (kvh == 0 && lane == 0) part.chain[x] = chain;
+  if (!solo && kvh == 0 && lane == 0) part.chain[x] = chain;
 }
 
 // Prompts and chunks: 128 rows per workgroup, 32 per wave.  Bound by the
@@ -1678,7 +1688,7 @@ constexpr int PRO_MIN = 4;
 // allow.  The decode kernel has as many workgroups as the chip holds at once
 // (two a CU, as its registers allow), or one a head.
 struct KvPlan {
-  bool prompt;
+  bool prompt, solo;                          // solo: decode only, a workgroup a row tile, nothing to join
   int nr;                                     // 16-row columns of a decode tile
   int groups, rows;                           // decode workgroups per head, rows of its slots
   int64_t pro_splits, pro_items, pro_slots;
@@ -1686,16 +1696,21 @@ struct KvPlan {
 };
 
 KvPlan kv_plan(int64_t batch, int64_t tokens, int64_t max_q, int q_heads, int kv_heads, int head_dim, int page,
-               int64_t max_blocks) {
+               int64_t max_blocks, int64_t window) {
   KvPlan p = {};
   const int64_t group = q_heads / kv_heads, reqs = batch < tokens ? batch : tokens;
   const int64_t tiles = (max_blocks * page + TILE - 1) / TILE;
   const int64_t most_q = max_q > 0 && max_q < tokens ? max_q : tokens;
   p.prompt = most_q * group > SHORT_ROWS;
   p.nr = most_q * group <= 16 ? 1 : 2;
-  const int64_t wgs = DEC_GROUPS / kv_heads;
-  p.groups = (int)(wgs > 1 ? wgs : 1);
   p.rows = 16 * p.nr;
+  const int64_t wgs = DEC_GROUPS / kv_heads, row_tiles = tokens * group / p.rows + reqs;
+  const int64_t seen = window > 0 && window < tiles * TILE ? (window + most_q - 2) / TILE + 2 : tiles;
+  const int64_t work = row_tiles * kv_heads;
+  p.solo = !p.prompt && (seen < tiles ? seen : tiles) <= (work < DEC_GROUPS / 4 ? SOLO_TILES : SOLO_TILES_MANY) &&
+           work <= 2 * DEC_GROUPS;
+  p.groups = (int)(p.solo ? row_tiles : wgs > 1 ? wgs : 1);
+  if (p.solo) return p;
   p.pro_splits = (PRO_ITEMS + kv_heads - 1) / kv_heads;
   const int64_t pro_rows = p.prompt ? tokens * group / PROWS + reqs : 0;
   p.pro_items = p.prompt ? pro_rows + p.pro_splits : 0;
@@ -1741,6 +1756,7 @@ void launch_attention(const KvArgs& A, const KvPlan& p, const KvShare& dec, cons
   } else {
     k_kv_decode<D, CAP, REQ_ALL, 1><<<groups, KV_THREADS, 0, s>>>(A, dec);
   }
+  if (p.solo) return;
   const unsigned joins = 4 * groups * p.nr + (unsigned)(p.pro_slots * (PROWS / 16)) * h;
   if (p.nr == 2) k_kv_join<D, 2><<<joins, KV_THREADS, 0, s>>>(A, dec, pro);
   else k_kv_join<D, 1><<<joins, KV_THREADS, 0, s>>>(A, dec, pro);
@@ -1751,11 +1767,11 @@ void launch_attention(const KvArgs& A, const KvPlan& p, const KvShare& dec, cons
 extern "C" {
 
 size_t wq_kv_attention_workspace_size(int64_t batch, int64_t tokens, int64_t max_q, int32_t q_heads, int32_t kv_heads,
-                                      int32_t head_dim, int32_t page, int64_t max_blocks) {
-  if ((head_dim != 64 && head_dim != 128) || log2_page(page) < 0 ||
+                                      int32_t head_dim, int32_t page, int64_t max_blocks, int64_t window) {
+  if (window < 0 || (head_dim != 64 && head_dim != 128) || log2_page(page) < 0 ||
       !kv_sizes_ok(batch, tokens, max_q, q_heads, kv_heads, page, max_blocks))
     return 0;
-  return kv_plan(batch, tokens, max_q, q_heads, kv_heads, head_dim, page, max_blocks).bytes;
+  return batch && tokens ? kv_plan(batch, tokens, max_q, q_heads, kv_heads, head_dim, page, max_blocks, window).bytes : 0;
 }
 
 wq_status wq_kv_attention(const void* q_bf16, int64_t q_stride, const int32_t* cu_q, const int32_t* kv_lens,
@@ -1780,14 +1796,14 @@ wq_status wq_kv_attention(const void* q_bf16, int64_t q_stride, const int32_t* c
   if (!wq_aligned(q_bf16) || !wq_aligned(out) || !wq_aligned(k_codes) || !wq_aligned(v_codes) || !wq_aligned(workspace))
     return WQ_EALIGN;
   if (batch == 0 || tokens == 0) return WQ_OK;               // nothing to compute
-  const KvPlan p = kv_plan(batch, tokens, max_q, q_heads, kv_heads, head_dim, page, max_blocks);
-  if (ws_bytes < p.bytes || !workspace) return WQ_EINVAL;
+  const KvPlan p = kv_plan(batch, tokens, max_q, q_heads, kv_heads, head_dim, page, max_blocks, window);
+  if (p.bytes > 0 && (ws_bytes < p.bytes || !workspace)) return WQ_EINVAL;
   if (p.pro_items * kv_heads > 0x7FFFFFFF / PTHREADS) return WQ_EINVAL;
   const KvArgs A = {(const uint16_t*)q_bf16, q_stride, cu_q, kv_lens, batch, tokens, q_heads, kv_heads,
                     q_heads / kv_heads, (int)(window < 0x7FFFFFFF ? window : 0), k_codes, k_scales, v_codes, v_scales,
                     log2_page(page), num_pages, block_table, max_blocks, sm_scale, softcap, out, lse};
   uint8_t* ws = (uint8_t*)workspace;
-  const KvShare dec = {p.groups, p.rows, (KvChain*)ws, (float*)(ws + p.dec_sums), (float*)(ws + p.dec_stats)};
+  const KvShare dec = {p.solo ? 0 : p.groups, p.rows, (KvChain*)ws, (float*)(ws + p.dec_sums), (float*)(ws + p.dec_stats)};
   const KvPart pro = {p.pro_splits, p.pro_slots, PRO_MIN, (int64_t*)(ws + p.pro_used), (KvRec*)(ws + p.pro_rec),
                       (float*)(ws + p.pro_sums), (float*)(ws + p.pro_stats)};
   hipStream_t s = (hipStream_t)stream;
