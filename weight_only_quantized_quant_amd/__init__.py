@@ -411,7 +411,7 @@ _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch.cuda.cu
 
 def _ptr(t, dev, dtype, name):
     """The address of a contiguous tensor of `dtype` on GPU `dev`."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
         _dev(t, name)
         if t.dtype != dtype:
             raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
@@ -453,18 +453,31 @@ def _token_rows(t, name):
     return t.get_device(), n, h, d, sn if n > 1 else h * d
 
 
-def _kv_cache(k_codes, k_scales, v_codes, v_scales, dev):
-    """(num_pages, heads, page, head_dim) of a cache and the addresses of its four tensors."""
-    kc, ks = _ptr(k_codes, dev, _u8, "k_codes"), _ptr(k_scales, dev, _u8, "k_scales")
-    vc, vs = _ptr(v_codes, dev, _u8, "v_codes"), _ptr(v_scales, dev, _u8, "v_scales")
+def _refuse_cache(k_codes, k_scales, v_codes, v_scales, dev):
+    """Says what is wrong with a cache."""
+    for t, name in ((k_codes, "k_codes"), (k_scales, "k_scales"), (v_codes, "v_codes"), (v_scales, "v_scales")):
+        _ptr(t, dev, _u8, name)
     if k_codes.dim() != 4:
         raise ValueError("k_codes must be [num_pages, heads, page, head_dim]")
     n, h, p, d = k_codes.shape
     if v_codes.shape != (n, h, d, p):
         raise ValueError("v_codes must be [num_pages, heads, head_dim, page]")
-    if k_scales.shape != (n, h) or v_scales.shape != (n, h):
-        raise ValueError("k_scales and v_scales must be [num_pages, heads]")
-    return n, h, p, d, kc, ks, vc, vs
+    raise ValueError("k_scales and v_scales must be [num_pages, heads]")
+
+
+def _kv_cache(kc, ks, vc, vs, dev):
+    """(num_pages, heads, page, head_dim) of a cache and the addresses of its four tensors."""
+    try:
+        n, h, p, d = kc.shape
+        good = (kc.dtype is _u8 and ks.dtype is _u8 and vc.dtype is _u8 and vs.dtype is _u8 and kc.get_device() == dev
+                and ks.get_device() == dev and vc.get_device() == dev and vs.get_device() == dev
+                and kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and vs.is_contiguous()
+                and vc.shape == (n, h, d, p) and ks.shape == (n, h) and vs.shape == (n, h))
+    except (AttributeError, ValueError):
+        good = False
+    if not good:
+        _refuse_cache(kc, ks, vc, vs, dev)
+    return n, h, p, d, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr()
 
 
 def wq_kv_blocks(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor, block_table: torch.Tensor,
