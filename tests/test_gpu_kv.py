@@ -371,6 +371,17 @@ def test_attention_extreme_scores(W):
         _check_attention(W, q, cu, kv, cache, table, sm_scale=1e-3)
 
 
+@pytest.mark.parametrize("ql", [[1, 3, 1], [40, 1, 90]])
+@pytest.mark.parametrize("softcap,sm_scale", [(2.0, 1.0), (30.0, 0.5), (1000.0, 0.05), (0.002, 0.01), (50.0, 1e-4)])
+def test_attention_caps(W, ql, softcap, sm_scale):
+    """Scores far above their cap and far below it, in one tile and apart."""
+    banner("kv attention: caps", ql, softcap, sm_scale)
+    q, cu, kv, cache, table = _problem(17, 8, 2, 64, 16, ql, [300, 70, 500])
+    cache[1][:] = np.random.default_rng(17).integers(110, 128, cache[1].shape)
+    cache[0][:] = np.where((cache[0] & 0x78) > 0x50, cache[0] & 0x87, cache[0])   # keys of up to 30, most below 1
+    _check_attention(W, q, cu, kv, cache, table, softcap=softcap, sm_scale=sm_scale)
+
+
 def test_attention_strided_queries(W):
     banner("kv attention: queries as slices of wider rows")
     q, cu, kv, cache, table = _problem(9, 8, 2, 64, 16, [1, 40, 3], [50, 40, 9])

@@ -53,7 +53,7 @@ def test_attention_refusals(lib):
         return lib.wq_kv_attention(q, qs, cu, kv, batch, tokens, max_q, hq, hk, dim, kc, ksc, vc, vsc, page, pages,
                                    table, width, sm, cap, window, out, lse, ws, wsb, None)
     assert call(dim=32) == 3 and call(page=20) == 3
-    assert call(cap=2000.0, out=P2) == 3 and call(cap=1e-4, out=P2) == 3
+    assert call(cap=2000.0, out=P2) == 3 and call(cap=1e-4, out=P2) == 3 and call(cap=1.0, sm=20000.0) == 3
     inf, nan = float("inf"), float("nan")
     for bad in ({"batch": -1}, {"tokens": -1}, {"max_q": -1}, {"hk": 0}, {"hq": 6}, {"hq": 2}, {"pages": 0},
                 {"width": 0}, {"width": 1 << 26}, {"window": -1}, {"sm": 0.0}, {"sm": -1.0}, {"sm": inf}, {"sm": nan},
