@@ -628,6 +628,7 @@ struct KvChain {
 };
 struct KvShare {
   int groups, rows;                           // workgroups per head (0: one a row tile), rows of a slot
+  int log_joins;                              // log2 of the workgroups of k_kv_join for a row tile
   KvChain* chain;
   float* sums;
   float* stats;
@@ -1530,17 +1531,17 @@ __global__ __launch_bounds__(PTHREADS, 2) void k_kv_prompt(const KvArgs A, const
   if (A.lse && h == 0) A.lse[orow] = l == 0.0f ? -INFINITY : (mx + __builtin_log2f(l)) * LN2;
 }
 
-// Joins `parts` partial results of rows [row0, row0 + 16) of one head, a wave
+// Joins `parts` partial results of rows [row0, row0 + some) of one head, a wave
 // taking every fourth row: its lanes hold 4 channels each, and the groups of
 // lanes that this leaves share the parts, 4 of them in flight per lane, since a
 // long context alone in its batch has many parts of few rows.  slot_of(i) is
 // the place of part i among the slots of `room` rows.
 template <int D, typename SLOT>
 __device__ __forceinline__ void kv_join(const KvArgs& A, const float* sums, const float* stats, int room, int kvh,
-                                        int row0, int rows, int query0, int head0, int parts, SLOT slot_of) {
+                                        int row0, int some, int rows, int query0, int head0, int parts, SLOT slot_of) {
   constexpr int LANES = D / 4, GROUPS = 64 / LANES, DEEP = 4;
   const int lane = threadIdx.x & 63, grp = lane / LANES, ch = (lane % LANES) * 4;
-  for (int row = row0 + threadIdx.x / 64; row < row0 + 16 && row < rows; row += KV_THREADS / 64) {
+  for (int row = row0 + threadIdx.x / 64; row < row0 + some && row < rows; row += KV_THREADS / 64) {
     float M = -INFINITY, L = 0.0f;
     f32x4_t acc = {0, 0, 0, 0};
     for (int s0 = grp; s0 < parts; s0 += GROUPS * DEEP) {
@@ -1590,34 +1591,37 @@ __device__ __forceinline__ void kv_join(const KvArgs& A, const float* sums, cons
   }
 }
 
-// Workgroups of the decode kernel's waves first (NR each), then PROWS / 16 for
-// each prompt slot.
+// Workgroups of the decode kernel's waves first, 2^log_joins each, then
+// PROWS / 16 for each prompt slot.  8 rows each where more than 8 are likely (24
+// requests of 1-7 drafted tokens 10.2 -> 8.2 us), 16 else, since most of these
+// workgroups find nothing (64 requests of 4 rows 4.6 us, 5.8 in eights).
 template <int D, int NR>
 __global__ __launch_bounds__(KV_THREADS) void k_kv_join(const KvArgs A, const KvShare dec, const KvPart pro) {
   const int kvh = (int)(blockIdx.x % (unsigned)A.kv_heads);
   int64_t x = blockIdx.x / (unsigned)A.kv_heads;
-  const int64_t waves = 4 * (int64_t)dec.groups;
-  if (x < waves * NR) {
-    const KvChain c = dec.chain[x / NR];
+  const int64_t decode = 4 * (int64_t)dec.groups << dec.log_joins;
+  if (x < decode) {
+    const KvChain c = dec.chain[x >> dec.log_joins];
+    const int some = 16 * NR >> dec.log_joins, row0 = (int)(x & ((1 << dec.log_joins) - 1)) * some;
     if (c.rows == 0) return;
     // parts: the first workgroup's, one for each between, the last workgroup's
     const int ga = c.first / 4, gz = c.last / 4;
     const int a = c.first_joined ? 1 : (gz > ga ? 4 * ga + 3 : c.last) - c.first + 1;
     const int mid = gz > ga ? gz - ga - 1 : 0, z = gz > ga ? (c.last_joined ? 1 : c.last - 4 * gz + 1) : 0;
-    kv_join<D>(A, dec.sums, dec.stats, dec.rows, kvh, (int)(x % NR) * 16, c.rows, c.query0, c.head0, a + mid + z,
+    kv_join<D>(A, dec.sums, dec.stats, dec.rows, kvh, row0, some, c.rows, c.query0, c.head0, a + mid + z,
                [&](int i) -> int64_t {
                  if (i < a) return i == 0 ? 2 * c.first : 2 * (c.first + i) + 1;
                  return i < a + mid ? 8 * (ga + 1 + i - a) + 1 : 2 * (4 * gz + i - a - mid) + 1;
                });
     return;
   }
-  x -= waves * NR;
+  x -= decode;
   const int64_t slot = x / (PROWS / 16);
   if (slot >= pro.used[0]) return;
   const KvRec rec = pro.rec[slot];
   // entries that ranges of rows on top of each other left unwritten hold anything
   if (rec.splits <= 0 || slot + rec.splits > pro.slots || rec.rows > PROWS) return;
-  kv_join<D>(A, pro.sums, pro.stats, PROWS, kvh, (int)(x % (PROWS / 16)) * 16, rec.rows, rec.query0, rec.head0, rec.splits,
+  kv_join<D>(A, pro.sums, pro.stats, PROWS, kvh, (int)(x % (PROWS / 16)) * 16, 16, rec.rows, rec.query0, rec.head0, rec.splits,
              [&](int i) -> int64_t { return slot + i; });
 }
 
@@ -1717,7 +1721,7 @@ constexpr int PRO_MIN = 4;
 struct KvPlan {
   bool prompt, solo;                          // solo: decode only, a workgroup a row tile, nothing to join
   int nr;                                     // 16-row columns of a decode tile
-  int groups, rows;                           // decode workgroups per head, rows of its slots
+  int groups, rows, log_joins;                // decode workgroups per head, rows of its slots, joins a row tile
   int64_t pro_splits, pro_items, pro_slots;
   size_t dec_sums, dec_stats, pro_used, pro_rec, pro_sums, pro_stats, bytes;
 };
@@ -1731,6 +1735,7 @@ KvPlan kv_plan(int64_t batch, int64_t tokens, int64_t max_q, int q_heads, int kv
   p.prompt = most_q * group > SHORT_ROWS;
   p.nr = most_q * group <= 16 ? 1 : 2;
   p.rows = 16 * p.nr;
+  p.log_joins = (p.nr == 2) + (!p.prompt && most_q * group > 8);
   const int64_t wgs = DEC_GROUPS / kv_heads, row_tiles = tokens * group / p.rows + reqs;
   const int64_t seen = window > 0 && window < tiles * TILE ? (window + most_q - 2) / TILE + 2 : tiles;
   const int64_t work = row_tiles * kv_heads;
@@ -1784,7 +1789,7 @@ void launch_attention(const KvArgs& A, const KvPlan& p, const KvShare& dec, cons
     k_kv_decode<D, CAP, REQ_ALL, 1><<<groups, KV_THREADS, 0, s>>>(A, dec);
   }
   if (p.solo) return;
-  const unsigned joins = 4 * groups * p.nr + (unsigned)(p.pro_slots * (PROWS / 16)) * h;
+  const unsigned joins = (4 * groups << p.log_joins) + (unsigned)(p.pro_slots * (PROWS / 16)) * h;
   if (p.nr == 2) k_kv_join<D, 2><<<joins, KV_THREADS, 0, s>>>(A, dec, pro);
   else k_kv_join<D, 1><<<joins, KV_THREADS, 0, s>>>(A, dec, pro);
 }
@@ -1830,7 +1835,7 @@ wq_status wq_kv_attention(const void* q_bf16, int64_t q_stride, const int32_t* c
                     q_heads / kv_heads, (int)(window < 0x7FFFFFFF ? window : 0), k_codes, k_scales, v_codes, v_scales,
                     log2_page(page), num_pages, block_table, max_blocks, sm_scale, softcap, out, lse};
   uint8_t* ws = (uint8_t*)workspace;
-  const KvShare dec = {p.solo ? 0 : p.groups, p.rows, (KvChain*)ws, (float*)(ws + p.dec_sums), (float*)(ws + p.dec_stats)};
+  const KvShare dec = {p.solo ? 0 : p.groups, p.rows, p.log_joins, (KvChain*)ws, (float*)(ws + p.dec_sums), (float*)(ws + p.dec_stats)};
   const KvPart pro = {p.pro_splits, p.pro_slots, PRO_MIN, (int64_t*)(ws + p.pro_used), (KvRec*)(ws + p.pro_rec),
                       (float*)(ws + p.pro_sums), (float*)(ws + p.pro_stats)};
   hipStream_t s = (hipStream_t)stream;
