@@ -291,6 +291,8 @@ SHAPES = [
     (8, 2, 128, 64, [200], [520]),
     (4, 4, 128, 128, [300], [300]),
     (6, 2, 64, 64, [129, 70], [129, 1000]),
+    (128, 1, 64, 64, [1, 1, 2], [700, 90, 64]),            # more rows than a decode tile takes, for one token
+    (66, 2, 128, 16, [1, 1], [40, 1500]),
 ]
 
 
