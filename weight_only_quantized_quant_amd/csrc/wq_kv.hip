@@ -1197,7 +1197,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
 // scales and addresses are scalars, which takes a fifth of the loop's vector
 // instructions away (330 -> 323 us, capped 688 -> 654 us).
 //
-// Three prompts of 1500-4096 tokens, 32 heads of 128 on 8: 306-314 us (840-863
+// Three prompts of 1500-4096 tokens, 32 heads of 128 on 8: 306-319 us (828-863
 // TFLOP/s; matrix cores busy 0.37, vector units 0.46 of the cycles, no LDS bank
 // conflicts).  Power sets the clock: a tenth fewer cycles took 3 % off the time.
 template <int D, bool CAP, bool BIG>
