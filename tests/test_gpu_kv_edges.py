@@ -1,0 +1,73 @@
+"""The 8-bit key/value cache where it can go wrong unseen: softmaxes whose
+weights are spread over many tokens, small ratios of scale and cap, bytes that
+no row or not every row sees, NaN and infinite values, caller-owned workspaces."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv as OK
+from oracle.e4m3 import e4m3_from_f32
+from oracle.formats import bf16_decode, bf16_round
+from tests.gpu_helpers import banner, dev_bf16, dev_u8, host_bits16, host_f32
+from tests.test_gpu_kv import W, _bounds, _i32, _problem  # noqa: F401 (W is a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def _spread_problem(seed, Hq, H, D, P, q_lens, kv_lens, spare_cols=1):
+    """Scores of a standard deviation of 1.5 at the default scale: keys and values quantized from
+    normal numbers, page scales up to 2^6 apart."""
+    q, cu, kv, cache, table = _problem(seed, Hq, H, D, P, q_lens, kv_lens, spare_cols=spare_cols)
+    g = np.random.default_rng(seed + 1000)
+    N = len(cache[1])
+    out = []
+    for shape in ((N, H, P, D), (N, H, D, P)):
+        c = g.integers(124, 131, (N, H))
+        x = g.standard_normal(shape)
+        out += [e4m3_from_f32(np.ldexp(x, 127 - c[..., None, None]).astype(np.float32)), c.astype(np.uint8)]
+    return 3 * q, cu, kv, out, table
+
+
+def _attend(W, q, cu, kv, cache, table, **kw):
+    """Bits of out and of lse."""
+    out, lse = W.wq_kv_attention(dev_bf16(bf16_round(q)), *[dev_u8(c) for c in cache], _i32(table), _i32(cu), _i32(kv),
+                                 return_lse=True, **kw)
+    torch.cuda.synchronize()
+    return host_bits16(out), host_f32(lse).view(np.uint32)
+
+
+def _compare(bits, lse_bits, q, cu, kv, cache, table, sm_scale=None, softcap=0.0, window=0):
+    """Within the bound of the roundings; a capped score is off by softcap * 2^-22 more."""
+    D = q.shape[2]
+    ref, rl, weight, spread = OK.attention(bf16_decode(bf16_round(q)), cu, kv, *cache, table,
+                                           D ** -0.5 if sm_scale is None else sm_scale, softcap, window)
+    seen = int(max(kv))
+    e = softcap * 2.0 ** -22
+    tol, tol_lse = _bounds(ref, weight, spread + e / ((D + 16) * 2.0 ** -24), seen, D)
+    y, l = bf16_decode(bits), lse_bits.view(np.float32).astype(np.float64)
+    some = ~np.isneginf(rl)                                   # rows that see a token
+    assert np.array_equal(np.isfinite(l), some) and np.isneginf(l[~some]).all() and (y[~some] == 0).all()
+    assert np.isfinite(y).all()
+    worst = (np.abs(y - ref) / tol).max()
+    assert worst <= 1.0, f"output: error / bound = {worst:.3f}"
+    worst = (np.abs(l - rl)[some] / (tol_lse + 2.0 ** -22 * np.abs(rl))[some]).max()
+    assert worst <= 1.0, f"lse: error / bound = {worst:.3f}"
+
+
+# ---------------------------------------------------------------------------
+# capped scores
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("ql", [[1, 3], [70, 1]])
+@pytest.mark.parametrize("log_k", [10, 20, 32, 66, 90])
+@pytest.mark.parametrize("log_x", [-8, -7, -4])               # below a quarter of the cap, about it, above it
+def test_attention_cap_of_a_small_scale(W, ql, log_k, log_x):
+    """sm_scale / softcap far below 1, beside keys whose scales make up for it: dots of 2^log_k."""
+    banner("kv attention: scale / cap of 2^-", log_k, log_x, ql)
+    q, cu, kv, cache, table = _spread_problem(31, 8, 2, 64, 16, ql, [300, 70])
+    g = np.random.default_rng(31)
+    q = np.abs(q) / 3                                         # dots of one sign: what the cap takes away adds up
+    cache[0] = g.integers(0x28, 0x40, cache[0].shape).astype(np.uint8)
+    cache[1][:] = 127 + log_k + log_x
+    for softcap in (1.0, 300.0):
+        kw = {"softcap": softcap, "sm_scale": softcap * 2.0 ** -log_k}
+        _compare(*_attend(W, q, cu, kv, cache, table, **kw), q, cu, kv, cache, table, **kw)

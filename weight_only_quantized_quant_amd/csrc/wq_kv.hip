@@ -764,8 +764,14 @@ __device__ __forceinline__ void kv_tiles(const KvArgs& A, const KvItem& it, cons
 // sm_scale / cap.  Sixteen at a time: where all of a wave's have |x| <= 1/4 (most
 // scores are far below their cap), by the series of tanh up to x^7, whose next
 // term is under 3.4e-7 of the result; else as cap - 2 cap / (e^2x + 1), off by
-// at most cap * 2^-22.  Both take the same time (chunks 555 us); the series
-// keeps small scores exact (lse off by 5e-8 instead of 2.5e-7, 2-norm).
+// at most cap * 2^-22.  Both take the same time (chunks 560 us); the series
+// keeps small scores exact (lse off by 5e-8 instead of 2.5e-7, 2-norm).  It is
+// taken in powers of the dot, with k = sm_scale / cap in its coefficients: for k
+// from 2^-16 on (softcap 50 at heads of 128 has 2^-9) the squares of dots of up
+// to 1 / 4k and the coefficient of k^7 are in fp32's range with 2^20 to spare
+// against the bound.  A smaller k leaves it, so its scores all go by the
+// exponential.  (A series in x itself holds for every k but takes a
+// multiplication more a score: chunks 581 us.)
 template <bool CAP>
 struct KvScore {
   float mul;                                  // of what `cap` leaves
@@ -774,7 +780,7 @@ struct KvScore {
     mul = CAP ? 1.0f : A.sm_scale * LOG2E;
     if constexpr (CAP) {
       const float k = A.sm_scale / A.softcap, k2 = k * k;
-      limit = 0.25f / k;
+      limit = k >= 0x1p-16f ? 0.25f / k : 0.0f;
       to2x = 2.0f * LOG2E * k;
       twice = A.softcap * LOG2E;
       a0 = A.sm_scale * LOG2E;
