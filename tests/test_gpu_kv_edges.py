@@ -71,3 +71,39 @@ def test_attention_cap_of_a_small_scale(W, ql, log_k, log_x):
     for softcap in (1.0, 300.0):
         kw = {"softcap": softcap, "sm_scale": softcap * 2.0 ** -log_k}
         _compare(*_attend(W, q, cu, kv, cache, table, **kw), q, cu, kv, cache, table, **kw)
+
+
+# ---------------------------------------------------------------------------
+# bytes that no row sees
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("Hq,H,D,P,ql", [(8, 2, 128, 64, [1, 1, 1]), (4, 4, 64, 16, [1, 3, 2]), (8, 2, 64, 128, [5, 1, 4]),
+                                         (8, 2, 128, 64, [90, 1, 40]), (4, 2, 64, 32, [130, 3, 70])])
+@pytest.mark.parametrize("softcap", [0.0, 50.0])
+def test_attention_does_not_depend_on_bytes_no_row_sees(W, Hq, H, D, P, ql, softcap):
+    """Stale keys and values behind a request's length, before its window and in page 0, which is
+    read in place of a missing page: large ones give the bits that zeros give."""
+    banner("kv attention: unseen bytes", Hq, H, D, P, ql, softcap)
+    kl, window = [331, 90, 301], 150
+    q, cu, kv, cache, table = _spread_problem(32, Hq, H, D, P, ql, kl)
+    table = np.where(table >= 0, table + 1, -1)               # page 0 is nobody's
+    cache = [np.concatenate([c[:1], c]) for c in cache]
+    table[2, 300 // P - 1] = -1
+    for win in (0, window):
+        seen = np.zeros((len(cache[1]), P), bool)
+        for i, m in enumerate(kl):
+            for j in range(max(0, m - ql[i] - win + 1) if win else 0, m):
+                if table[i, j // P] >= 0:
+                    seen[table[i, j // P], j % P] = True
+        got = []
+        for code in (0x00, 0x7E, 0xFE):
+            c = [x.copy() for x in cache]
+            c[0][np.nonzero(~seen)[0], :, np.nonzero(~seen)[1]] = code
+            c[2].transpose(0, 3, 1, 2)[~seen] = code
+            got.append(_attend(W, q, cu, kv, c, table, softcap=softcap, window=win))
+        for name, at in (("out", 0), ("lse", 1)):
+            for other in got[1:]:
+                assert np.array_equal(got[0][at], other[at]), (name, win)
+        # what the zeros give is right
+        zeros = [x.copy() for x in cache]
+        zeros[0][np.nonzero(~seen)[0], :, np.nonzero(~seen)[1]] = 0
+        _compare(*got[0], q, cu, kv, zeros, table, softcap=softcap, window=win)

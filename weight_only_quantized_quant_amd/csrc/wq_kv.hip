@@ -789,22 +789,31 @@ struct KvScore {
       a3 = a0 * k2 * k2 * k2 * (-17.0f / 315.0f);
     }
   }
+  __device__ __forceinline__ float series(float s) const {
+    const float y = s * s;
+    return s * __builtin_fmaf(__builtin_fmaf(__builtin_fmaf(a3, y, a2), y, a1), y, a0);
+  }
+  __device__ __forceinline__ float exponential(float s) const {
+    return __builtin_fmaf(__builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(s * to2x) + 1.0f), -2.0f * twice, twice);
+  }
+  // `edge`: some of the sixteen are of tokens that their row does not see.  The form
+  // of one that it does see must not follow their bytes, so each goes by itself then
+  // (the series where all are below the limit is what each would take).
   template <typename T>
-  __device__ __forceinline__ void cap(T& s, int n) const {
+  __device__ __forceinline__ void cap(T& s, bool edge) const {
     if constexpr (CAP) {
       float big = 0.0f;
 #pragma unroll
-      for (int i = 0; i < n; i++) big = __builtin_fmaxf(big, __builtin_fabsf(s[i]));
-      if (__any(big > limit)) {
+      for (int i = 0; i < 16; i++) big = __builtin_fmaxf(big, __builtin_fabsf(s[i]));
+      if (!__any(big > limit)) {
 #pragma unroll
-        for (int i = 0; i < n; i++)
-          s[i] = __builtin_fmaf(__builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(s[i] * to2x) + 1.0f), -2.0f * twice, twice);
+        for (int i = 0; i < 16; i++) s[i] = series(s[i]);
+      } else if (!edge) {
+#pragma unroll
+        for (int i = 0; i < 16; i++) s[i] = exponential(s[i]);
       } else {
 #pragma unroll
-        for (int i = 0; i < n; i++) {
-          const float y = s[i] * s[i];
-          s[i] *= __builtin_fmaf(__builtin_fmaf(__builtin_fmaf(a3, y, a2), y, a1), y, a0);
-        }
+        for (int i = 0; i < 16; i++) s[i] = __builtin_fabsf(s[i]) > limit ? exponential(s[i]) : series(s[i]);
       }
     }
   }
@@ -1045,7 +1054,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
           float v[16];
 #pragma unroll
           for (int i = 0; i < 16; i++) v[i] = s[c][i >> 2][i & 3];
-          sc.cap(v, 16);
+          sc.cap(v, edge);
 #pragma unroll
           for (int i = 0; i < 16; i++) s[c][i >> 2][i & 3] = v[i];
         }
@@ -1206,8 +1215,11 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
 // Three prompts of 1500-4096 tokens, 32 heads of 128 on 8: 306-319 us (828-863
 // TFLOP/s; matrix cores busy 0.37, vector units 0.46 of the cycles, no LDS bank
 // conflicts).  Power sets the clock: a tenth fewer cycles took 3 % off the time.
+//
+// Registers allow two waves a SIMD at heads of 128 and three at heads of 64, where
+// capped scores need that said (the same three prompts: 282 us at two, 251 at three).
 template <int D, bool CAP, bool BIG>
-__global__ __launch_bounds__(PTHREADS, 2) void k_kv_prompt(const KvArgs A, const KvPart part) {
+__global__ __launch_bounds__(PTHREADS, D == 64 ? 3 : 2) void k_kv_prompt(const KvArgs A, const KvPart part) {
   constexpr int KS = D / 16, DT = D / 32;     // k steps, channel tiles
   constexpr int XK = D == 128 ? 1 : 2;
   constexpr int ST = D / 64;                  // 16-byte pieces of K, and of V^T, a thread
@@ -1409,9 +1421,10 @@ __global__ __launch_bounds__(PTHREADS, 2) void k_kv_prompt(const KvArgs A, const
   // the result is the same
   auto settle = [&](int t, int u, f32x16_t& s) {
     const int j0 = t * TILE + 32 * u;
-    sc.cap(s, 16);
     const bool ok = there(BIG ? ids[0] : idm[u]);
-    if (j0 + 31 > w_min || j0 < w_lo_max || (BIG ? !ok : __any(!ok))) {
+    const bool edge = j0 + 31 > w_min || j0 < w_lo_max || (BIG ? !ok : __any(!ok));
+    sc.cap(s, edge);
+    if (edge) {
       const int j = j0 + 16 * h, z = ok ? pos - j : -1, b = rlo - j;
 #pragma unroll
       for (int i = 0; i < 16; i++) s[i] = i <= z && i >= b ? s[i] : -INFINITY;
