@@ -567,8 +567,9 @@ wq_status wq_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v
  * workspace   wq_kv_attention_workspace_size bytes (NULL if that is 0), 16-byte
  *             aligned, for this call alone while it runs; its contents need no
  *             preparation and mean nothing afterwards.
- * Keys with NaN codes make the rows that see them NaN.  A NaN value code may
- * reach every row of its request: it is outside the contract.
+ * Keys with NaN codes make the rows that see them NaN.  A value that is not
+ * finite (a NaN code, or one that its scale takes past bf16) makes its channel
+ * of the rows that see its token NaN or infinite.  Other rows do not change.
  */
 wq_status wq_kv_attention(const void* q_bf16, int64_t q_stride, const int32_t* cu_q, const int32_t* kv_lens,
                           int64_t batch, int64_t tokens, int64_t max_q, int32_t q_heads, int32_t kv_heads,

@@ -107,3 +107,85 @@ def test_attention_does_not_depend_on_bytes_no_row_sees(W, Hq, H, D, P, ql, soft
         zeros = [x.copy() for x in cache]
         zeros[0][np.nonzero(~seen)[0], :, np.nonzero(~seen)[1]] = 0
         _compare(*got[0], q, cu, kv, zeros, table, softcap=softcap, window=win)
+
+
+# ---------------------------------------------------------------------------
+# NaN and infinite values
+# ---------------------------------------------------------------------------
+def _rows_that_see(cu, kv, i, j, window):
+    """Rows of request i that see its token j."""
+    n = int(cu[i + 1] - cu[i])
+    pos = kv[i] - n + np.arange(n)
+    return cu[i] + np.nonzero((pos >= j) & ((pos - j < window) if window else True))[0]
+
+
+VALUE_SHAPES = [
+    # Hq, H, D, page, query lengths, cache lengths, spare columns of the table, window
+    (8, 2, 128, 64, [5, 3, 1], [200, 66, 90], 1, 0),           # a workgroup a row tile
+    (4, 2, 64, 16, [7, 4, 2], [300, 129, 40], 1, 40),
+    (8, 2, 128, 32, [6, 8, 2], [700, 1400, 64], 200, 0),       # shares of tiles
+    (16, 2, 64, 128, [2, 7, 1], [900, 3000, 5], 100, 3),
+    (8, 2, 128, 64, [130, 70, 40], [330, 70, 200], 1, 0),      # prompts
+    (4, 4, 64, 16, [200, 129, 3], [200, 300, 77], 1, 0),
+    (6, 2, 128, 16, [90, 50, 1], [150, 800, 9], 1, 30),
+    (8, 2, 64, 128, [64, 40, 64], [3000, 2500, 64], 1, 700),   # rows split over the cache
+]
+
+
+@pytest.mark.parametrize("shape", VALUE_SHAPES, ids=lambda s: f"{s[0]}x{s[1]}x{s[2]}p{s[3]}w{s[7]}")
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_attention_value_that_is_not_finite(W, shape, softcap):
+    """A NaN value, or one whose scale takes it past bf16, reaches its own channel of the rows that
+    see its token, and nothing else: the rest has the bits that a zero in its place gives."""
+    Hq, H, D, P, ql, kl, spare, window = shape
+    banner("kv attention: values that are not finite", shape, softcap)
+    q, cu, kv, cache, table = _spread_problem(33, Hq, H, D, P, ql, kl, spare_cols=spare)
+    G = Hq // H
+    for i in range(2):
+        for back in sorted({0, 1, ql[i] // 2, ql[i] - 1, min(ql[i] + 5, kl[i] - 1)}):
+            j, head, ch = kl[i] - 1 - back, (i + back) % H, (37 * back + 11) % D
+            page = table[i, j // P]
+            for code, scale in ((0x7F, None), (0xFF, None), (0x7E, 250), (0xFA, 247)):
+                c = [x.copy() for x in cache]
+                if scale is not None:                          # the others of the page stay below 2^-4
+                    c[3][page, head] = scale
+                    c[2][page, head] &= 0x97
+                c[2][page, head, ch, j % P] = 0
+                want, want_lse = _attend(W, q, cu, kv, c, table, softcap=softcap, window=window)
+                assert np.isfinite(bf16_decode(want)).all()
+                c[2][page, head, ch, j % P] = code
+                got, lse = _attend(W, q, cu, kv, c, table, softcap=softcap, window=window)
+                hit = np.zeros(got.shape, bool)
+                hit[_rows_that_see(cu, kv, i, j, window), head * G:(head + 1) * G, ch] = True
+                y = bf16_decode(got)
+                assert not np.isfinite(y[hit]).any(), (i, back, code)
+                if scale is None:
+                    assert np.isnan(y[hit]).all(), (i, back, code)
+                assert np.array_equal(got[~hit], want[~hit]) and np.array_equal(lse, want_lse), (i, back, code)
+
+
+@pytest.mark.parametrize("shape", VALUE_SHAPES, ids=lambda s: f"{s[0]}x{s[1]}x{s[2]}p{s[3]}w{s[7]}")
+def test_attention_nan_keys_and_queries(W, shape):
+    """A NaN key makes the rows that see it NaN, a NaN query its own row, and no others."""
+    Hq, H, D, P, ql, kl, spare, window = shape
+    banner("kv attention: NaN keys and queries", shape)
+    q, cu, kv, cache, table = _spread_problem(34, Hq, H, D, P, ql, kl, spare_cols=spare)
+    G = Hq // H
+    for softcap in (0.0, 20.0):
+        want, want_lse = _attend(W, q, cu, kv, cache, table, softcap=softcap, window=window)
+        for i, back in ((0, ql[0] // 2), (1, 0), (1, min(ql[1] + 5, kl[1] - 1))):
+            j, head = kl[i] - 1 - back, back % H
+            c = [x.copy() for x in cache]
+            c[0][table[i, j // P], head, j % P, 5] = 0x7F
+            got, lse = _attend(W, q, cu, kv, c, table, softcap=softcap, window=window)
+            hit = np.zeros(want_lse.shape, bool)
+            hit[_rows_that_see(cu, kv, i, j, window), head * G:(head + 1) * G] = True
+            assert np.isnan(bf16_decode(got)[hit]).all() and np.isnan(lse.view(np.float32)[hit]).all()
+            assert np.isfinite(bf16_decode(got)[~hit]).all() and np.isfinite(lse.view(np.float32)[~hit]).all()
+        x = q.copy()
+        x[1, 1, 3] = np.nan
+        got, lse = _attend(W, x, cu, kv, cache, table, softcap=softcap, window=window)
+        hit = np.zeros(want_lse.shape, bool)
+        hit[1, 1] = True
+        assert np.isnan(bf16_decode(got)[hit]).all() and np.isnan(lse.view(np.float32)[hit]).all()
+        assert np.isfinite(bf16_decode(got)[~hit]).all() and np.isfinite(lse.view(np.float32)[~hit]).all()

@@ -841,6 +841,73 @@ __device__ __forceinline__ u32x4_t keep_tokens(u32x4_t v, int j, int lo, int hi)
   return v;
 }
 
+// Values that are not finite: the NaN code, and what a scale above 2^119 takes
+// past bf16's range.  In a tile whose rows see different tokens the product
+// would carry them to every row (0 * NaN), so such bytes are taken out there, and
+// `add_not_finite` gives them to the rows that see them once the sums are done.
+// Where there are none this costs up to 2 % (chunks 543 -> 550 us, window step
+// 13.0 -> 13.2 us, drafted tokens the same): the bytes are looked at in those
+// tiles only.
+// The least magnitude that is not finite with E8M0 code c:
+__device__ __forceinline__ uint32_t not_finite_from(uint32_t c) { return c > 246 ? (262 - c) * 8 : 0x7F; }
+// What takes the magnitudes from there on, and no other, to bit 7 of their byte.
+__device__ __forceinline__ uint32_t not_finite_add(uint32_t c) { return (0x80u - not_finite_from(c)) * 0x01010101u; }
+// 16 bytes without those that are not finite; bit 7 of some byte of `found` is set if there were any.
+__device__ __forceinline__ u32x4_t take_not_finite(u32x4_t v, uint32_t add, uint32_t& found) {
+#pragma unroll
+  for (int w = 0; w < 4; w++) {
+    const uint32_t t = (v[w] & 0x7F7F7F7Fu) + add;
+    found |= t;
+    v[w] &= ~__builtin_amdgcn_perm(t, t << 8, 0x0B090A08u);    // bit 7 of each byte of t all over it
+  }
+  return v;
+}
+
+// The pieces of 16 tokens, at j, that every row of a tile sees alike: those in
+// [lo, hi).  Rows at positions first to last see different tokens of the tiles
+// before (whose lowest token the last row does not see) and behind.
+struct KvAlike {
+  int lo, hi;
+  __device__ __forceinline__ KvAlike(int first, int last, int window) {
+    const int last_lo = kv_lowest(last, window);
+    lo = last > first ? (last_lo + TILE - 1) / TILE * TILE : 0;
+    hi = last > first ? (first < 0 ? 0 : (first + 1) / TILE * TILE) : 0x7FFFFFFF;
+  }
+  __device__ __forceinline__ bool operator()(int j) const { return j >= lo && j <= hi - 16; }
+};
+// What was taken out of tiles [t0, t1) in channels ch .. ch + 3 and a row at `pos`
+// sees, added to the row's results as they were stored: sums or, if null, outputs.
+// Rare, so done afterwards in memory: the loops' registers have no room for it.
+template <typename TAB>
+__device__ __forceinline__ void add_not_finite(const KvArgs& A, TAB tab, int kvh, int head_dim, int t0, int t1, KvAlike alike,
+                                               int pos, int ch, float* sums, uint16_t* outs) {
+  const int rlo = kv_lowest(pos, A.window), last = t1 * TILE - 1 < pos ? t1 * TILE - 1 : pos;
+  float add[4] = {0, 0, 0, 0};
+#pragma unroll 1
+  for (int j = t0 * TILE > rlo ? t0 * TILE : rlo; j <= last; j++) {      // below kv_len, as pos is
+    if (alike(j & ~15)) {
+      j |= 15;
+      continue;
+    }
+    const int id = tab[j >> A.log_page];
+    if (id < 0 || id >= A.num_pages) continue;
+    const int64_t block = (int64_t)id * A.kv_heads + kvh;
+    const uint32_t least = not_finite_from(A.v_scales[block]);
+    const uint8_t* p = A.v_codes + (((block * head_dim + ch) << A.log_page) + (j & ((1 << A.log_page) - 1)));
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      const uint32_t v = p[e << A.log_page], mag = v & 0x7Fu;
+      if (mag >= least) add[e] += mag == 0x7Fu ? __builtin_nanf("") : v & 0x80u ? -INFINITY : INFINITY;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; e++) {
+    if (add[e] == 0.0f) continue;
+    if (sums) sums[e] += add[e];
+    else outs[e] = (uint16_t)(pack_bf16x2(bf16_lo(outs[e]) + add[e], 0.0f) & 0xFFFFu);
+  }
+}
+
 // Decode: 16 or 32 rows (the query heads of a group, for one token or a few
 // drafted ones) per row tile.  Bound by the bytes of K and V: they go from HBM
 // straight into the registers that feed v_mfma_f32_16x16x32_bf16, the next
@@ -867,6 +934,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
   constexpr int KP = D / 64, DT = D / 16, R = 16 * NR;
   __shared__ __attribute__((aligned(16))) float so[4][R][D + 4];
   __shared__ float sm[4][R], sl[4][R];
+  __shared__ int st[4];
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int group = (int)(blockIdx.x / (unsigned)A.kv_heads), kvh = (int)(blockIdx.x % (unsigned)A.kv_heads);
@@ -950,8 +1018,11 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
     int lo = kv_lowest(rows.pos0, A.window);
     lo = lo < hi ? lo : hi;
     const int lo_max = kv_lowest(row_max, A.window);
-    int t = q.first + (int)((joined ? g0 : u) - row_begin), t1 = q.first + (solo ? q.tiles : (int)((joined ? g1 : stop) - row_begin));
-    t = t < lo / TILE ? lo / TILE : t;
+    auto first_tile = [&]() {
+      const int a = q.first + (int)((joined ? g0 : u) - row_begin);
+      return a < lo / TILE ? lo / TILE : a;
+    };
+    int t = first_tile(), t1 = q.first + (solo ? q.tiles : (int)((joined ? g1 : stop) - row_begin));
     t1 = t1 > (hi + TILE - 1) / TILE ? (hi + TILE - 1) / TILE : t1;
     t += joined ? wave : 0;
 
@@ -982,6 +1053,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
 #pragma unroll
       for (int d = 0; d < DT; d++) vr[d] = ld16(p + ((16 * d) << A.log_page));
     };
+    uint32_t taken = 0;                       // values of this lane's that are not finite
     if (t < t1) {
       load_ids(t);
       load_k(t);
@@ -1040,12 +1112,16 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
       }
       if (more) load_k(t + step);
       float vs = e8m0_as_scale(vsc);
-      const bool edge = t * TILE + TILE - 1 > rows.pos0 || t * TILE < lo_max || __any(!vok);
+      const bool differs = t * TILE + TILE - 1 > rows.pos0 || t * TILE < lo_max, edge = differs || __any(!vok);
       if (edge) {                             // bytes of V that no row may see
         const int a = vok ? lo : 0, z = vok ? hi : 0;
         if (j0 + 16 <= a || j0 >= z) vs = 1.0f;
+        const uint32_t add = hi - 1 > rows.pos0 && differs ? not_finite_add(vsc) : 0;   // 0 takes nothing
 #pragma unroll
         for (int d = 0; d < DT; d++) vr[d] = keep_tokens(vr[d], j0, a, z);
+        if (__builtin_expect(add != 0, 0))    // by itself, so that V^T keeps its registers
+#pragma unroll
+          for (int d = 0; d < DT; d++) vr[d] = take_not_finite(vr[d], add, taken);
       }
       bf16x8_t p0[NR], p1[NR];
 #pragma unroll
@@ -1143,6 +1219,13 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
           u32x2_t{pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv)};
       if (A.lse && ch == 0) A.lse[orow] = sum == 0.0f ? -INFINITY : (top + __builtin_log2f(sum)) * LN2;
     };
+    auto put_not_finite = [&](int row, int ch) {
+      const int query = rows.query(A, row);
+      const int64_t at = ((int64_t)slot * A.kv_heads + kvh) * part.rows + row;
+      const int64_t orow = (int64_t)(q.q0 + rows.first + query) * A.q_heads + kvh * A.group + rows.head(A, row);
+      add_not_finite(A, tab, kvh, D, first_tile(), t1, KvAlike(rows.pos0, row_max, A.window), rows.pos0 + query, ch,
+                     whole ? nullptr : part.sums + at * D + ch, A.out + orow * D + ch);
+    };
     if (!joined) {
 #pragma unroll
       for (int c = 0; c < NR; c++)
@@ -1150,6 +1233,11 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
 #pragma unroll
           for (int d = 0; d < DT; d++) put(16 * c + m, 16 * d + 4 * g, o[c][d], mx[c], l[c]);
         }
+      if (__builtin_expect(__any((taken & 0x80808080u) != 0), 0)) {
+#pragma unroll 1
+        for (int i = 0; i < NR * DT; i++)
+          if (16 * (i / DT) + m < n_rows) put_not_finite(16 * (i / DT) + m, 16 * (i % DT) + 4 * g);
+      }
       u = stop;
       if (u >= u1) break;
       if (++rt == q.row_tiles) {              // on to the next request that has rows
@@ -1170,10 +1258,13 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
         sm[wave][16 * c + m] = mx[c];
         sl[wave][16 * c + m] = l[c];
       }
+      const bool wave_taken = __any((taken & 0x80808080u) != 0);
+      if (lane == 0) st[wave] = wave_taken;
 #pragma unroll
       for (int d = 0; d < DT; d++) *reinterpret_cast<f32x4_t*>(&so[wave][16 * c + m][16 * d + 4 * g]) = o[c][d];
     }
     __syncthreads();
+    const bool any_taken = (st[0] | st[1] | st[2] | st[3]) != 0;
     for (int i = tid; i < n_rows * (D / 4); i += KV_THREADS) {
       const int row = i / (D / 4), ch = i % (D / 4) * 4;
       float top = sm[0][row], sum = 0.0f;
@@ -1189,6 +1280,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
         for (int e = 0; e < 4; e++) acc[e] = __builtin_fmaf(f, v[e], acc[e]);
       }
       put(row, ch, acc, top, sum);
+      if (__builtin_expect(any_taken, 0)) put_not_finite(row, ch);
     }
     break;
   }
@@ -1340,14 +1432,21 @@ __global__ __launch_bounds__(PTHREADS, D == 64 ? 3 : 2) void k_kv_prompt(const K
       *reinterpret_cast<bf16x8_t*>(kdst[i] + at + 32 * 16) = e4m3_bf16x8(kr[i][2], kr[i][3], s);
     }
   };
+  KvAlike alike(rows.pos0, rows.pos0 + rows.query(A, it.rows - 1), A.window);
+  alike.lo = alike.lo > lo ? alike.lo : lo;   // and nothing of theirs is unseen
+  alike.hi = alike.hi < hi ? alike.hi : hi;
+  uint32_t taken = 0;                         // whether this lane took values out that are not finite
   auto store_v = [&](int t, int buf) {        // without the bytes that no row may see
     const int j = t * TILE + vtok;
     float s = e8m0_as_scale(vsc);
-    if (!vok || j < lo || j + 16 > hi) {
+    if (!vok || !alike(j)) {
       const int a = vok ? lo : 0, z = vok ? hi : 0;
+      const uint32_t add = not_finite_add(vsc);
+      uint32_t found = 0;
       if (j + 16 <= a || j >= z) s = 1.0f;
 #pragma unroll
-      for (int i = 0; i < ST; i++) vr[i] = keep_tokens(vr[i], j, a, z);
+      for (int i = 0; i < ST; i++) vr[i] = take_not_finite(keep_tokens(vr[i], j, a, z), add, found);
+      taken |= found & 0x80808080u;
     }
 #pragma unroll
     for (int i = 0; i < ST; i++) {
@@ -1522,6 +1621,14 @@ __global__ __launch_bounds__(PTHREADS, D == 64 ? 3 : 2) void k_kv_prompt(const K
     k1 = k2;
     k2 = k;
   }
+  bool any_taken = false;
+  if (t0 < t1 && !(alike(t0 * TILE) && alike(t1 * TILE - 16))) {
+    uint32_t* flags = reinterpret_cast<uint32_t*>(sk[0] + k2);     // free in the last step
+    const bool wave_taken = __any(taken != 0);
+    if (lane == 0) flags[wave] = wave_taken;
+    tile_barrier();
+    any_taken = (flags[0] | flags[1] | flags[2] | flags[3]) != 0;
+  }
   l += __shfl_xor(l, 32, 64);
   if (!live) return;
   if (split) {
@@ -1536,18 +1643,25 @@ __global__ __launch_bounds__(PTHREADS, D == 64 ? 3 : 2) void k_kv_prompt(const K
       part.stats[2 * at] = mx;
       part.stats[2 * at + 1] = l;
     }
-    return;
   }
   const int64_t orow = (int64_t)(it.q0 + rows.first + query) * A.q_heads + head;
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  if (!split) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-  for (int d = 0; d < DT; d++)
+    for (int d = 0; d < DT; d++)
 #pragma unroll
-    for (int i = 0; i < 4; i++)
-      *reinterpret_cast<u32x2_t*>(A.out + orow * D + 32 * d + 8 * i + 4 * h) =
-          u32x2_t{pack_bf16x2(o[d][4 * i] * inv, o[d][4 * i + 1] * inv),
-                  pack_bf16x2(o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv)};
-  if (A.lse && h == 0) A.lse[orow] = l == 0.0f ? -INFINITY : (mx + __builtin_log2f(l)) * LN2;
+      for (int i = 0; i < 4; i++)
+        *reinterpret_cast<u32x2_t*>(A.out + orow * D + 32 * d + 8 * i + 4 * h) =
+            u32x2_t{pack_bf16x2(o[d][4 * i] * inv, o[d][4 * i + 1] * inv),
+                    pack_bf16x2(o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv)};
+    if (A.lse && h == 0) A.lse[orow] = l == 0.0f ? -INFINITY : (mx + __builtin_log2f(l)) * LN2;
+  }
+  if (__builtin_expect(any_taken, 0)) {
+    float* sums = split ? part.sums + ((it.slot * A.kv_heads + kvh) * PROWS + wrow + m) * D : nullptr;
+#pragma unroll 1
+    for (int ch = 4 * h; ch < D; ch += 8)
+      add_not_finite(A, tab, kvh, D, t0, t1, alike, pos, ch, split ? sums + ch : nullptr, A.out + orow * D + ch);
+  }
 }
 
 // Joins `parts` partial results of rows [row0, row0 + some) of one head, a wave
