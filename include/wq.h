@@ -556,7 +556,7 @@ wq_status wq_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v
  *             not seen, so that no access leaves the buffers.
  * max_q       the largest number of queries of one request, or 0 if unknown.
  *             Only the choice of kernels depends on it.
- * sm_scale    > 0, finite; window >= 0.
+ * sm_scale    > 0, finite, at most 2^127 (WQ_EUNSUPPORTED above); window >= 0.
  * softcap     0, or 2^-10 to 2^10 with sm_scale / softcap in (2^-100, 2^14)
  *             (WQ_EUNSUPPORTED outside): a capped score is off by at most
  *             softcap * 2^-22.

@@ -189,3 +189,14 @@ def test_attention_nan_keys_and_queries(W, shape):
         hit[1, 1] = True
         assert np.isnan(bf16_decode(got)[hit]).all() and np.isnan(lse.view(np.float32)[hit]).all()
         assert np.isfinite(bf16_decode(got)[~hit]).all() and np.isfinite(lse.view(np.float32)[~hit]).all()
+
+
+@pytest.mark.parametrize("ql", [[1, 2], [70, 1]])
+def test_attention_largest_scale(W, ql):
+    """sm_scale 2^127: a query of zeros sees all its tokens alike."""
+    banner("kv attention: the largest scale", ql)
+    q, cu, kv, cache, table = _spread_problem(39, 4, 2, 64, 16, ql, [200, 70])
+    kw = {"sm_scale": 2.0 ** 127}
+    _compare(*_attend(W, 0 * q, cu, kv, cache, table, **kw), 0 * q, cu, kv, cache, table, **kw)
+    with pytest.raises(ValueError):
+        W.wq_kv_attention(dev_bf16(bf16_round(q)), *[dev_u8(c) for c in cache], _i32(table), _i32(cu), _i32(kv), sm_scale=3e38)

@@ -1949,6 +1949,7 @@ wq_status wq_kv_attention(const void* q_bf16, int64_t q_stride, const int32_t* c
   if (!kv_sizes_ok(batch, tokens, max_q, q_heads, kv_heads, page, max_blocks) || num_pages < 1 || window < 0)
     return WQ_EINVAL;
   if (!(sm_scale > 0.0f) || !(sm_scale < INFINITY) || !(softcap >= 0.0f) || !(softcap < INFINITY)) return WQ_EINVAL;
+  if (sm_scale > 0x1p127f) return WQ_EUNSUPPORTED;           // scores go to base 2: sm_scale * log2 e is finite
   if (softcap > 0.0f && (softcap < 0x1p-10f || softcap > 0x1p10f || !(sm_scale / softcap < 0x1p14f) || !(sm_scale / softcap > 0x1p-100f)))
     return WQ_EUNSUPPORTED;
   const int64_t row = (int64_t)q_heads * head_dim;
