@@ -492,8 +492,8 @@ wq_status wq_moe_gemm_w4a8(const uint8_t* x8, int64_t T, const float* a_scale, c
  * state       2 int32 (output): the cursor behind the last page taken
  *             (cursor + the pages of the requests not refused), and how many
  *             requests were refused.
- * Outputs must not overlap inputs (equal pointers are WQ_EINVAL): a step is a
- * function of its inputs, and calling it again changes nothing.
+ * Outputs must not overlap inputs or one another (equal pointers are WQ_EINVAL):
+ * a step is a function of its inputs, and calling it again changes nothing.
  */
 wq_status wq_kv_blocks(const int32_t* ctx_lens, const int32_t* new_lens, int64_t batch, const int32_t* free_pages,
                        int64_t num_free, const int32_t* cursor, int32_t page, int32_t* block_table, int64_t max_blocks,

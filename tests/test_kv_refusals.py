@@ -20,3 +20,19 @@ def test_attention_scale_whose_exponent_overflows(lib, cap):
     for sm in (3.4e38, 3e38, 2.4e38, 1.8e38):
         assert call(sm) == 3, sm
     assert call(float("inf")) == 1
+
+
+def test_blocks_outputs_that_are_inputs(lib):
+    """Every output of a step beside every input and every other output: equal pointers are refused."""
+    names = ["ctx", "new", "free", "cur", "table", "slots", "pos", "cu", "kv", "state"]
+
+    def call(**kw):
+        a = {n: 0x100000 + 0x1000 * i for i, n in enumerate(names)}
+        a.update(kw)
+        return lib.wq_kv_blocks(a["ctx"], a["new"], 4, a["free"], 3, a["cur"], 64, a["table"], 8, 4, a["slots"],
+                                a["pos"], a["cu"], a["kv"], a["state"], None)
+    at = {n: 0x100000 + 0x1000 * i for i, n in enumerate(names)}
+    for out in ["table", "slots", "pos", "cu", "kv", "state"]:
+        for other in names:
+            if other != out:
+                assert call(**{out: at[other]}) == 1, (out, other)

@@ -1790,10 +1790,13 @@ wq_status wq_kv_blocks(const int32_t* ctx_lens, const int32_t* new_lens, int64_t
   if (!cu_new || !state || (batch > 0 && (!ctx_lens || !new_lens || !block_table || !kv_lens)) ||
       (num_free > 0 && !free_pages) || (tokens > 0 && (!slots || !positions)))
     return WQ_EINVAL;
-  if (kv_lens && (kv_lens == ctx_lens || kv_lens == new_lens)) return WQ_EINVAL;
-  if (cu_new == ctx_lens || cu_new == new_lens || cu_new == cursor || state == cursor || state == ctx_lens ||
-      state == new_lens || (block_table && block_table == free_pages))
-    return WQ_EINVAL;
+  // the outputs, and behind them the inputs; what has no elements is nowhere
+  const void* at[] = {cu_new, state, batch ? kv_lens : nullptr, batch ? block_table : nullptr,
+                      tokens ? slots : nullptr, tokens ? positions : nullptr, batch ? ctx_lens : nullptr,
+                      batch ? new_lens : nullptr, num_free ? free_pages : nullptr, cursor};
+  for (int i = 0; i < 6; i++)
+    for (int j = i + 1; j < 10; j++)
+      if (at[i] && at[i] == at[j]) return WQ_EINVAL;
   const int64_t groups = (tokens + KV_THREADS - 1) / KV_THREADS;
   k_kv_blocks<<<(unsigned)(groups > 1 ? groups : 1), KV_THREADS, 0, (hipStream_t)stream>>>(
       ctx_lens, new_lens, batch, free_pages, num_free, cursor, log2_page(page), block_table, max_blocks, tokens, slots,
