@@ -200,3 +200,16 @@ def test_attention_largest_scale(W, ql):
     _compare(*_attend(W, 0 * q, cu, kv, cache, table, **kw), 0 * q, cu, kv, cache, table, **kw)
     with pytest.raises(ValueError):
         W.wq_kv_attention(dev_bf16(bf16_round(q)), *[dev_u8(c) for c in cache], _i32(table), _i32(cu), _i32(kv), sm_scale=3e38)
+
+
+# ---------------------------------------------------------------------------
+# workspaces
+# ---------------------------------------------------------------------------
+def test_workspace_of_another_kind_is_refused(W):
+    banner("kv attention: workspaces that are no tensors on the GPU")
+    q, cu, kv, cache, table = _spread_problem(35, 8, 2, 64, 16, [1, 1], [100, 60])
+    args = (dev_bf16(bf16_round(q)), *[dev_u8(c) for c in cache], _i32(table), _i32(cu), _i32(kv))
+    for bad in (1 << 20, bytearray(1 << 20), np.zeros(1 << 20, np.uint8), torch.zeros(1 << 20, dtype=torch.uint8),
+                torch.zeros((1 << 10, 2), dtype=torch.uint8, device="cuda")[:, :1]):
+        with pytest.raises(ValueError, match="workspace"):
+            W.wq_kv_attention(*args, workspace=bad)

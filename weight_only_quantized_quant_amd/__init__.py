@@ -567,7 +567,7 @@ def wq_kv_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tens
         workspace = q.new_empty(ws_bytes, dtype=_u8) if ws_bytes else None
         ws = workspace.data_ptr() if ws_bytes else None
     else:
-        ws = _ptr(workspace, dev, workspace.dtype, "workspace")
+        ws = _ptr(workspace, dev, getattr(workspace, "dtype", None), "workspace")
         ws_bytes = workspace.numel() * workspace.element_size()
     _launch(lib.wq_kv_attention, dev, "wq_kv_attention", q.data_ptr(), q_stride, cu, kl, B, T, max_q, hq, h, dim, kc,
             ks, vc, vs, p, n, table, width, sm_scale, softcap, window, op, lse.data_ptr() if return_lse else None,
