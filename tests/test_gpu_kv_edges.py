@@ -213,3 +213,90 @@ def test_workspace_of_another_kind_is_refused(W):
                 torch.zeros((1 << 10, 2), dtype=torch.uint8, device="cuda")[:, :1]):
         with pytest.raises(ValueError, match="workspace"):
             W.wq_kv_attention(*args, workspace=bad)
+
+
+def _padded(t, n):
+    """t between n rows of other memory on either side, and the whole."""
+    whole = torch.full((t.shape[0] + 2 * n, *t.shape[1:]), 7, dtype=t.dtype, device=t.device)
+    return whole[n:n + t.shape[0]], whole
+
+
+@pytest.mark.parametrize("ql", [[1, 1, 5], [40, 2, 90]])
+def test_workspace_of_the_caller(W, ql):
+    """The bytes asked for are enough, whatever they hold; one less is refused; nothing beside them changes."""
+    banner("kv attention: caller's workspace", ql)
+    q, cu, kv, cache, table = _spread_problem(37, 8, 2, 128, 64, ql, [900, 4000, 3000])
+    x = dev_bf16(bf16_round(q))
+    args = (x, *[dev_u8(c) for c in cache], _i32(table), _i32(cu), _i32(kv))
+    want, want_lse = W.wq_kv_attention(*args, return_lse=True)
+    need = W.wq_kv_attention_workspace_size(3, len(q), 0, 8, 2, 128, 64, table.shape[1])
+    assert need > 0
+    for fill in (0x00, 0xFF, 0x7F, 0x01):
+        whole = torch.full((need + 1024,), fill, dtype=torch.uint8, device="cuda")
+        for _ in range(2):                                     # as the call before left it
+            got, lse = W.wq_kv_attention(*args, return_lse=True, workspace=whole[512:512 + need])
+            assert torch.equal(got, want) and torch.equal(lse, want_lse)
+        assert (whole[:512] == fill).all() and (whole[512 + need:] == fill).all()
+    with pytest.raises(ValueError):
+        W.wq_kv_attention(*args, workspace=whole[512:512 + need - 1])
+
+
+def test_lengths_outside_the_contract_stay_inside_the_outputs(W):
+    """Row ranges that decrease, overlap or leave the arrays: nothing beside the outputs changes."""
+    banner("kv attention: row ranges that do not fit, outputs inside larger memory")
+    q, cu, kv, cache, table = _spread_problem(38, 4, 2, 64, 16, [2, 3, 1, 2], [40, 20, 9, 30], spare_cols=0)
+    x = dev_bf16(bf16_round(q))
+    dev = [dev_u8(c) for c in cache]
+    for bad in ([0, 2, 5, 4, 100], [-3, 2, 5, 6, 8], [0, 2 ** 31 - 1, 5, 6, 8], [5, 4, 3, 2, 1]):
+        for hint in (0, 1):
+            out, whole = _padded(x, 64)
+            W.wq_kv_attention(x, *dev, _i32(table), _i32(bad), _i32(kv), max_q=hint, out=out)
+            torch.cuda.synchronize()
+            assert (whole[:64] == 7).all() and (whole[64 + len(q):] == 7).all()
+
+
+# ---------------------------------------------------------------------------
+# weights spread over many tokens
+# ---------------------------------------------------------------------------
+def _effective(q, cu, kv, cache, table, window=0):
+    """Median over requests of the tokens that the last row's softmax is spread over, 1 / sum p^2."""
+    N, H, P, D = cache[0].shape
+    n = []
+    for i, m in enumerate(kv):
+        if m == 0 or cu[i + 1] == cu[i]:
+            continue
+        pages = table[i, :-(-m // P)]
+        k = OK.e4m3_decode(cache[0][pages, 0]) * OK.e8m0_decode(cache[1][pages, 0])[:, None, None]
+        k = k.reshape(-1, D)[max(0, m - window) if window else 0:m]
+        s = k @ q[cu[i + 1] - 1, 0] * D ** -0.5
+        p = np.exp(s - s.max())
+        n.append(p.sum() ** 2 / (p * p).sum())
+    return float(np.median(n))
+
+
+SPREAD = [
+    # Hq, H, D, page, query lengths, cache lengths, spare columns, tokens that count at least
+    (32, 8, 128, 64, [1] * 5, [700, 1000, 64, 65, 900], 1, 50),            # a workgroup a row tile
+    (32, 8, 128, 64, [1] * 3, [700, 2000, 1500], 100, 90),                 # shares of tiles and joins
+    (16, 16, 64, 16, [1] * 7, [3000, 5, 1, 900, 2048, 0, 1000], 1, 50),
+    (40, 8, 128, 32, [7, 1, 2, 5], [3000, 500, 1200, 600], 1, 60),         # drafted tokens
+    (24, 1, 64, 128, [1, 3], [2500, 800], 1, 90),
+    (4, 2, 64, 64, [1, 1, 1, 2], [20000, 600, 900, 5000], 1, 90),          # one long context
+    (8, 2, 128, 64, [200, 130], [520, 400], 1, 30),                        # prompts
+    (4, 4, 64, 16, [300, 40, 1], [300, 900, 700], 1, 30),
+    (8, 2, 128, 32, [40, 1, 90, 5], [3000, 700, 2500, 64], 1, 90),         # rows split over the cache
+    (16, 2, 64, 128, [40, 1, 90, 5], [3000, 700, 2500, 64], 1, 90),
+]
+
+
+@pytest.mark.parametrize("shape", SPREAD, ids=lambda s: f"{s[0]}x{s[1]}x{s[2]}p{s[3]}")
+@pytest.mark.parametrize("softcap,window", [(0.0, 0), (0.0, 640), (8.0, 0)])
+def test_attention_of_spread_weights(W, shape, softcap, window):
+    Hq, H, D, P, ql, kl, spare, least = shape
+    banner("kv attention: spread weights", shape, softcap, window)
+    q, cu, kv, cache, table = _spread_problem(36, Hq, H, D, P, ql, kl, spare_cols=spare)
+    assert _effective(q, cu, kv, cache, table, window) >= (least if not window else 25)
+    for hint in (0, max(ql)):
+        kw = {"softcap": softcap, "window": window}
+        bits, lse = _attend(W, q, cu, kv, cache, table, max_q=hint, **kw)
+        _compare(bits, lse, q, cu, kv, cache, table, **kw)
