@@ -50,7 +50,7 @@ def _compare(bits, lse_bits, q, cu, kv, cache, table, sm_scale=None, softcap=0.0
     assert np.isfinite(y).all()
     worst = (np.abs(y - ref) / tol).max()
     assert worst <= 1.0, f"output: error / bound = {worst:.3f}"
-    worst = (np.abs(l - rl)[some] / (tol_lse + 2.0 ** -22 * np.abs(rl))[some]).max()
+    worst = (np.abs(l[some] - rl[some]) / (tol_lse[some] + 2.0 ** -22 * np.abs(rl[some]))).max()
     assert worst <= 1.0, f"lse: error / bound = {worst:.3f}"
 
 

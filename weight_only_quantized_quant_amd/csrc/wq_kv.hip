@@ -385,8 +385,9 @@ __device__ __forceinline__ void append_run(const void* __restrict__ x, int64_t s
 // begin one, `slot` the slot of token t0 + lane.  D / 8 lanes a token, many
 // tokens at once and no barrier among them; the pages whose scale grew are
 // gone over by the whole workgroup afterwards.  64 tokens, 8 heads of 128: 4.2
-// us (5.3 as runs); 2048: 66 us, bound by the cache line that each value byte
-// of the transposed page touches (76 as runs).
+// us where no scale grows (5.3 as runs), 7.8 us where half of the pages' do and
+// 8.5 us where all do; 2048: 66 us, bound by the cache line that each value
+// byte of the transposed page touches (76 as runs).
 template <bool BF16, bool VALUES, int D, int PAGE>
 __device__ __forceinline__ void append_ones(const void* __restrict__ x, int64_t stride, int64_t t0, int chunk,
                                             unsigned long long runs, int64_t slot, int heads, int head,
@@ -574,7 +575,9 @@ constexpr int SHORT_ROWS = 64;
 // 9 and 14 % slower on short windows).
 constexpr int DEC_GROUPS = 512;
 // A workgroup a row tile where no request can have more tiles than this (few row
-// tiles, enough of them for half the CUs) and they fit the chip twice over.  8
+// tiles, enough of them for half the CUs) and they fit the chip twice over.  The
+// host knows lengths by the table's width and the window only: 1000 tokens take
+// 12.8 us on a table of 17 columns of 64, 17.0 us on one of 520, in shares.  8
 // heads of 128, calls back to back: 1 x 700 tokens 12.8 us against 18.0 in
 // shares and a join, 1 x 2000 17 against 16; 16 x 2000 18.5 against 21.8, 16 x
 // 4000 30 against 31.
@@ -925,7 +928,9 @@ __device__ __forceinline__ void add_not_finite(const KvArgs& A, TAB tab, int kvh
 // instead (`solo`): the join's launch costs more than the tiles in turn do.
 //
 // 8 heads of 128, 4 query heads each: 64 x 8192 tokens 187 us (5.76 TB/s, 0.92
-// of a streaming read's rate); 64 x 2048-8192 tokens 105 us and 4.9 us joining.
+// of a streaming read's rate); 64 x 2048-8192 tokens 106 us and 5.0 us joining.
+// 32 rows of heads of 128 take 256 registers and spill 6 more (12 capped) outside
+// the loop over tiles; the scalars that do not fit lie in lanes of others.
 //
 // Lane l = 16 g + m.  K tile a (of 4): operand row m is token
 // 16 (m / 4) + 4 a + m % 4, result rows 4 g + i are then tokens 16 g + 4 a + i.
@@ -1223,7 +1228,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
       const int query = rows.query(A, row);
       const int64_t at = ((int64_t)slot * A.kv_heads + kvh) * part.rows + row;
       const int64_t orow = (int64_t)(q.q0 + rows.first + query) * A.q_heads + kvh * A.group + rows.head(A, row);
-      add_not_finite(A, tab, kvh, D, first_tile(), t1, KvAlike(rows.pos0, row_max, A.window), rows.pos0 + query, ch,
+      add_not_finite(A, tab, kvh, D, first_tile(), t1, KvAlike(rows.pos0, hi - 1, A.window), rows.pos0 + query, ch,
                      whole ? nullptr : part.sums + at * D + ch, A.out + orow * D + ch);
     };
     if (!joined) {
@@ -1304,9 +1309,12 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
 // scales and addresses are scalars, which takes a fifth of the loop's vector
 // instructions away (330 -> 323 us, capped 688 -> 654 us).
 //
-// Three prompts of 1500-4096 tokens, 32 heads of 128 on 8: 306-319 us (828-863
-// TFLOP/s; matrix cores busy 0.37, vector units 0.46 of the cycles, no LDS bank
-// conflicts).  Power sets the clock: a tenth fewer cycles took 3 % off the time.
+// Three prompts of 1500-4096 tokens, 32 heads of 128 on 8: 304-326 us over six
+// boxes (810-868 TFLOP/s; matrix cores busy 0.36 of the cycles, vector units 0.45,
+// both 0.15, neither 0.34; no LDS bank conflicts).  The clock falls under the load
+// (a tenth fewer cycles took 3 % off the time); at 2.4 GHz the same cycles would
+// take 298 us.  Heads of 64 195 us, pages of 16 341 us (211 us), a cap of 50 371 us
+// (251 us).
 //
 // Registers allow two waves a SIMD at heads of 128 and three at heads of 64, where
 // capped scores need that said (the same three prompts: 282 us at two, 251 at three).
