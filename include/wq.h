@@ -472,7 +472,8 @@ wq_status wq_moe_gemm_w4a8(const uint8_t* x8, int64_t T, const float* a_scale, c
  * refused when its pages do not fit its table row (then it takes none), when
  * the list ends before its last page, or when its tokens end behind row
  * `tokens` (the pages it would have taken are not given to others): its table
- * row stays as it was, its length stays ctx, and its tokens get no slot.
+ * row stays as it was, its length stays ctx, and its tokens get no slot.  They
+ * keep their rows in cu_new; what an attention over cu_new writes there means nothing.
  *
  * ctx_lens, new_lens  batch int32.
  * free_pages  num_free int32 page ids (NULL when num_free is 0).  Not changed.
@@ -564,6 +565,9 @@ wq_status wq_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v
  *             memory, since a row's queries are read while others are written
  *             (an equal pointer is WQ_EINVAL).
  * lse         tokens x q_heads fp32 (output), or NULL.
+ * max_blocks  also bounds the contexts for the choice of kernels: a table no wider
+ *             than its longest request needs (or a window) lets a step of short
+ *             contexts go without workspace and join, in three quarters of the time.
  * workspace   wq_kv_attention_workspace_size bytes (NULL if that is 0), 16-byte
  *             aligned, for this call alone while it runs; its contents need no
  *             preparation and mean nothing afterwards.
@@ -579,7 +583,8 @@ wq_status wq_kv_attention(const void* q_bf16, int64_t q_stride, const int32_t* c
                           float* lse, void* workspace, size_t ws_bytes, void* stream);
 
 /* Bytes of workspace wq_kv_attention needs for this problem: 0 where nothing is
- * split, and for sizes it refuses. */
+ * split, and for sizes it refuses.  Not monotone: a smaller batch may be split
+ * and need more than a larger one, so ask for the sizes of each call. */
 size_t wq_kv_attention_workspace_size(int64_t batch, int64_t tokens, int64_t max_q, int32_t q_heads, int32_t kv_heads,
                                       int32_t head_dim, int32_t page, int64_t max_blocks, int64_t window);
 

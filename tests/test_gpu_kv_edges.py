@@ -300,3 +300,27 @@ def test_attention_of_spread_weights(W, shape, softcap, window):
         kw = {"softcap": softcap, "window": window}
         bits, lse = _attend(W, q, cu, kv, cache, table, max_q=hint, **kw)
         _compare(bits, lse, q, cu, kv, cache, table, **kw)
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_nan_value_appended_in_a_prompt(W, page):
+    """Append and attention together: the tokens before a NaN value do not see it."""
+    banner("kv append and attention: a NaN value in a prompt", page)
+    g = torch.Generator("cuda").manual_seed(40)
+    T, H, G, D, at = 90, 2, 4, 64, 50
+    q = torch.randn(T, H * G, D, device="cuda", generator=g).to(torch.bfloat16)
+    k, v = (torch.randn(T, H, D, device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    got = []
+    for x in (0.0, float("nan")):
+        v[at, 1, 7] = x
+        N = -(-T // page)
+        c = [torch.zeros(s, dtype=torch.uint8, device="cuda") for s in ((N, H, page, D), (N, H), (N, H, D, page), (N, H))]
+        table = torch.full((1, N), -1, dtype=torch.int32, device="cuda")
+        slots, _, cu, kv, _ = W.wq_kv_blocks(_i32([0]), _i32([T]), _i32(np.arange(N)), table, page, T)
+        W.wq_kv_append(k, v, slots, *c)
+        got.append(W.wq_kv_attention(q, *c, table, cu, kv))
+    want, y = got
+    hit = torch.zeros_like(y, dtype=torch.bool)
+    hit[at:, G:, 7] = True
+    assert y[hit].isnan().all() and want.isfinite().all()
+    assert torch.equal(y[~hit], want[~hit])

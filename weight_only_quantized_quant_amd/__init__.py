@@ -486,7 +486,7 @@ def wq_kv_blocks(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: tor
     free_pages int32 [F] page ids, the first cursor[0] of them taken already; block_table int32
     [B, W], completed in place.  Returns (slots int64 [tokens], positions int32 [tokens],
     cu_new int32 [B + 1], kv_lens int32 [B], state int32 [2]: the next cursor and the number of
-    refused requests)."""
+    refused requests; the last four are parts of one allocation)."""
     _dev(ctx_lens, "ctx_lens")
     dev, (B, *rest) = ctx_lens.get_device(), ctx_lens.shape or (0, 0)
     if ctx_lens.dtype is not _i32t or rest:
@@ -542,7 +542,8 @@ def wq_kv_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tens
     rows cu_q[i] .. cu_q[i + 1]) over the cache's kv_lens[i] tokens of the pages block_table[i].
     cu_q int32 [B + 1], kv_lens int32 [B], block_table int32 [B, W].  sm_scale defaults to
     head_dim ** -0.5; softcap 0 or 2^-10 .. 2^10; max_q: the largest number of queries of one
-    request if known (it only chooses kernels).  Returns out
+    request if known (it only chooses kernels, as does the width W: short contexts are
+    fastest on a table no wider than they need).  Returns out
     bf16 [tokens, q_heads, head_dim] (and lse fp32 [tokens, q_heads])."""
     dev, T, hq, qd, q_stride = _token_rows(q, "q")
     n, h, p, dim, kc, ks, vc, vs = _kv_cache(k_codes, k_scales, v_codes, v_scales, dev)

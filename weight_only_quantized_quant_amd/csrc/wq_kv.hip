@@ -1313,7 +1313,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
 // boxes (810-868 TFLOP/s; matrix cores busy 0.36 of the cycles, vector units 0.45,
 // both 0.15, neither 0.34; no LDS bank conflicts).  The clock falls under the load
 // (a tenth fewer cycles took 3 % off the time); at 2.4 GHz the same cycles would
-// take 298 us.  Heads of 64 195 us, pages of 16 341 us (211 us), a cap of 50 371 us
+// take 302 us.  Heads of 64 195 us, pages of 16 341 us (211 us), a cap of 50 371 us
 // (251 us).
 //
 // Registers allow two waves a SIMD at heads of 128 and three at heads of 64, where
