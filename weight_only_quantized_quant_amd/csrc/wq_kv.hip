@@ -1309,8 +1309,8 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
 // scales and addresses are scalars, which takes a fifth of the loop's vector
 // instructions away (330 -> 323 us, capped 688 -> 654 us).
 //
-// Three prompts of 1500-4096 tokens, 32 heads of 128 on 8: 304-326 us over six
-// boxes (810-868 TFLOP/s; matrix cores busy 0.36 of the cycles, vector units 0.45,
+// Three prompts of 1500-4096 tokens, 32 heads of 128 on 8: 304-326 us over
+// several runs (810-868 TFLOP/s; matrix cores busy 0.36 of the cycles, vector units 0.45,
 // both 0.15, neither 0.34; no LDS bank conflicts).  The clock falls under the load
 // (a tenth fewer cycles took 3 % off the time); at 2.4 GHz the same cycles would
 // take 302 us.  Heads of 64 195 us, pages of 16 341 us (211 us), a cap of 50 371 us
