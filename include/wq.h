@@ -588,6 +588,90 @@ wq_status wq_kv_attention(const void* q_bf16, int64_t q_stride, const int32_t* c
 size_t wq_kv_attention_workspace_size(int64_t batch, int64_t tokens, int64_t max_q, int32_t q_heads, int32_t kv_heads,
                                       int32_t head_dim, int32_t page, int64_t max_blocks, int64_t window);
 
+/*
+ * 4-bit key/value cache
+ * ---------------------
+ * The same pages, slots and block tables with E2M1 elements and one E8M0 scale
+ * for 32 channels of one token and head: what quantize_mxfp4 writes with block
+ * 32, so that no code of a token depends on another token.  Half the bytes of
+ * the 8-bit cache, and 1/16 of that for the scales.
+ *   k_codes   num_pages x heads x page x head_dim/2 bytes (WQ_E2M1X2: channel 2j in
+ *             the low nibble of byte j)
+ *   v_codes   num_pages x heads x head_dim/2 x page bytes: the same bytes transposed,
+ *             the tokens of a pair of channels contiguous
+ *   k_scales, v_scales   num_pages x heads x head_dim/32 x page E8M0 bytes
+ * head_dim is 64 or 128; all four are 16-byte aligned.  wq_kv_blocks makes the
+ * tables and slots of either cache.
+ */
+
+/*
+ * wq_kv4_append -- fp32/bf16 keys and values -> their slots of the 4-bit cache.
+ *
+ * For each token, head and 32 channels: amax over the finite elements; the scale
+ * is quantize_mxfp4's, c = max(0, biased exponent of (bits(amax) + 2^21) - 2), at
+ * most 252; codes are x * 2^(127-c) rounded to the nearest E2M1 value (ties to
+ * even code), saturating at 6.  E2M1 has neither: infinities become 6 with their
+ * sign, and a NaN becomes 0.
+ * Arguments as wq_kv_append's.  A token whose slot is outside [0, num_pages *
+ * page) is skipped; slots may come in any order.  A slot given twice in one call
+ * holds bytes of either token.  Bytes of other slots stay as they were.
+ */
+wq_status wq_kv4_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride, int x_dtype,
+                        const int64_t* slots, int64_t tokens, int32_t heads, int32_t head_dim, int32_t page,
+                        int64_t num_pages, uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes, uint8_t* v_scales,
+                        void* stream);
+
+/*
+ * wq_kv4_attention -- wq_kv_attention over the 4-bit cache: the same arguments,
+ * formulas, limits and clamps (see there), with k_scales and v_scales 16-byte
+ * aligned.  Scale codes above 252 count as 252 for values, and are outside the
+ * contract for keys: only rows that see such a token are affected.
+ */
+wq_status wq_kv4_attention(const void* q_bf16, int64_t q_stride, const int32_t* cu_q, const int32_t* kv_lens,
+                           int64_t batch, int64_t tokens, int64_t max_q, int32_t q_heads, int32_t kv_heads,
+                           int32_t head_dim, const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                           const uint8_t* v_scales, int32_t page, int64_t num_pages, const int32_t* block_table,
+                           int64_t max_blocks, float sm_scale, float softcap, int64_t window, uint16_t* out,
+                           float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace wq_kv4_attention needs, as wq_kv_attention_workspace_size. */
+size_t wq_kv4_attention_workspace_size(int64_t batch, int64_t tokens, int64_t max_q, int32_t q_heads, int32_t kv_heads,
+                                       int32_t head_dim, int32_t page, int64_t max_blocks, int64_t window);
+
+/*
+ * wq_kv_append_rotary -- queries and keys rotated by position, keys and values
+ * written to either cache, in one launch.
+ *
+ * The first `rot` channels of a head are rot / 2 pairs: (i, i + rot/2), or
+ * (2i, 2i + 1) if `interleaved`.  Pair i of a token at position p is turned by the
+ * angle whose cosine is cos_sin[p][i] and whose sine is cos_sin[p][rot/2 + i]:
+ *   a' = a cos - b sin,   b' = b cos + a sin;
+ * the other channels stay.  Keys are turned in 64 bits and rounded once to fp32,
+ * then quantized as wq_kv_append or wq_kv4_append do; values are not turned.
+ * Queries are turned in fp32 and rounded once to bf16.
+ *
+ * q            tokens x q_heads x head_dim, dtype x_dtype, rows of a token q_stride
+ *              elements apart; NULL with q_heads 0 for keys alone.
+ * positions    `tokens` int32 device positions (wq_kv_blocks writes them).  A token
+ *              whose position is outside [0, max_pos) is left out: its row of
+ *              q_out stays as it was and its slot is not written.
+ * cos_sin      max_pos x rot fp32; rot is 16 to head_dim and a multiple of 16
+ *              (WQ_EUNSUPPORTED otherwise).
+ * cache_dtype  WQ_E4M3 (8-bit cache) or WQ_E2M1X2 (4-bit cache).
+ * q_out        tokens x q_heads x head_dim bf16 (output), rows q_out_stride elements
+ *              apart.  May be q itself where x_dtype is WQ_BF16 and the strides are
+ *              equal (WQ_EINVAL otherwise); any other overlap with an input is
+ *              outside the contract.
+ * Strides and the other arguments as wq_kv_append's; q, q_out and cos_sin are
+ * 16-byte aligned.
+ */
+wq_status wq_kv_append_rotary(const void* q, int64_t q_stride, int32_t q_heads, const void* k, int64_t k_stride,
+                              const void* v, int64_t v_stride, int x_dtype, const int32_t* positions,
+                              const float* cos_sin, int64_t max_pos, int32_t rot, int32_t interleaved,
+                              const int64_t* slots, int64_t tokens, int32_t heads, int32_t head_dim, int cache_dtype,
+                              int32_t page, int64_t num_pages, uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes,
+                              uint8_t* v_scales, uint16_t* q_out, int64_t q_out_stride, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

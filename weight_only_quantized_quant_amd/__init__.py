@@ -58,6 +58,13 @@ _SIGS = {
                      ctypes.c_int),
     "wq_kv_attention": ([_vp, _i64, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i64, _vp,
                          _i64, ctypes.c_float, ctypes.c_float, _i64, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "wq_kv4_append": ([_vp, _i64, _vp, _i64, ctypes.c_int, _vp, _i64, _i32, _i32, _i32, _i64, _vp, _vp, _vp, _vp, _vp],
+                      ctypes.c_int),
+    "wq_kv_append_rotary": ([_vp, _i64, _i32, _vp, _i64, _vp, _i64, ctypes.c_int, _vp, _vp, _i64, _i32, _i32, _vp, _i64,
+                             _i32, _i32, ctypes.c_int, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp], ctypes.c_int),
+    "wq_kv4_attention": ([_vp, _i64, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i64, _vp,
+                          _i64, ctypes.c_float, ctypes.c_float, _i64, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "wq_kv4_attention_workspace_size": ([_i64, _i64, _i64, _i32, _i32, _i32, _i32, _i64, _i64], _sz),
     "wq_kv_attention_workspace_size": ([_i64, _i64, _i64, _i32, _i32, _i32, _i32, _i64, _i64], _sz),
     "wq_util_stream_read": ([_vp, _i64, ctypes.c_uint32, _vp, _vp], ctypes.c_int),
     "wq_util_spin": ([_i64, ctypes.c_uint32, _vp, _vp], ctypes.c_int),
@@ -480,6 +487,33 @@ def _kv_cache(kc, ks, vc, vs, dev):
     return n, h, p, d, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr()
 
 
+def _refuse_cache4(k_codes, k_scales, v_codes, v_scales, dev):
+    """Says what is wrong with a 4-bit cache."""
+    for t, name in ((k_codes, "k_codes"), (k_scales, "k_scales"), (v_codes, "v_codes"), (v_scales, "v_scales")):
+        _ptr(t, dev, _u8, name)
+    if k_codes.dim() != 4:
+        raise ValueError("k_codes must be [num_pages, heads, page, head_dim / 2]")
+    n, h, p, w = k_codes.shape
+    if v_codes.shape != (n, h, w, p):
+        raise ValueError("v_codes must be [num_pages, heads, head_dim / 2, page]")
+    raise ValueError("k_scales and v_scales must be [num_pages, heads, head_dim / 32, page]")
+
+
+def _kv4_cache(kc, ks, vc, vs, dev):
+    """(num_pages, heads, page, head_dim) of a 4-bit cache and the addresses of its four tensors."""
+    try:
+        n, h, p, w = kc.shape
+        good = (kc.dtype is _u8 and ks.dtype is _u8 and vc.dtype is _u8 and vs.dtype is _u8 and kc.get_device() == dev
+                and ks.get_device() == dev and vc.get_device() == dev and vs.get_device() == dev
+                and kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and vs.is_contiguous()
+                and vc.shape == (n, h, w, p) and ks.shape == (n, h, w // 16, p) and vs.shape == (n, h, w // 16, p))
+    except (AttributeError, ValueError):
+        good = False
+    if not good:
+        _refuse_cache4(kc, ks, vc, vs, dev)
+    return n, h, p, 2 * w, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr()
+
+
 def wq_kv_blocks(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor, block_table: torch.Tensor,
                  page: int, tokens: int, cursor=None):
     """Block tables, slot map and positions of one step.  ctx_lens, new_lens int32 [B];
@@ -518,14 +552,69 @@ def wq_kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_codes:
     """Quantize k, v (bf16/fp32 [tokens, heads, head_dim], tokens may be strided) into their slots
     (int64 [tokens], negative: skipped) of the cache: codes uint8 [N, heads, page, head_dim] and
     [N, heads, head_dim, page], E8M0 scales uint8 [N, heads]."""
+    _append(lib.wq_kv_append, "wq_kv_append", _kv_cache, k, v, slots, k_codes, k_scales, v_codes, v_scales)
+
+
+def wq_kv4_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor,
+                  v_codes: torch.Tensor, v_scales: torch.Tensor) -> None:
+    """wq_kv_append into the 4-bit cache: codes uint8 [N, heads, page, head_dim / 2] and
+    [N, heads, head_dim / 2, page] (two E2M1 channels a byte), E8M0 scales uint8
+    [N, heads, head_dim / 32, page]."""
+    _append(lib.wq_kv4_append, "wq_kv4_append", _kv4_cache, k, v, slots, k_codes, k_scales, v_codes, v_scales)
+
+
+def _append(fn, where, cache, k, v, slots, k_codes, k_scales, v_codes, v_scales):
     dev, T, heads, hd, k_stride = _token_rows(k, "k")
     v_stride = _token_rows(v, "v")[4]
-    n, h, p, dim, kc, ks, vc, vs = _kv_cache(k_codes, k_scales, v_codes, v_scales, dev)
+    n, h, p, dim, kc, ks, vc, vs = cache(k_codes, k_scales, v_codes, v_scales, dev)
     if heads != h or hd != dim or v.shape != k.shape or v.dtype is not k.dtype or v.get_device() != dev:
         raise ValueError(f"k and v must be [tokens, {h}, {dim}] of one dtype on one device")
     sp = _shaped(slots, dev, _i64t, (T,), "slots")
-    _launch(lib.wq_kv_append, dev, "wq_kv_append", k.data_ptr(), k_stride, v.data_ptr(), v_stride, _x_dtype(k), sp, T,
-            h, dim, p, n, kc, ks, vc, vs)
+    _launch(fn, dev, where, k.data_ptr(), k_stride, v.data_ptr(), v_stride, _x_dtype(k), sp, T, h, dim, p, n, kc, ks, vc, vs)
+
+
+def wq_kv_append_rotary(q, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor,
+                        slots: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
+                        v_scales: torch.Tensor, interleaved: bool = False, q_out=None):
+    """Rotate q and k by position and quantize k, v into their slots of the 8-bit or the 4-bit cache
+    (told by the number of dimensions of k_scales).  q [tokens, q_heads, head_dim] (or None), k, v
+    [tokens, heads, head_dim], bf16 or fp32, tokens may be strided; positions int32 [tokens], cos_sin
+    fp32 [max_pos, rot]: cosines of the rot / 2 pairs, then their sines.  Pairs are channels
+    (i, i + rot / 2), or (2i, 2i + 1) if interleaved.  Returns the rotated queries, bf16: q_out
+    (tokens may be strided; q itself if that is bf16) or a new tensor.  Rows of tokens whose
+    position is outside [0, max_pos) are not written."""
+    dev, T, heads, hd, k_stride = _token_rows(k, "k")
+    v_stride = _token_rows(v, "v")[4]
+    four = isinstance(k_scales, torch.Tensor) and k_scales.dim() == 4
+    n, h, p, dim, kc, ks, vc, vs = (_kv4_cache if four else _kv_cache)(k_codes, k_scales, v_codes, v_scales, dev)
+    if heads != h or hd != dim or v.shape != k.shape or v.dtype is not k.dtype or v.get_device() != dev:
+        raise ValueError(f"k and v must be [tokens, {h}, {dim}] of one dtype on one device")
+    sp = _shaped(slots, dev, _i64t, (T,), "slots")
+    pp = _shaped(positions, dev, _i32t, (T,), "positions")
+    cs = _ptr(cos_sin, dev, torch.float32, "cos_sin")
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [max_pos, rot]")
+    max_pos, rot = cos_sin.shape
+    hq = q_stride = o_stride = 0
+    qp = op = None
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    else:
+        q_dev, tq, hq, qd, q_stride = _token_rows(q, "q")
+        if q_dev != dev or tq != T or qd != dim or q.dtype is not k.dtype:
+            raise ValueError(f"q must be [{T}, q_heads, {dim}] of k's dtype and device")
+        if q_out is None:
+            q_out, o_stride = q.new_empty((T, hq, dim), dtype=_bf16), hq * dim
+        else:
+            o_dev, *o_shape, o_stride = _token_rows(q_out, "q_out")
+            if o_dev != dev or o_shape != [T, hq, dim] or q_out.dtype is not _bf16:
+                raise ValueError(f"q_out must be bfloat16 [{T}, {hq}, {dim}] on q's device")
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    _launch(lib.wq_kv_append_rotary, dev, "wq_kv_append_rotary", qp, q_stride, hq, k.data_ptr(), k_stride, v.data_ptr(),
+            v_stride, _x_dtype(k), pp, cs, max_pos, rot, bool(interleaved), sp, T, h, dim, WQ_E2M1X2 if four else WQ_E4M3,
+            p, n, kc, ks, vc, vs, op, o_stride)
+    return q_out
 
 
 def wq_kv_attention_workspace_size(batch: int, tokens: int, max_q: int, q_heads: int, kv_heads: int, head_dim: int,
@@ -545,8 +634,32 @@ def wq_kv_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tens
     request if known (it only chooses kernels, as does the width W: short contexts are
     fastest on a table no wider than they need).  Returns out
     bf16 [tokens, q_heads, head_dim] (and lse fp32 [tokens, q_heads])."""
+    return _attention(lib.wq_kv_attention_workspace_size, lib.wq_kv_attention, "wq_kv_attention", _kv_cache, q, k_codes, k_scales,
+                      v_codes, v_scales, block_table, cu_q, kv_lens, sm_scale, softcap, window, max_q, out, return_lse,
+                      workspace)
+
+
+def wq_kv4_attention_workspace_size(batch: int, tokens: int, max_q: int, q_heads: int, kv_heads: int, head_dim: int,
+                                    page: int, max_blocks: int, window: int = 0) -> int:
+    return int(lib.wq_kv4_attention_workspace_size(batch, tokens, max_q, q_heads, kv_heads, head_dim, page, max_blocks,
+                                                   window))
+
+
+def wq_kv4_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
+                     v_scales: torch.Tensor, block_table: torch.Tensor, cu_q: torch.Tensor, kv_lens: torch.Tensor,
+                     sm_scale=None, softcap: float = 0.0, window: int = 0, max_q: int = 0, out=None,
+                     return_lse: bool = False, workspace=None):
+    """wq_kv_attention over the 4-bit cache (layout: wq_kv4_append), with the same arguments; its
+    workspace is of wq_kv4_attention_workspace_size."""
+    return _attention(lib.wq_kv4_attention_workspace_size, lib.wq_kv4_attention, "wq_kv4_attention", _kv4_cache, q, k_codes, k_scales,
+                      v_codes, v_scales, block_table, cu_q, kv_lens, sm_scale, softcap, window, max_q, out, return_lse,
+                      workspace)
+
+
+def _attention(size, fn, where, cache, q, k_codes, k_scales, v_codes, v_scales, block_table, cu_q, kv_lens, sm_scale,
+               softcap, window, max_q, out, return_lse, workspace):
     dev, T, hq, qd, q_stride = _token_rows(q, "q")
-    n, h, p, dim, kc, ks, vc, vs = _kv_cache(k_codes, k_scales, v_codes, v_scales, dev)
+    n, h, p, dim, kc, ks, vc, vs = cache(k_codes, k_scales, v_codes, v_scales, dev)
     if q.dtype is not _bf16 or qd != dim:
         raise ValueError(f"q must be bfloat16 [tokens, q_heads, {dim}]")
     table = _ptr(block_table, dev, _i32t, "block_table")
@@ -564,13 +677,13 @@ def wq_kv_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tens
         op = _shaped(out, dev, _bf16, (T, hq, dim), "out")
     lse = q.new_empty((T, hq), dtype=torch.float32) if return_lse else None
     if workspace is None:
-        ws_bytes = lib.wq_kv_attention_workspace_size(B, T, max_q, hq, h, dim, p, width, window)
+        ws_bytes = size(B, T, max_q, hq, h, dim, p, width, window)
         workspace = q.new_empty(ws_bytes, dtype=_u8) if ws_bytes else None
         ws = workspace.data_ptr() if ws_bytes else None
     else:
         ws = _ptr(workspace, dev, getattr(workspace, "dtype", None), "workspace")
         ws_bytes = workspace.numel() * workspace.element_size()
-    _launch(lib.wq_kv_attention, dev, "wq_kv_attention", q.data_ptr(), q_stride, cu, kl, B, T, max_q, hq, h, dim, kc,
+    _launch(fn, dev, where, q.data_ptr(), q_stride, cu, kl, B, T, max_q, hq, h, dim, kc,
             ks, vc, vs, p, n, table, width, sm_scale, softcap, window, op, lse.data_ptr() if return_lse else None,
             ws, ws_bytes)
     return (out, lse) if return_lse else out

@@ -1,33 +1,13 @@
 // 8-bit key/value cache for gfx950: block tables and slot maps from request
-// lengths, the append that quantizes new keys and values into their pages
-// (E4M3 elements, one E8M0 scale per page and head), and the attention that
-// reads the pages.
-#include <hip/hip_runtime.h>
-
-#include "wq.h"
-#include "wq_device.h"
-#include "wq_host.h"
-
-using namespace wq;
+// lengths, and the attention that reads the pages (E4M3 elements, one E8M0
+// scale per page and head).
+#include "wq_kv_common.h"
 
 namespace {
-
-constexpr int KV_THREADS = 256;
-typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 
 // ---------------------------------------------------------------------------
 // Block tables and slot maps
 // ---------------------------------------------------------------------------
-// Sum of v over the lower lanes of the wave and this one.
-__device__ __forceinline__ int64_t wave_scan(int64_t v, int lane) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int64_t u = __shfl_up(v, o, 64);
-    if (lane >= o) v += u;
-  }
-  return v;
-}
-
 // The first of `count` running sums that is above v (the last one is).
 __device__ __forceinline__ int first_above(const int64_t* sums, int count, int64_t v) {
   int a = 0, z = count - 1;
@@ -160,392 +140,6 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_blocks(
 }
 
 // ---------------------------------------------------------------------------
-// Append
-// ---------------------------------------------------------------------------
-// Four fp32 -> four E4M3 bytes, RNE, saturating, NaN -> 0x7F with its sign.
-__device__ __forceinline__ uint32_t e4m3_word(const float v[4]) {
-  uint32_t r = e4m3_pack2<false>(clamp448(v[0]), clamp448(v[1]), 0u);
-  r = e4m3_pack2<true>(clamp448(v[2]), clamp448(v[3]), r);
-#pragma unroll
-  for (int i = 0; i < 4; i++)
-    if (v[i] != v[i]) r = (r & ~(0xFFu << (8 * i))) | ((0x7Fu | ((__float_as_uint(v[i]) >> 24) & 0x80u)) << (8 * i));
-  return r;
-}
-
-// Four E4M3 bytes times 2^shift, rounded again.
-__device__ __forceinline__ uint32_t e4m3_word_shifted(uint32_t w, int shift) {
-  const auto a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, 1.0f, false);
-  const auto b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, 1.0f, true);
-  const float v[4] = {__builtin_ldexpf(a[0], shift), __builtin_ldexpf(a[1], shift), __builtin_ldexpf(b[0], shift),
-                      __builtin_ldexpf(b[1], shift)};
-  return e4m3_word(v);
-}
-
-// The least E8M0 code c with amax <= 448 * 2^(c-127), amax as its bits: 448 = 1.75 * 2^8, so
-// the biased exponent less 8, one more where the fraction is above .75.
-__device__ __forceinline__ int e8m0_cover(uint32_t bits) {
-  const int c = (int)(bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  return c > 0 ? c : 0;
-}
-
-// Eight elements as they were loaded.
-template <bool BF16>
-struct Raw8 {
-  uint32_t w[BF16 ? 4 : 8];
-  // the larger of m and the magnitudes, as bit patterns: one half word each for
-  // bf16 (both halves of m), one word for fp32; NaN and infinity come out largest
-  __device__ __forceinline__ uint32_t magnitude(uint32_t m) const {
-#pragma unroll
-    for (int i = 0; i < (BF16 ? 4 : 8); i++) {
-      if constexpr (BF16) {
-        const u16x2_t a = __builtin_bit_cast(u16x2_t, w[i] & 0x7FFF7FFFu), b = __builtin_bit_cast(u16x2_t, m);
-        m = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(a, b));
-      } else {
-        const uint32_t a = w[i] & 0x7FFFFFFFu;
-        m = a > m ? a : m;
-      }
-    }
-    return m;
-  }
-  __device__ __forceinline__ void widen(float v[8]) const {
-#pragma unroll
-    for (int i = 0; i < 8; i++)
-      v[i] = BF16 ? (i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2])) : __uint_as_float(w[BF16 ? 0 : i]);
-  }
-  // E4M3 codes of x * 2^(127-c); the finite magnitudes are at most 448 then
-  __device__ __forceinline__ u32x2_t codes(float scale_as_e8m0) const {
-    u32x2_t out;
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-      s16x2_t r = {0, 0};
-      if constexpr (BF16) {
-        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, w[2 * h]), scale_as_e8m0, false);
-        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, w[2 * h + 1]), scale_as_e8m0, true);
-      } else {
-        const uint32_t* f = w + (BF16 ? 0 : 4 * h);
-        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, __uint_as_float(f[0]), __uint_as_float(f[1]), scale_as_e8m0, false);
-        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, __uint_as_float(f[2]), __uint_as_float(f[3]), scale_as_e8m0, true);
-      }
-      out[h] = __builtin_bit_cast(uint32_t, r);
-    }
-    return out;
-  }
-};
-
-// One run (tokens t .. t+n-1 at offsets off .. off+n-1 of one page) of one
-// head, keys or values, by the whole workgroup.  A thread takes 8 channels of
-// the 4 tokens of an aligned quad of the page and keeps them in registers
-// between the run's maximum and its codes: values then leave as words of 4
-// tokens, which LDS turns into whole rows of the transposed page.  Bound by
-// bytes, so the arithmetic is kept to one and a half instructions an element:
-// maxima of bit patterns, two for bf16 at a time, and conversions that take
-// the scale; a run that holds a NaN or an infinity goes the long way.  8192
-// tokens of prompts, 8 heads of 128, bf16: 13.3 us a call (3.8 TB/s).
-template <bool BF16, bool VALUES, int D, int PAGE>
-__device__ __forceinline__ void append_run(const void* __restrict__ x, int64_t stride, int64_t t, int n, int off,
-                                           uint8_t* __restrict__ codes, uint8_t* __restrict__ scale, uint8_t* lds,
-                                           uint32_t* red) {
-  constexpr int CH = D / 8, ITEMS = PAGE / 4 * CH, R = (ITEMS + KV_THREADS - 1) / KV_THREADS, LROW = PAGE + 4;
-  const int tid = threadIdx.x, end = off + n;
-  const int old = off ? (int)*scale : 0;
-  Raw8<BF16> v[R][4];
-  uint32_t m = 0;
-#pragma unroll
-  for (int r = 0; r < R; r++) {
-    const int p = r * KV_THREADS + tid, o = p / CH * 4;            // o: first offset of the quad
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const bool in = o + i >= off && o + i < end;
-      const uint8_t* from = (const uint8_t*)x + ((t + (in ? o + i - off : 0)) * stride + (p % CH) * 8) * (BF16 ? 2 : 4);
-#pragma unroll
-      for (int e = 0; e < (BF16 ? 1 : 2); e++) {
-        const u32x4_t q = in ? ld16(from + 16 * e) : u32x4_t{0, 0, 0, 0};
-#pragma unroll
-        for (int b = 0; b < 4; b++) v[r][i].w[4 * e + b] = q[b];
-      }
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < R; r++)
-#pragma unroll
-    for (int i = 0; i < 4; i++) m = v[r][i].magnitude(m);
-  if constexpr (BF16) m = (m & 0xFFFFu) > (m >> 16) ? m << 16 : m & 0xFFFF0000u;
-  auto join = [&](uint32_t a) {               // the largest over the workgroup
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const uint32_t b = (uint32_t)__shfl_xor((int)a, o, 64);
-      a = a > b ? a : b;
-    }
-    if ((tid & 63) == 0) red[tid >> 6] = a;
-    __syncthreads();
-    a = red[0] > red[1] ? red[0] : red[1];
-    const uint32_t b = red[2] > red[3] ? red[2] : red[3];
-    return a > b ? a : b;
-  };
-  m = join(m);
-  const bool odd = m >= 0x7F800000u;          // NaN or infinity: the maximum of the others, element by element
-  if (odd) {
-    m = 0;
-#pragma unroll
-    for (int r = 0; r < R; r++)
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        float f[8];
-        v[r][i].widen(f);
-#pragma unroll
-        for (int e = 0; e < 8; e++) {
-          const uint32_t a = __float_as_uint(f[e]) & 0x7FFFFFFFu;
-          m = a < 0x7F800000u && a > m ? a : m;
-        }
-      }
-    __syncthreads();
-    m = join(m);
-  }
-  const int need = e8m0_cover(m);
-  const int c = need > old ? need : old;
-  const int moved = off && c > old ? off : 0; // tokens before the run whose codes change
-  if (tid == 0 && (!off || c != old)) *scale = (uint8_t)c;
-  const float sc = e8m0_as_scale((uint32_t)c);
-#pragma unroll
-  for (int r = 0; r < R; r++) {
-    const int p = r * KV_THREADS + tid, o = p / CH * 4, ch = (p % CH) * 8;
-    if (o + 3 < off || o >= end) continue;
-    u32x2_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      if (!odd) {
-        w[i] = v[r][i].codes(sc);
-      } else {
-        float q[8];
-        v[r][i].widen(q);
-#pragma unroll
-        for (int e = 0; e < 8; e++) q[e] = __builtin_ldexpf(q[e], 127 - c);
-        w[i] = u32x2_t{e4m3_word(q), e4m3_word(q + 4)};
-      }
-    }
-    if constexpr (!VALUES) {
-#pragma unroll
-      for (int i = 0; i < 4; i++)
-        if (o + i >= off && o + i < end) *reinterpret_cast<u32x2_t*>(codes + (o + i) * D + ch) = w[i];
-    } else {
-      // 4 tokens x 4 channels at a time: bytes of one channel into one word
-#pragma unroll
-      for (int hf = 0; hf < 2; hf++) {
-        const uint32_t lo01 = __builtin_amdgcn_perm(w[1][hf], w[0][hf], 0x05010400u);
-        const uint32_t hi01 = __builtin_amdgcn_perm(w[1][hf], w[0][hf], 0x07030602u);
-        const uint32_t lo23 = __builtin_amdgcn_perm(w[3][hf], w[2][hf], 0x05010400u);
-        const uint32_t hi23 = __builtin_amdgcn_perm(w[3][hf], w[2][hf], 0x07030602u);
-        uint32_t* l = reinterpret_cast<uint32_t*>(lds + (ch + 4 * hf) * LROW + o);
-        l[0] = __builtin_amdgcn_perm(lo23, lo01, 0x05040100u);
-        l[LROW / 4] = __builtin_amdgcn_perm(lo23, lo01, 0x07060302u);
-        l[2 * (LROW / 4)] = __builtin_amdgcn_perm(hi23, hi01, 0x05040100u);
-        l[3 * (LROW / 4)] = __builtin_amdgcn_perm(hi23, hi01, 0x07060302u);
-      }
-    }
-  }
-  if constexpr (!VALUES) {
-    for (int p = tid; p < moved * D / 4; p += KV_THREADS) {
-      uint32_t* w = reinterpret_cast<uint32_t*>(codes) + p;
-      *w = e4m3_word_shifted(*w, old - c);
-    }
-  } else {
-    __syncthreads();
-    if (n == PAGE) {                          // a whole page: 16-byte stores
-      for (int p = tid; p < D * PAGE / 16; p += KV_THREADS) {
-        const uint32_t* l = reinterpret_cast<const uint32_t*>(lds + p / (PAGE / 16) * LROW + p % (PAGE / 16) * 16);
-        *reinterpret_cast<u32x4_t*>(codes + p * 16) = u32x4_t{l[0], l[1], l[2], l[3]};
-      }
-    } else {
-      const int w0 = moved ? 0 : off >> 2, words = ((end + 3) >> 2) - w0;
-      for (int p = tid; p < D * words; p += KV_THREADS) {
-        const int d = p / words, w = w0 + p % words;
-        uint8_t* g = codes + d * PAGE + 4 * w;
-        // bytes [a, z) of the word are this run's
-        const int a = off - 4 * w > 0 ? off - 4 * w : 0, z = end - 4 * w < 4 ? end - 4 * w : 4;
-        const uint32_t fresh = a < 4 ? *reinterpret_cast<const uint32_t*>(lds + d * LROW + 4 * w) : 0u;
-        if (a == 0 && z == 4) {
-          *reinterpret_cast<uint32_t*>(g) = fresh;
-        } else if (moved && a > 0) {
-          const uint32_t had = *reinterpret_cast<const uint32_t*>(g);
-          const uint32_t kept = e4m3_word_shifted(had, old - c);
-          uint32_t res = 0;
-#pragma unroll
-          for (int b = 0; b < 4; b++) res |= (b < a ? kept : b < z ? fresh : had) & (0xFFu << (8 * b));
-          *reinterpret_cast<uint32_t*>(g) = res;
-        } else {
-          for (int b = a; b < z; b++) g[b] = (uint8_t)(fresh >> (8 * b));
-        }
-      }
-    }
-  }
-  __syncthreads();                            // LDS is free for the next run
-}
-
-// Runs of one token each (a decode step): `runs` has the chunk's tokens that
-// begin one, `slot` the slot of token t0 + lane.  D / 8 lanes a token, many
-// tokens at once and no barrier among them; the pages whose scale grew are
-// gone over by the whole workgroup afterwards.  64 tokens, 8 heads of 128: 4.2
-// us where no scale grows (5.3 as runs), 7.8 us where half of the pages' do and
-// 8.5 us where all do; 2048: 66 us, bound by the cache line that each value
-// byte of the transposed page touches (76 as runs).
-template <bool BF16, bool VALUES, int D, int PAGE>
-__device__ __forceinline__ void append_ones(const void* __restrict__ x, int64_t stride, int64_t t0, int chunk,
-                                            unsigned long long runs, int64_t slot, int heads, int head,
-                                            uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int* grown) {
-  constexpr int GL = D / 8, AT_ONCE = KV_THREADS / GL;
-  const int tid = threadIdx.x, lane = tid & 63, ch = tid % GL * 8;
-  if (tid < 64) grown[tid] = 0;
-  __syncthreads();
-  for (int base = 0; base < chunk; base += AT_ONCE) {
-    const int i = base + tid / GL;
-    const int64_t sl = __shfl(slot, i & 63, 64);
-    if (i >= chunk || !(runs >> i & 1)) continue;                  // the same for all lanes of a token
-    const int off = (int)(sl & (PAGE - 1));
-    const int64_t block = sl / PAGE * heads + head;
-    const int old = off ? (int)scales[block] : 0;
-    Raw8<BF16> v;
-    const uint8_t* from = (const uint8_t*)x + ((t0 + i) * stride + ch) * (BF16 ? 2 : 4);
-#pragma unroll
-    for (int e = 0; e < (BF16 ? 1 : 2); e++) {
-      const u32x4_t q = ld16(from + 16 * e);
-#pragma unroll
-      for (int b = 0; b < 4; b++) v.w[4 * e + b] = q[b];
-    }
-    auto join = [&](uint32_t a) {
-#pragma unroll
-      for (int o = 1; o < GL; o <<= 1) {
-        const uint32_t b = (uint32_t)__shfl_xor((int)a, o, 64);
-        a = a > b ? a : b;
-      }
-      return a;
-    };
-    uint32_t m = v.magnitude(0);
-    if constexpr (BF16) m = (m & 0xFFFFu) > (m >> 16) ? m << 16 : m & 0xFFFF0000u;
-    m = join(m);
-    const bool odd = m >= 0x7F800000u;        // NaN or infinity
-    float f[8];
-    if (odd) {
-      v.widen(f);
-      m = 0;
-#pragma unroll
-      for (int e = 0; e < 8; e++) {
-        const uint32_t a = __float_as_uint(f[e]) & 0x7FFFFFFFu;
-        m = a < 0x7F800000u && a > m ? a : m;
-      }
-      m = join(m);
-    }
-    const int need = e8m0_cover(m), c = need > old ? need : old;
-    u32x2_t w;
-    if (!odd) {
-      w = v.codes(e8m0_as_scale((uint32_t)c));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; e++) f[e] = __builtin_ldexpf(f[e], 127 - c);
-      w = u32x2_t{e4m3_word(f), e4m3_word(f + 4)};
-    }
-    uint8_t* p = codes + block * PAGE * D;
-    if constexpr (!VALUES) {
-      *reinterpret_cast<u32x2_t*>(p + off * D + ch) = w;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; e++) p[(ch + e) * PAGE + off] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
-    }
-    if (ch == 0 && (!off || c != old)) scales[block] = (uint8_t)c;
-    if (ch == 0 && off && c > old) grown[i] = c - old;
-  }
-  __syncthreads();
-  const int shift = grown[lane];
-  for (unsigned long long todo = __ballot(shift != 0); todo; todo &= todo - 1) {
-    const int i = __builtin_ctzll(todo);
-    const int64_t sl = __shfl(slot, i, 64);
-    const int by = -__shfl(shift, i, 64), off = (int)(sl & (PAGE - 1));
-    uint8_t* p = codes + (sl / PAGE * heads + head) * PAGE * D;
-    if constexpr (!VALUES) {
-      for (int j = tid; j < off * D / 4; j += KV_THREADS) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(p) + j;
-        *w = e4m3_word_shifted(*w, by);
-      }
-    } else {
-      const int words = (off + 3) >> 2;
-      for (int j = tid; j < D * words; j += KV_THREADS) {
-        const int k = j % words;
-        uint32_t* w = reinterpret_cast<uint32_t*>(p + j / words * PAGE) + k;
-        const uint32_t had = *w, keep = off - 4 * k < 4 ? ~0u << (8 * (off - 4 * k)) : 0u;   // bytes from `off` on
-        *w = (had & keep) | (e4m3_word_shifted(had, by) & ~keep);
-      }
-    }
-  }
-}
-
-// Workgroup (x, head, keys or values) writes the runs that begin in tokens
-// [x * chunk, (x + 1) * chunk), chunk <= 64: one token where that gives no more
-// than 2048 workgroups, else up to a page, since a workgroup without a run of
-// its own costs its start (8192 tokens: 14.7 us at 2048, 17.4 at 4096, 22 at 8192).
-template <bool BF16, int D, int PAGE>
-__global__ __launch_bounds__(KV_THREADS) void k_kv_append(
-    const void* __restrict__ k, int64_t k_stride, const void* __restrict__ v, int64_t v_stride,
-    const int64_t* __restrict__ slots, int64_t tokens, int chunk, int64_t num_pages, uint8_t* __restrict__ k_codes,
-    uint8_t* __restrict__ k_scales, uint8_t* __restrict__ v_codes, uint8_t* __restrict__ v_scales) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[D * (PAGE + 4)];
-  __shared__ uint32_t red[KV_THREADS / 64];
-  __shared__ int grown[64];
-  const int lane = threadIdx.x & 63, head = blockIdx.y, heads = gridDim.y;
-  const int64_t limit = num_pages * PAGE;
-  const int64_t t0 = (int64_t)blockIdx.x * chunk;
-  // every wave looks at the chunk's slots and those that a run of them may reach
-  auto slot_of = [&](int64_t t) { return t < tokens ? slots[t] : (int64_t)-1; };
-  const int64_t s0 = slot_of(t0 + lane), s1 = slot_of(t0 + 64 + lane);
-  const int64_t before0 = t0 ? slots[t0 - 1] : -1;
-  int64_t before = __shfl_up(s0, 1, 64);
-  before = lane ? before : before0;
-  const bool valid = s0 >= 0 && s0 < limit;
-  const bool begins = valid && lane < chunk && !((s0 & (PAGE - 1)) && before == s0 - 1);
-  unsigned long long runs = __ballot(begins);
-  // follows: the token extends the run of the one before it
-  const int64_t last0 = __shfl(s0, 63, 64), up1 = __shfl_up(s1, 1, 64), before1 = lane ? up1 : last0;
-  const unsigned long long on0 = __ballot((s0 & (PAGE - 1)) && before == s0 - 1);
-  const unsigned long long on1 = __ballot((s1 & (PAGE - 1)) && before1 == s1 - 1);
-  const int64_t col = (int64_t)head * D * (BF16 ? 2 : 4);
-  // no token of the chunk, nor the one behind it, goes on in another's run
-  const unsigned long long behind = chunk < 64 ? on0 & ((2ull << chunk) - 2) : (on0 & ~1ull) | (on1 & 1);
-  if (!behind) {
-    if (blockIdx.z == 0)
-      append_ones<BF16, false, D, PAGE>((const uint8_t*)k + col, k_stride, t0, chunk, runs, s0, heads, head, k_codes,
-                                        k_scales, grown);
-    else
-      append_ones<BF16, true, D, PAGE>((const uint8_t*)v + col, v_stride, t0, chunk, runs, s0, heads, head, v_codes,
-                                       v_scales, grown);
-    return;
-  }
-  unsigned long long on2 = 0;
-  if constexpr (PAGE == 128) {
-    const int64_t s2 = slot_of(t0 + 128 + lane);
-    const int64_t last1 = __shfl(s1, 63, 64), up2 = __shfl_up(s2, 1, 64), before2 = lane ? up2 : last1;
-    on2 = __ballot((s2 & (PAGE - 1)) && before2 == s2 - 1 && lane < 63);
-  }
-  while (runs) {
-    const int i = __builtin_ctzll(runs);
-    runs &= runs - 1;
-    const int64_t t = t0 + i, slot = __shfl(s0, i, 64);
-    // tokens that follow i without a gap: up to PAGE - 1 of them
-    const unsigned long long a = i < 63 ? ~(on0 >> (i + 1)) : ~0ull;
-    int n = 1 + (a ? __builtin_ctzll(a) : 64);
-    if (n >= 64 - i) {
-      n = 64 - i + (~on1 ? __builtin_ctzll(~on1) : 64);
-      if (PAGE == 128 && n == 128 - i) n += __builtin_ctzll(~on2);   // a page is at most 128 tokens: ~on2 != 0
-    }
-    const int off = (int)(slot & (PAGE - 1));
-    const int64_t block = slot / PAGE * heads + head;
-    if (blockIdx.z == 0)
-      append_run<BF16, false, D, PAGE>((const uint8_t*)k + col, k_stride, t, n, off, k_codes + block * PAGE * D,
-                                       k_scales + block, lds, red);
-    else
-      append_run<BF16, true, D, PAGE>((const uint8_t*)v + col, v_stride, t, n, off, v_codes + block * PAGE * D,
-                                      v_scales + block, lds, red);
-  }
-}
-
-// ---------------------------------------------------------------------------
 // Attention
 // ---------------------------------------------------------------------------
 // Both attention kernels compute the transposed products S^T = K q^T and
@@ -561,267 +155,6 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_append(
 // channel of V^T.
 //
 // Rows of one key/value head are numbered r = query * group + head in group:
-// the `group` query heads that share a key/value head share its tiles.
-constexpr int TILE = 64;                      // tokens per step
-constexpr int PROWS = 128, PTHREADS = 256;    // rows of a prompt tile, threads of its workgroup
-// Requests of at most this many rows go through the decode kernel: its tiles of
-// 32 read K and V once each, the prompt kernel once for 128, but a prompt
-// tile's staging and barriers cost the same however few there are.  24 requests
-// on 500-6000 tokens, 8 heads of 128: 48 rows 54 us decoded against 58 in
-// prompt tiles, 64 rows 56 against 57, 128 rows 79 against 66.
-constexpr int SHORT_ROWS = 64;
-// Decode workgroups over all heads: two a CU, as the registers of D = 128 allow
-// (256: 2-4 % slower on drafted tokens; 768 and 1024 at D = 64, where they fit:
-// 9 and 14 % slower on short windows).
-constexpr int DEC_GROUPS = 512;
-// A workgroup a row tile where no request can have more tiles than this (few row
-// tiles, enough of them for half the CUs) and they fit the chip twice over.  The
-// host knows lengths by the table's width and the window only: 1000 tokens take
-// 12.8 us on a table of 17 columns of 64, 17.0 us on one of 520, in shares.  8
-// heads of 128, calls back to back: 1 x 700 tokens 12.8 us against 18.0 in
-// shares and a join, 1 x 2000 17 against 16; 16 x 2000 18.5 against 21.8, 16 x
-// 4000 30 against 31.
-constexpr int SOLO_TILES = 20, SOLO_TILES_MANY = 40;
-constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
-
-struct KvArgs {
-  const uint16_t* q;
-  int64_t q_stride;
-  const int32_t* cu_q;
-  const int32_t* kv_lens;
-  int64_t batch, tokens;
-  int q_heads, kv_heads, group, window;
-  const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
-  int log_page;
-  int64_t num_pages;
-  const int32_t* table;
-  int64_t max_blocks;
-  float sm_scale, softcap;
-  uint16_t* out;
-  float* lse;
-};
-
-// Partial results of the prompt kernel's split rows: `used[0]` slots are in
-// use; slot s of head h holds PROWS * D sums and (maximum, sum) pairs.  `rec`
-// names the slot's rows in the entry of the first split, with the number of
-// splits that follow.
-struct KvRec {
-  int32_t splits;                             // 0 in the entries of the other splits
-  int32_t rows, query0, head0;                // the first row: query row of the tensors, head in its group
-};
-struct KvPart {
-  int64_t splits;                             // aim: items per head, over which the tiles are spread
-  int64_t slots;                              // room in the arrays below: nothing is written past it, whatever cu_q holds
-  int min_tiles;                              // no split is shorter
-  int64_t* used;
-  KvRec* rec;
-  float* sums;
-  float* stats;
-};
-
-// Partial results of the decode kernel.  Wave x of a head (4 to a workgroup)
-// has two slots: 2 x for a row tile that begins in its share of the work and
-// ends behind it, 2 x + 1 for one that began before.  A workgroup inside one
-// row tile joins its waves first and uses the slots of its first wave alone.
-// chain[x] describes the row tile of slot 2 x; every wave writes its own entry.
-struct KvChain {
-  int32_t rows, query0, head0;                // 0 rows: none
-  int32_t first, last;                        // waves that share the row tile
-  int32_t first_joined, last_joined;          // whether the workgroups of those joined their waves
-};
-struct KvShare {
-  int groups, rows;                           // workgroups per head (0: one a row tile), rows of a slot
-  int log_joins;                              // log2 of the workgroups of k_kv_join for a row tile
-  KvChain* chain;
-  float* sums;
-  float* stats;
-};
-
-// Which requests a launch takes: all of them, those of at most SHORT_ROWS rows,
-// or the others.
-enum { REQ_ALL, REQ_SHORT, REQ_LONG };
-
-// One item of work: rows [r0, r0 + rows) of a request, a share of their tiles.
-// Uniform over the workgroup (read from one lane, so it lives in scalar registers).
-struct KvItem {
-  int request, q0, n, len;                    // first query row, queries, tokens in the cache
-  int r0, rows, splits, split;
-  int64_t slot;                               // partial slot, where splits > 1
-};
-
-__device__ __forceinline__ int64_t wave_sum(int64_t v) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
-__device__ __forceinline__ int lane32(int v, int src) { return __builtin_amdgcn_readlane(v, src); }
-__device__ __forceinline__ int64_t lane64(int64_t v, int src) {
-  return (int64_t)(((uint64_t)(uint32_t)lane32((int)(v >> 32), src) << 32) | (uint32_t)lane32((int)v, src));
-}
-
-// The lowest token that position `pos` sees (window 0: the first).
-__device__ __forceinline__ int kv_lowest(int pos, int window) { return window > 0 && pos >= window ? pos - window + 1 : 0; }
-
-// Request i (its lengths clamped to what the tensors hold): first query row,
-// queries, tokens, tiles that some query sees, row tiles of R rows.
-struct KvRequest {
-  int q0, n, len, first, tiles, row_tiles;    // first: the first of the tiles
-  template <int R, int WHICH>
-  __device__ __forceinline__ void load(const KvArgs& A, int64_t i) {
-    q0 = n = len = 0;
-    if (i < A.batch) {
-      const int cap = (int)(A.max_blocks << A.log_page);
-      int a = A.cu_q[i], z = A.cu_q[i + 1];
-      len = A.kv_lens[i];
-      a = a < 0 ? 0 : a;
-      z = z > A.tokens ? (int)A.tokens : z;
-      q0 = a;
-      n = z > a ? z - a : 0;
-      len = len < 0 ? 0 : len > cap ? cap : len;
-    }
-    const int rows = n * A.group;             // below 2^31, as tokens * group is
-    if (WHICH == REQ_SHORT ? rows > SHORT_ROWS : WHICH == REQ_LONG ? rows <= SHORT_ROWS : false) n = 0;
-    row_tiles = n > 0 ? (int)(((int64_t)rows + R - 1) / R) : 0;
-    first = kv_lowest(len - n, A.window) / TILE;
-    tiles = len > 0 ? (len - 1) / TILE - first + 1 : 0;
-  }
-  __device__ __forceinline__ KvRequest from(int src) const {       // another lane's
-    return KvRequest{lane32(q0, src), lane32(n, src), lane32(len, src), lane32(first, src), lane32(tiles, src),
-                     lane32(row_tiles, src)};
-  }
-};
-
-// Every wave finds its item itself, from the lengths: the tiles of all
-// requests are spread evenly over about part.splits items, a request of
-// `tiles` tiles being cut into tiles / share splits per row tile, to the
-// nearest (rounding up costs more in partial sums than it evens out).
-// False if there is no such item.
-template <int R, int WHICH>
-__device__ __forceinline__ bool kv_find(const KvArgs& A, const KvPart& part, int64_t item, bool count_all, KvItem& it) {
-  const int lane = threadIdx.x & 63;
-  KvRequest q;
-  int64_t total = 0;
-  for (int64_t base = 0; base < A.batch; base += 64) {
-    q.load<R, WHICH>(A, base + lane);
-    total += (int64_t)q.tiles * q.row_tiles;
-  }
-  total = lane64(wave_sum(total), 0);
-  int64_t share = (total + part.splits - 1) / part.splits;
-  share = share < part.min_tiles ? part.min_tiles : share;
-  const int per = share > 0x7FFFFFFF ? 0x7FFFFFFF : (int)share;
-  int64_t items = 0, slots = 0;
-  bool found = false;
-  for (int64_t base = 0; base < A.batch; base += 64) {
-    if (A.batch > 64) q.load<R, WHICH>(A, base + lane);
-    const int rounded = (int)((2 * (int64_t)q.tiles + per) / (2 * (int64_t)per)), splits = rounded > 1 ? rounded : 1;
-    const int64_t own = (int64_t)q.row_tiles * splits, part_own = splits > 1 ? own : 0;
-    const int64_t end = items + wave_scan(own, lane), part_end = slots + wave_scan(part_own, lane);
-    const unsigned long long at = __ballot(end > item);
-    if (at && !found) {
-      const int src = __builtin_ctzll(at);
-      const int idx = (int)(item - lane64(end - own, src));
-      it.splits = lane32(splits, src);
-      it.split = idx % it.splits;
-      it.request = (int)base + src;
-      it.q0 = lane32(q.q0, src);
-      it.n = lane32(q.n, src);
-      it.len = lane32(q.len, src);
-      it.r0 = (lane32(q.row_tiles, src) - 1 - idx / it.splits) * R;  // the longest rows first
-      const int left = it.n * A.group - it.r0;
-      it.rows = left < R ? left : R;
-      it.slot = lane64(part_end - part_own, src) + idx;
-      found = true;
-    }
-    if (found && !count_all) return true;
-    items = lane64(end, 63);
-    slots = lane64(part_end, 63);
-  }
-  if (count_all && threadIdx.x == 0) part.used[0] = slots < part.slots ? slots : part.slots;
-  return found;
-}
-
-// Queries of a row tile: row r0 is query `first` of the request and head
-// `head0` of the group; row r0 + i is i rows on.
-struct KvRows {
-  int first, head0, pos0;                     // pos0: position of query `first`
-  __device__ __forceinline__ KvRows(const KvArgs& A, int r0, int n, int len)
-      : first((int)((uint32_t)r0 / (uint32_t)A.group)), head0((int)((uint32_t)r0 % (uint32_t)A.group)),
-        pos0(len - n + first) {}
-  __device__ __forceinline__ int query(const KvArgs& A, int i) const { return (int)((uint32_t)(head0 + i) / (uint32_t)A.group); }
-  __device__ __forceinline__ int head(const KvArgs& A, int i) const { return (int)((uint32_t)(head0 + i) % (uint32_t)A.group); }
-};
-
-// Tokens [lo, hi) that the item's rows see between them, and its tiles [t0, t1).
-__device__ __forceinline__ void kv_tiles(const KvArgs& A, const KvItem& it, const KvRows& rows, int& lo, int& hi,
-                                         int& t0, int& t1) {
-  const int last = rows.pos0 + rows.query(A, it.rows - 1);
-  hi = last < 0 ? 0 : last + 1;
-  lo = kv_lowest(rows.pos0, A.window);
-  lo = lo < hi ? lo : hi;
-  const int a = lo / TILE, n = hi > lo ? (hi - 1) / TILE + 1 - a : 0;
-  t0 = a + (int)((int64_t)n * it.split / it.splits);
-  t1 = a + (int)((int64_t)n * (it.split + 1) / it.splits);
-}
-
-// Scores to base 2: dot * mul, or, capped, cap * tanh(x) * log2 e with x = dot *
-// sm_scale / cap.  Sixteen at a time: where all of a wave's have |x| <= 1/4 (most
-// scores are far below their cap), by the series of tanh up to x^7, whose next
-// term is under 3.4e-7 of the result; else as cap - 2 cap / (e^2x + 1), off by
-// at most cap * 2^-22.  Both take the same time (chunks 560 us); the series
-// keeps small scores exact (lse off by 5e-8 instead of 2.5e-7, 2-norm).  It is
-// taken in powers of the dot, with k = sm_scale / cap in its coefficients: for k
-// from 2^-16 on (softcap 50 at heads of 128 has 2^-9) the squares of dots of up
-// to 1 / 4k and the coefficient of k^7 are in fp32's range with 2^20 to spare
-// against the bound.  A smaller k leaves it, so its scores all go by the
-// exponential.  (A series in x itself holds for every k but takes a
-// multiplication more a score: chunks 581 us.)
-template <bool CAP>
-struct KvScore {
-  float mul;                                  // of what `cap` leaves
-  float limit, to2x, twice, a0, a1, a2, a3;
-  __device__ __forceinline__ explicit KvScore(const KvArgs& A) {
-    mul = CAP ? 1.0f : A.sm_scale * LOG2E;
-    if constexpr (CAP) {
-      const float k = A.sm_scale / A.softcap, k2 = k * k;
-      limit = k >= 0x1p-16f ? 0.25f / k : 0.0f;
-      to2x = 2.0f * LOG2E * k;
-      twice = A.softcap * LOG2E;
-      a0 = A.sm_scale * LOG2E;
-      a1 = a0 * k2 * (-1.0f / 3.0f);
-      a2 = a0 * k2 * k2 * (2.0f / 15.0f);
-      a3 = a0 * k2 * k2 * k2 * (-17.0f / 315.0f);
-    }
-  }
-  __device__ __forceinline__ float series(float s) const {
-    const float y = s * s;
-    return s * __builtin_fmaf(__builtin_fmaf(__builtin_fmaf(a3, y, a2), y, a1), y, a0);
-  }
-  __device__ __forceinline__ float exponential(float s) const {
-    return __builtin_fmaf(__builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(s * to2x) + 1.0f), -2.0f * twice, twice);
-  }
-  // `edge`: some of the sixteen are of tokens that their row does not see.  The form
-  // of one that it does see must not follow their bytes, so each goes by itself then
-  // (the series where all are below the limit is what each would take).
-  template <typename T>
-  __device__ __forceinline__ void cap(T& s, bool edge) const {
-    if constexpr (CAP) {
-      float big = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 16; i++) big = __builtin_fmaxf(big, __builtin_fabsf(s[i]));
-      if (!__any(big > limit)) {
-#pragma unroll
-        for (int i = 0; i < 16; i++) s[i] = series(s[i]);
-      } else if (!edge) {
-#pragma unroll
-        for (int i = 0; i < 16; i++) s[i] = exponential(s[i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; i++) s[i] = __builtin_fabsf(s[i]) > limit ? exponential(s[i]) : series(s[i]);
-      }
-    }
-  }
-};
-
 // Eight E4M3 bytes with E8M0 scale operand -> eight bf16.
 __device__ __forceinline__ bf16x8_t e4m3_bf16x8(uint32_t a, uint32_t b, float scale) {
   const u32x4_t w = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, false)),
@@ -1672,117 +1005,6 @@ __global__ __launch_bounds__(PTHREADS, D == 64 ? 3 : 2) void k_kv_prompt(const K
   }
 }
 
-// Joins `parts` partial results of rows [row0, row0 + some) of one head, a wave
-// taking every fourth row: its lanes hold 4 channels each, and the groups of
-// lanes that this leaves share the parts, 4 of them in flight per lane, since a
-// long context alone in its batch has many parts of few rows.  slot_of(i) is
-// the place of part i among the slots of `room` rows.
-template <int D, typename SLOT>
-__device__ __forceinline__ void kv_join(const KvArgs& A, const float* sums, const float* stats, int room, int kvh,
-                                        int row0, int some, int rows, int query0, int head0, int parts, SLOT slot_of) {
-  constexpr int LANES = D / 4, GROUPS = 64 / LANES, DEEP = 4;
-  const int lane = threadIdx.x & 63, grp = lane / LANES, ch = (lane % LANES) * 4;
-  for (int row = row0 + threadIdx.x / 64; row < row0 + some && row < rows; row += KV_THREADS / 64) {
-    float M = -INFINITY, L = 0.0f;
-    f32x4_t acc = {0, 0, 0, 0};
-    for (int s0 = grp; s0 < parts; s0 += GROUPS * DEEP) {
-      float ms[DEEP], ls[DEEP], top = M;
-      f32x4_t v[DEEP];
-#pragma unroll
-      for (int u = 0; u < DEEP; u++) {
-        const int sp = s0 + GROUPS * u;
-        const int64_t a = (slot_of(sp < parts ? sp : s0) * A.kv_heads + kvh) * room + row;
-        ms[u] = stats[2 * a];
-        ls[u] = stats[2 * a + 1];
-        v[u] = *reinterpret_cast<const f32x4_t*>(sums + a * D + ch);
-        if (sp >= parts) ms[u] = -INFINITY;
-        top = __builtin_fmaxf(top, ms[u]);
-      }
-      const float keep = M == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(M - top);
-      M = top;
-      L *= keep;
-      acc *= keep;
-#pragma unroll
-      for (int u = 0; u < DEEP; u++) {
-        const float f = ms[u] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ms[u] - M);
-        L = __builtin_fmaf(f, ls[u], L);
-#pragma unroll
-        for (int e = 0; e < 4; e++) acc[e] = __builtin_fmaf(f, v[u][e], acc[e]);
-      }
-    }
-#pragma unroll
-    for (int o = LANES; o < 64; o <<= 1) {
-      const float mo = __shfl_xor(M, o, 64), lo = __shfl_xor(L, o, 64), top = __builtin_fmaxf(M, mo);
-      const float a = M == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(M - top);
-      const float b = mo == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mo - top);
-      L = a * L + b * lo;
-#pragma unroll
-      for (int e = 0; e < 4; e++) acc[e] = a * acc[e] + b * __shfl_xor(acc[e], o, 64);
-      M = top;
-    }
-    if (grp == 0) {
-      const uint32_t rr = (uint32_t)head0 + row, group = A.group;
-      const int64_t token = (int64_t)query0 + rr / group, orow = token * A.q_heads + kvh * group + rr % group;
-      if (token < 0 || token >= A.tokens) continue;
-      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-      *reinterpret_cast<u32x2_t*>(A.out + orow * D + ch) =
-          u32x2_t{pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv)};
-      if (A.lse && ch == 0) A.lse[orow] = L == 0.0f ? -INFINITY : (M + __builtin_log2f(L)) * LN2;
-    }
-  }
-}
-
-// Workgroups of the decode kernel's waves first, 2^log_joins each, then
-// PROWS / 16 for each prompt slot.  8 rows each where more than 8 are likely (24
-// requests of 1-7 drafted tokens 10.2 -> 8.2 us), 16 else, since most of these
-// workgroups find nothing (64 requests of 4 rows 4.6 us, 5.8 in eights).
-template <int D, int NR>
-__global__ __launch_bounds__(KV_THREADS) void k_kv_join(const KvArgs A, const KvShare dec, const KvPart pro) {
-  const int kvh = (int)(blockIdx.x % (unsigned)A.kv_heads);
-  int64_t x = blockIdx.x / (unsigned)A.kv_heads;
-  const int64_t decode = 4 * (int64_t)dec.groups << dec.log_joins;
-  if (x < decode) {
-    const KvChain c = dec.chain[x >> dec.log_joins];
-    const int some = 16 * NR >> dec.log_joins, row0 = (int)(x & ((1 << dec.log_joins) - 1)) * some;
-    if (c.rows == 0) return;
-    // parts: the first workgroup's, one for each between, the last workgroup's
-    const int ga = c.first / 4, gz = c.last / 4;
-    const int a = c.first_joined ? 1 : (gz > ga ? 4 * ga + 3 : c.last) - c.first + 1;
-    const int mid = gz > ga ? gz - ga - 1 : 0, z = gz > ga ? (c.last_joined ? 1 : c.last - 4 * gz + 1) : 0;
-    kv_join<D>(A, dec.sums, dec.stats, dec.rows, kvh, row0, some, c.rows, c.query0, c.head0, a + mid + z,
-               [&](int i) -> int64_t {
-                 if (i < a) return i == 0 ? 2 * c.first : 2 * (c.first + i) + 1;
-                 return i < a + mid ? 8 * (ga + 1 + i - a) + 1 : 2 * (4 * gz + i - a - mid) + 1;
-               });
-    return;
-  }
-  x -= decode;
-  const int64_t slot = x / (PROWS / 16);
-  if (slot >= pro.used[0]) return;
-  const KvRec rec = pro.rec[slot];
-  // entries that ranges of rows on top of each other left unwritten hold anything
-  if (rec.splits <= 0 || slot + rec.splits > pro.slots || rec.rows > PROWS) return;
-  kv_join<D>(A, pro.sums, pro.stats, PROWS, kvh, (int)(x % (PROWS / 16)) * 16, 16, rec.rows, rec.query0, rec.head0, rec.splits,
-             [&](int i) -> int64_t { return slot + i; });
-}
-
-int log2_page(int page) {
-  return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : page == 128 ? 7 : -1;
-}
-
-template <bool BF16, int D>
-void launch_append(int page, dim3 grid, hipStream_t s, const void* k, int64_t ks, const void* v, int64_t vs,
-                   const int64_t* slots, int64_t tokens, int chunk, int64_t num_pages, uint8_t* kc, uint8_t* ksc,
-                   uint8_t* vc, uint8_t* vsc) {
-#define WQ_APPEND(PAGE) \
-  k_kv_append<BF16, D, PAGE><<<grid, KV_THREADS, 0, s>>>(k, ks, v, vs, slots, tokens, chunk, num_pages, kc, ksc, vc, vsc)
-  if (page == 16) WQ_APPEND(16);
-  else if (page == 32) WQ_APPEND(32);
-  else if (page == 64) WQ_APPEND(64);
-  else WQ_APPEND(128);
-#undef WQ_APPEND
-}
-
 }  // namespace
 
 extern "C" {
@@ -1811,113 +1033,9 @@ wq_status wq_kv_blocks(const int32_t* ctx_lens, const int32_t* new_lens, int64_t
       positions, cu_new, kv_lens, state);
   return wq_launch_status();
 }
-
-wq_status wq_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride, int x_dtype,
-                       const int64_t* slots, int64_t tokens, int32_t heads, int32_t head_dim, int32_t page,
-                       int64_t num_pages, uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes, uint8_t* v_scales,
-                       void* stream) {
-  if ((x_dtype != WQ_F32 && x_dtype != WQ_BF16) || (head_dim != 64 && head_dim != 128) || log2_page(page) < 0)
-    return WQ_EUNSUPPORTED;
-  if (tokens < 0 || tokens > 0x7FFFFFFF || heads < 1 || heads > 65535 || num_pages < 1) return WQ_EINVAL;
-  if (!k_codes || !k_scales || !v_codes || !v_scales || (tokens > 0 && (!k || !v || !slots))) return WQ_EINVAL;
-  const int64_t row = (int64_t)heads * head_dim;
-  if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8 || k_stride > (int64_t(1) << 40) ||
-      v_stride > (int64_t(1) << 40) || !wq_numel_ok(num_pages, row * page) || !wq_numel_ok(tokens ? tokens : 1, row))
-    return WQ_EINVAL;
-  if (!wq_aligned(k) || !wq_aligned(v) || !wq_aligned(k_codes) || !wq_aligned(v_codes)) return WQ_EALIGN;
-  if (tokens == 0) return WQ_OK;
-  int chunk = 1;
-  while (chunk < 64 && chunk < page && (tokens + chunk - 1) / chunk * heads * 2 > 2048) chunk *= 2;
-  const dim3 grid((unsigned)((tokens + chunk - 1) / chunk), (unsigned)heads, 2);
-  hipStream_t s = (hipStream_t)stream;
-  const bool bf = x_dtype == WQ_BF16;
-  if (bf && head_dim == 128)
-    launch_append<true, 128>(page, grid, s, k, k_stride, v, v_stride, slots, tokens, chunk, num_pages, k_codes,
-                             k_scales, v_codes, v_scales);
-  else if (bf)
-    launch_append<true, 64>(page, grid, s, k, k_stride, v, v_stride, slots, tokens, chunk, num_pages, k_codes,
-                            k_scales, v_codes, v_scales);
-  else if (head_dim == 128)
-    launch_append<false, 128>(page, grid, s, k, k_stride, v, v_stride, slots, tokens, chunk, num_pages, k_codes,
-                              k_scales, v_codes, v_scales);
-  else
-    launch_append<false, 64>(page, grid, s, k, k_stride, v, v_stride, slots, tokens, chunk, num_pages, k_codes,
-                             k_scales, v_codes, v_scales);
-  return wq_launch_status();
-}
-
 }  // extern "C"
 
 namespace {
-
-// Items aimed at for prompts, over all key/value heads (two workgroups a CU; 256
-// leaves 24 x 128 rows at 80 us instead of 66, 1024 slows 4 x 512 queries on
-// 4000 tokens from 164 to 190 us by its partial sums), and the fewest tiles of
-// a split (1: the same; 16: 72 us instead of 66).
-constexpr int64_t PRO_ITEMS = 512;
-constexpr int PRO_MIN = 4;
-
-// What a call launches and where its workspace lies.  Prompt items per head are
-// at most splits + row tiles; slots (items of requests with two splits or
-// more) at most 2 * splits, and no more than the tiles of the table's width
-// allow.  The decode kernel has as many workgroups as the chip holds at once
-// (two a CU, as its registers allow), or one a head.
-struct KvPlan {
-  bool prompt, solo;                          // solo: decode only, a workgroup a row tile, nothing to join
-  int nr;                                     // 16-row columns of a decode tile
-  int groups, rows, log_joins;                // decode workgroups per head, rows of its slots, joins a row tile
-  int64_t pro_splits, pro_items, pro_slots;
-  size_t dec_sums, dec_stats, pro_used, pro_rec, pro_sums, pro_stats, bytes;
-};
-
-KvPlan kv_plan(int64_t batch, int64_t tokens, int64_t max_q, int q_heads, int kv_heads, int head_dim, int page,
-               int64_t max_blocks, int64_t window) {
-  KvPlan p = {};
-  const int64_t group = q_heads / kv_heads, reqs = batch < tokens ? batch : tokens;
-  const int64_t tiles = (max_blocks * page + TILE - 1) / TILE;
-  const int64_t most_q = max_q > 0 && max_q < tokens ? max_q : tokens;
-  p.prompt = most_q * group > SHORT_ROWS;
-  p.nr = most_q * group <= 16 ? 1 : 2;
-  p.rows = 16 * p.nr;
-  p.log_joins = (p.nr == 2) + (!p.prompt && most_q * group > 8);
-  const int64_t wgs = DEC_GROUPS / kv_heads, row_tiles = tokens * group / p.rows + reqs;
-  const int64_t seen = window > 0 && window < tiles * TILE ? (window + most_q - 2) / TILE + 2 : tiles;
-  const int64_t work = row_tiles * kv_heads;
-  p.solo = !p.prompt && (seen < tiles ? seen : tiles) <= (work < DEC_GROUPS / 4 ? SOLO_TILES : SOLO_TILES_MANY) &&
-           work <= 2 * DEC_GROUPS;
-  p.groups = (int)(p.solo ? row_tiles : wgs > 1 ? wgs : 1);
-  if (p.solo) return p;
-  p.pro_splits = (PRO_ITEMS + kv_heads - 1) / kv_heads;
-  const int64_t pro_rows = p.prompt ? tokens * group / PROWS + reqs : 0;
-  p.pro_items = p.prompt ? pro_rows + p.pro_splits : 0;
-  if (p.prompt && tiles > PRO_MIN) {
-    const int64_t most = (tiles + PRO_MIN - 1) / PRO_MIN;
-    p.pro_slots = pro_rows > 2 * p.pro_splits / most ? 2 * p.pro_splits : pro_rows * most;
-  }
-  size_t at = 0;
-  auto take = [&](size_t n) {
-    const size_t a = at;
-    at += (n + 255) & ~(size_t)255;
-    return a;
-  };
-  const size_t slots = 8 * (size_t)p.groups * kv_heads * p.rows;
-  take(4 * (size_t)p.groups * sizeof(KvChain));
-  p.dec_sums = take(slots * head_dim * 4);
-  p.dec_stats = take(slots * 8);
-  p.pro_used = take(8);
-  p.pro_rec = take(p.pro_slots * sizeof(KvRec));
-  p.pro_sums = take((size_t)p.pro_slots * kv_heads * PROWS * head_dim * 4);
-  p.pro_stats = take((size_t)p.pro_slots * kv_heads * PROWS * 8);
-  p.bytes = at;
-  return p;
-}
-
-bool kv_sizes_ok(int64_t batch, int64_t tokens, int64_t max_q, int32_t q_heads, int32_t kv_heads, int32_t page,
-                 int64_t max_blocks) {
-  return batch >= 0 && batch <= 0x7FFFFFFF && tokens >= 0 && tokens <= 0x7FFFFFFF && max_q >= 0 &&
-         max_q <= 0x7FFFFFFF && kv_heads >= 1 && q_heads >= kv_heads && q_heads % kv_heads == 0 && q_heads <= 65535 &&
-         tokens * (q_heads / kv_heads) <= 0x7FFFFFFF - PROWS && max_blocks >= 1 && max_blocks <= 0x7FFFFF00 / page;
-}
 
 template <int D, bool CAP>
 void launch_attention(const KvArgs& A, const KvPlan& p, const KvShare& dec, const KvPart& pro, hipStream_t s) {
@@ -1937,7 +1055,6 @@ void launch_attention(const KvArgs& A, const KvPlan& p, const KvShare& dec, cons
   if (p.nr == 2) k_kv_join<D, 2><<<joins, KV_THREADS, 0, s>>>(A, dec, pro);
   else k_kv_join<D, 1><<<joins, KV_THREADS, 0, s>>>(A, dec, pro);
 }
-
 }  // namespace
 
 extern "C" {
@@ -1949,47 +1066,26 @@ size_t wq_kv_attention_workspace_size(int64_t batch, int64_t tokens, int64_t max
     return 0;
   return batch && tokens ? kv_plan(batch, tokens, max_q, q_heads, kv_heads, head_dim, page, max_blocks, window).bytes : 0;
 }
-
 wq_status wq_kv_attention(const void* q_bf16, int64_t q_stride, const int32_t* cu_q, const int32_t* kv_lens,
                           int64_t batch, int64_t tokens, int64_t max_q, int32_t q_heads, int32_t kv_heads,
                           int32_t head_dim, const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
                           const uint8_t* v_scales, int32_t page, int64_t num_pages, const int32_t* block_table,
                           int64_t max_blocks, float sm_scale, float softcap, int64_t window, uint16_t* out,
                           float* lse, void* workspace, size_t ws_bytes, void* stream) {
-  if ((head_dim != 64 && head_dim != 128) || log2_page(page) < 0) return WQ_EUNSUPPORTED;
-  if (!kv_sizes_ok(batch, tokens, max_q, q_heads, kv_heads, page, max_blocks) || num_pages < 1 || window < 0)
-    return WQ_EINVAL;
-  if (!(sm_scale > 0.0f) || !(sm_scale < INFINITY) || !(softcap >= 0.0f) || !(softcap < INFINITY)) return WQ_EINVAL;
-  if (sm_scale > 0x1p127f) return WQ_EUNSUPPORTED;           // scores go to base 2: sm_scale * log2 e is finite
-  if (softcap > 0.0f && (softcap < 0x1p-10f || softcap > 0x1p10f || !(sm_scale / softcap < 0x1p14f) || !(sm_scale / softcap > 0x1p-100f)))
-    return WQ_EUNSUPPORTED;
-  const int64_t row = (int64_t)q_heads * head_dim;
-  if (q_stride < row || q_stride % 8 || q_stride > (int64_t(1) << 40) ||
-      !wq_numel_ok(num_pages, (int64_t)kv_heads * head_dim * page) || !wq_numel_ok(tokens ? tokens : 1, row) ||
-      !wq_numel_ok(batch ? batch : 1, max_blocks))
-    return WQ_EINVAL;
-  if (!k_codes || !k_scales || !v_codes || !v_scales) return WQ_EINVAL;
-  if (batch > 0 && tokens > 0 && (!q_bf16 || !cu_q || !kv_lens || !block_table || !out || out == q_bf16)) return WQ_EINVAL;
-  if (!wq_aligned(q_bf16) || !wq_aligned(out) || !wq_aligned(k_codes) || !wq_aligned(v_codes) || !wq_aligned(workspace))
-    return WQ_EALIGN;
+  const KvCall c = {q_bf16, q_stride, cu_q, kv_lens, batch, tokens, max_q, q_heads, kv_heads, head_dim, k_codes, k_scales,
+                    v_codes, v_scales, page, num_pages, block_table, max_blocks, sm_scale, softcap, window, out, lse,
+                    workspace, ws_bytes};
+  if (const wq_status bad = kv_check(c)) return bad;
   if (batch == 0 || tokens == 0) return WQ_OK;               // nothing to compute
-  const KvPlan p = kv_plan(batch, tokens, max_q, q_heads, kv_heads, head_dim, page, max_blocks, window);
-  if (p.bytes > 0 && (ws_bytes < p.bytes || !workspace)) return WQ_EINVAL;
-  if (p.pro_items * kv_heads > 0x7FFFFFFF / PTHREADS) return WQ_EINVAL;
-  const KvArgs A = {(const uint16_t*)q_bf16, q_stride, cu_q, kv_lens, batch, tokens, q_heads, kv_heads,
-                    q_heads / kv_heads, (int)(window < 0x7FFFFFFF ? window : 0), k_codes, k_scales, v_codes, v_scales,
-                    log2_page(page), num_pages, block_table, max_blocks, sm_scale, softcap, out, lse};
-  uint8_t* ws = (uint8_t*)workspace;
-  const KvShare dec = {p.solo ? 0 : p.groups, p.rows, p.log_joins, (KvChain*)ws, (float*)(ws + p.dec_sums), (float*)(ws + p.dec_stats)};
-  const KvPart pro = {p.pro_splits, p.pro_slots, PRO_MIN, (int64_t*)(ws + p.pro_used), (KvRec*)(ws + p.pro_rec),
-                      (float*)(ws + p.pro_sums), (float*)(ws + p.pro_stats)};
+  KvLaunch l;
+  if (const wq_status bad = l.lay_out(c)) return bad;
   hipStream_t s = (hipStream_t)stream;
   if (head_dim == 128) {
-    if (softcap > 0.0f) launch_attention<128, true>(A, p, dec, pro, s);
-    else launch_attention<128, false>(A, p, dec, pro, s);
+    if (softcap > 0.0f) launch_attention<128, true>(l.args, l.plan, l.dec, l.pro, s);
+    else launch_attention<128, false>(l.args, l.plan, l.dec, l.pro, s);
   } else {
-    if (softcap > 0.0f) launch_attention<64, true>(A, p, dec, pro, s);
-    else launch_attention<64, false>(A, p, dec, pro, s);
+    if (softcap > 0.0f) launch_attention<64, true>(l.args, l.plan, l.dec, l.pro, s);
+    else launch_attention<64, false>(l.args, l.plan, l.dec, l.pro, s);
   }
   return wq_launch_status();
 }
