@@ -624,8 +624,8 @@ wq_status wq_kv4_append(const void* k, int64_t k_stride, const void* v, int64_t 
 /*
  * wq_kv4_attention -- wq_kv_attention over the 4-bit cache: the same arguments,
  * formulas, limits and clamps (see there), with k_scales and v_scales 16-byte
- * aligned.  Scale codes above 252 count as 252 for values, and are outside the
- * contract for keys: only rows that see such a token are affected.
+ * aligned.  Scale codes above 252 are outside the contract; they affect only
+ * the rows that see such a token.
  */
 wq_status wq_kv4_attention(const void* q_bf16, int64_t q_stride, const int32_t* cu_q, const int32_t* kv_lens,
                            int64_t batch, int64_t tokens, int64_t max_q, int32_t q_heads, int32_t kv_heads,
