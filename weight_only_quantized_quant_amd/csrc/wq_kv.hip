@@ -58,7 +58,7 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_blocks(
     const int64_t held = (c + page - 1) >> log_page, total = (after + page - 1) >> log_page;
     const bool fits = total <= max_blocks && after <= 0x7FFFFFFF;
     const int64_t need = fits ? total - held : 0;
-    int64_t tok = wave_scan(n, lane), pg = wave_scan(need, lane);
+    int64_t tok = wave_scan(n), pg = wave_scan(need);
     __syncthreads();                          // the previous chunk's arrays are no longer read
     if (lane == 63) {
       wave_sum[0][wave] = tok;
@@ -118,8 +118,8 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_blocks(
     positions[row] = -1;
   }
   if (lead) {
-    used = wave_scan(used, lane);
-    const int64_t ref = wave_scan(refused, lane);
+    used = wave_scan(used);
+    const int64_t ref = wave_scan(refused);
     if (lane == 63) {
       used_sum[wave] = used;
       refused_sum[wave] = (int32_t)ref;
@@ -288,7 +288,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
     lanes.load<R, WHICH>(A, base + lane);
     total += (int64_t)units_of(lanes) * lanes.row_tiles;
   }
-  total = lane64(wave_sum(total), 0);
+  total = wave_sum(total);
   const int64_t shares = solo ? 4 * total : total < 4 * part.groups ? total : 4 * part.groups;
   auto share_at = [&](int64_t y) { return y >= shares ? total : solo ? y / 4 : y * total / shares; };
   const int64_t u0 = share_at(x), u1 = share_at(x + 1), g0 = share_at(4 * group), g1 = share_at(4 * group + 4);
@@ -305,7 +305,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv_decode(const KvArgs A, con
     for (int64_t base = 0; base < A.batch; base += 64) {
       if (A.batch > 64) lanes.load<R, WHICH>(A, base + lane);
       const int64_t own = (int64_t)units_of(lanes) * lanes.row_tiles;
-      const int64_t end = before + wave_scan(own, lane);
+      const int64_t end = before + wave_scan(own);
       const unsigned long long at = __ballot(end > u);
       if (at) {
         const int src = __builtin_ctzll(at);

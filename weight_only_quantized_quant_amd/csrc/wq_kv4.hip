@@ -1,5 +1,7 @@
 // Attention over the 4-bit key/value cache for gfx950 (E2M1 elements, one E8M0
 // scale per 32 channels of a token and head).
+#include <utility>
+
 #include "wq_kv_common.h"
 
 namespace {
@@ -54,10 +56,16 @@ __device__ __forceinline__ uint32_t finite_scales(uint32_t w) {
   const uint32_t t = ((w & 0x7F7F7F7Fu) + 0x03030303u) & w & 0x80808080u;     // bytes 253 to 255
   return w & ~((t >> 7) | (t >> 6));
 }
-__device__ __forceinline__ u32x4_t finite_scales(u32x4_t v) {
-#pragma unroll
-  for (int i = 0; i < 4; i++) v[i] = finite_scales(v[i]);
-  return v;
+
+// Lane I of the row of 16 that a lane is in.
+template <int I>
+__device__ __forceinline__ uint32_t row_lane(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x150 + I, 0xF, 0xF, false);
+}
+
+template <typename F, int... I>
+__device__ __forceinline__ void for_each(std::integer_sequence<int, I...>, F f) {
+  (f(std::integral_constant<int, I>{}), ...);
 }
 
 // The pieces of 16 tokens, at j, that every row of a tile sees alike: those in
@@ -75,73 +83,79 @@ struct KvAlike {
 // Decode, as over the 8-bit cache: 16 or 32 rows a row tile, tiles of 64 tokens cut
 // into equal shares, one a wave, K and V from HBM straight into registers.
 //
-// Lane l = 16 g + m.  K tile a (of 4): operand row m is token 4 m + a, result
-// rows 4 g + i are then tokens 16 g + 4 i + a; step h of the products takes
-// channels D / 4 g + 8 h on of each.  V^T: operand row m of tiles 2 b and 2 b + 1 are
+// Lane l = 16 g + m.  K tile a (of 4): operand row m is token
+// 16 (m / 4) + 4 a + m % 4, result rows 4 g + i are then tokens 16 g + 4 a + i;
+// step h of the products takes channels D / 4 g + 8 h on of each.  V^T: operand row m of tiles 2 b and 2 b + 1 are
 // channels 32 b + 2 m and the next.
-template <int D, bool CAP, int WHICH, int NR>
-__global__ __launch_bounds__(KV_THREADS, 2) void k_kv4_decode(const KvArgs A, const KvShare part) {
+template <int D, bool CAP, int WHICH, int NR, int WAVES = 4, int DEEP = (D == 128 && NR == 2 ? 1 : 2)>
+__global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, const KvShare part) {
   constexpr int KH = D / 32, NB = D / 32, DT = D / 16, R = 16 * NR;   // k steps, blocks, channel tiles
-  __shared__ __attribute__((aligned(16))) float so[4][R][D + 4];
-  __shared__ float sm[4][R], sl[4][R];
+  __shared__ __attribute__((aligned(16))) float so[WAVES][R][D + 4];
+  __shared__ float sm[WAVES][R], sl[WAVES][R];
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int group = (int)(blockIdx.x / (unsigned)A.kv_heads), kvh = (int)(blockIdx.x % (unsigned)A.kv_heads);
-  const int x = 4 * group + wave;
+  const int x = WAVES * group + wave;
   const KvChain none = {};
 
   // all the work, in tiles or in row tiles, and this wave's share [u0, u1) of it
   const bool solo = part.groups == 0;
   auto units_of = [&](const KvRequest& r) { return solo || r.tiles <= 0 ? 1 : r.tiles; };
   KvRequest lanes;
-  int64_t total = 0;
+  int64_t total = 0, all_tiles = 0;
   for (int64_t base = 0; base < A.batch; base += 64) {
     lanes.load<R, WHICH>(A, base + lane);
     total += (int64_t)units_of(lanes) * lanes.row_tiles;
+    all_tiles += lanes.row_tiles;
   }
-  total = lane64(wave_sum(total), 0);
-  const int64_t shares = solo ? 4 * total : total < 4 * part.groups ? total : 4 * part.groups;
-  auto share_at = [&](int64_t y) { return y >= shares ? total : solo ? y / 4 : y * total / shares; };
-  const int64_t u0 = share_at(x), u1 = share_at(x + 1), g0 = share_at(4 * group), g1 = share_at(4 * group + 4);
+  total = wave_sum(total);
+  if (part.by_tile && blockIdx.x == 0)        // entries behind the last row tile's
+    for (int64_t i = wave_sum(all_tiles) + tid; i < part.chains; i += 64 * WAVES) part.chain[i] = none;
+  const bool each = !solo && !part.by_tile;   // an entry for each wave
+  const int64_t shares = solo ? WAVES * total : total < WAVES * part.groups ? total : WAVES * part.groups;
+  auto share_at = [&](int64_t y) { return y >= shares ? total : solo ? y / WAVES : mul_div(y, total, shares); };
+  const int64_t u0 = share_at(x), u1 = share_at(x + 1), g0 = share_at(WAVES * group), g1 = share_at(WAVES * (group + 1));
   if (g0 >= g1) {                             // an idle workgroup
-    if (!solo && kvh == 0 && lane == 0) part.chain[x] = none;
+    if (each && kvh == 0 && lane == 0) part.chain[x] = none;
     return;
   }
-  // the request that holds unit u, and its first unit
+  // the request that holds unit u
   KvRequest q = {};
   int request = 0;
-  int64_t begin = 0;
+  int64_t begin = 0, tile0 = 0;               // its first unit, and row tile
   auto find = [&](int64_t u) {
-    int64_t before = 0;
+    int64_t before = 0, tiles_before = 0;
     for (int64_t base = 0; base < A.batch; base += 64) {
       if (A.batch > 64) lanes.load<R, WHICH>(A, base + lane);
       const int64_t own = (int64_t)units_of(lanes) * lanes.row_tiles;
-      const int64_t end = before + wave_scan(own, lane);
+      const int64_t end = before + wave_scan(own), tiles_end = tiles_before + wave_scan(lanes.row_tiles);
       const unsigned long long at = __ballot(end > u);
       if (at) {
         const int src = __builtin_ctzll(at);
         q = lanes.from(src);
         request = (int)base + src;
         begin = lane64(end - own, src);
+        tile0 = lane64(tiles_end - lanes.row_tiles, src);
         return;
       }
       before = lane64(end, 63);
+      tiles_before = lane64(tiles_end, 63);
     }
   };
   find(g0);
   auto units = [&]() { return units_of(q); };
-  int rt = (int)((g0 - begin) / units());     // row tiles in order of their units, the last rows first
+  int rt = (int)mul_div(g0 - begin, 1, units());     // row tiles in order of their units, the last rows first
   const bool joined = g1 <= begin + (int64_t)(rt + 1) * units();   // always so if solo
   if (!joined) {
     if (u0 >= u1) {
-      if (kvh == 0 && lane == 0) part.chain[x] = none;
+      if (each && kvh == 0 && lane == 0) part.chain[x] = none;
       return;
     }
     find(u0);
-    rt = (int)((u0 - begin) / units());
+    rt = (int)mul_div(u0 - begin, 1, units());
   }
   if (q.row_tiles == 0) {                     // lengths that changed under the kernel
-    if (!solo && kvh == 0 && lane == 0) part.chain[x] = none;
+    if (each && kvh == 0 && lane == 0) part.chain[x] = none;
     return;
   }
 
@@ -158,7 +172,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv4_decode(const KvArgs A, co
   for (int64_t u = u0;;) {
     const int64_t row_begin = begin + (int64_t)rt * units(), row_end = row_begin + units();
     const int64_t stop = u1 < row_end ? u1 : row_end;
-    const int step = joined ? 4 : 1;          // the waves of a joined workgroup take its tiles in turn
+    const int step = joined ? WAVES : 1;          // the waves of a joined workgroup take its tiles in turn
     const int r0 = (q.row_tiles - 1 - rt) * R;
     const int n_rows = q.n * A.group - r0 < R ? q.n * A.group - r0 : R;
     const KvRows rows(A, r0, q.n, q.len);
@@ -177,50 +191,59 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv4_decode(const KvArgs A, co
     t += joined ? wave : 0;
 
     const int32_t* tab = A.table + (int64_t)request * A.max_blocks;
-    uint32_t kr[4][KH];
-    u32x4_t vr[NB], vsc[NB];
-    uint32_t ksc;                             // scales of this lane's four keys
-    bool vok;
-    int idk, idv;                             // page ids of the next tile to load
-    auto load_ids = [&](int t) {
-      const int ck = (t * TILE + 4 * m) >> A.log_page, cv = (t * TILE + 16 * g) >> A.log_page;
-      idk = tab[ck < last_col ? ck : last_col];
-      idv = tab[cv < last_col ? cv : last_col];
+    struct Buffer {                           // a tile on its way
+      uint32_t kr[4][KH];
+      u32x4_t vr[NB];
+      u32x4_t ksc;                            // scales of 16 keys, this lane's among them
+      uint32_t vsc;                           // scales of four of its 16 values, in block m / 4
+      bool vok;
+    } buf[DEEP];
+    struct Ids {
+      int k, v;
+    } next;                                   // page ids of the next tile to load
+    auto ids_of = [&](int t) {
+      const int ck = (t * TILE + 16 * (m >> 2)) >> A.log_page, cv = (t * TILE + 16 * g) >> A.log_page;
+      return Ids{tab[ck < last_col ? ck : last_col], tab[cv < last_col ? cv : last_col]};
     };
-    auto load_k = [&](int t) {
+    auto load_k = [&](Buffer& b, int t, int idk) {
       const uint64_t id = idk >= 0 && idk < A.num_pages ? idk : 0;
-      const int off = (t * TILE + 4 * m) & in_page;
-      ksc = *reinterpret_cast<const uint32_t*>(ksb + (id * page_scales + (((D == 128 ? g : g >> 1) << A.log_page) + off)));
-      const uint8_t* p = kbase + (id * page_bytes + off * (D / 2) + 4 * KH * g);
+      const int off = (t * TILE + 16 * (m >> 2)) & in_page;
+      b.ksc = ld16(ksb + (id * page_scales + (((D == 128 ? g : g >> 1) << A.log_page) + off)));
+      const uint8_t* p = kbase + (id * page_bytes + (off + (m & 3)) * (D / 2) + 4 * KH * g);
 #pragma unroll
       for (int a = 0; a < 4; a++) {
         if constexpr (D == 128) {
-          const u32x4_t w = ld16(p + a * (D / 2));
+          const u32x4_t w = ld16(p + 4 * a * (D / 2));
 #pragma unroll
-          for (int h = 0; h < KH; h++) kr[a][h] = w[h];
+          for (int h = 0; h < KH; h++) b.kr[a][h] = w[h];
         } else {
-          const u32x2_t w = *reinterpret_cast<const u32x2_t*>(p + a * (D / 2));
+          const u32x2_t w = *reinterpret_cast<const u32x2_t*>(p + 4 * a * (D / 2));
 #pragma unroll
-          for (int h = 0; h < KH; h++) kr[a][h] = w[h];
+          for (int h = 0; h < KH; h++) b.kr[a][h] = w[h];
         }
       }
     };
-    auto load_v = [&](int t) {
-      vok = idv >= 0 && idv < A.num_pages;
-      const uint64_t id = vok ? idv : 0;
+    auto load_v = [&](Buffer& b, int t, int idv) {
+      b.vok = idv >= 0 && idv < A.num_pages;
+      const uint64_t id = b.vok ? idv : 0;
       const int off = (t * TILE + 16 * g) & in_page;
-      const uint8_t *p = vbase + (id * page_bytes + ((m << A.log_page) + off)), *c = vsb + (id * page_scales + off);
+      const uint8_t* p = vbase + (id * page_bytes + ((m << A.log_page) + off));
+      b.vsc = *reinterpret_cast<const uint32_t*>(vsb + (id * page_scales + ((((m >> 2) & (NB - 1)) << A.log_page) + off + 4 * (m & 3))));
 #pragma unroll
-      for (int b = 0; b < NB; b++) {
-        vsc[b] = ld16(c + (b << A.log_page));
-        vr[b] = ld16(p + ((16 * b) << A.log_page));
-      }
+      for (int i = 0; i < NB; i++) b.vr[i] = ld16(p + ((16 * i) << A.log_page));
     };
     if (t < t1) {
-      load_ids(t);
-      load_k(t);
-      load_v(t);
-      if (t + step < t1) load_ids(t + step);
+      Ids first[DEEP];
+#pragma unroll
+      for (int x = 0; x < DEEP; x++)
+        if (x == 0 || t + x * step < t1) first[x] = ids_of(t + x * step);
+#pragma unroll
+      for (int x = 0; x < DEEP; x++)
+        if (x == 0 || t + x * step < t1) {
+          load_k(buf[x], t + x * step, first[x].k);
+          load_v(buf[x], t + x * step, first[x].v);
+        }
+      if (t + DEEP * step < t1) next = ids_of(t + DEEP * step);
     }
 
     // query fragments: columns m of q^T, channels D / 4 g + 8 h on in step h; row m's limits
@@ -250,31 +273,33 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv4_decode(const KvArgs A, co
       mx[c] = -INFINITY;
       l[c] = 0.0f;
     }
-    for (; t < t1; t += step) {
+    auto turn = [&](Buffer& b, int t) {
       const int j0 = t * TILE + 16 * g;       // this lane's 16 tokens in scores and V^T
-      const bool more = t + step < t1;
+      const bool more = t + DEEP * step < t1;
       f32x4_t s[NR][4];
 #pragma unroll
       for (int a = 0; a < 4; a++) {
-        const float ks = scale_of(ksc, a);
+        // byte m % 4, turned to where the conversion reads a scale
+        const float ks = __uint_as_float(__builtin_amdgcn_alignbit(b.ksc[a], b.ksc[a], 9 + 8 * (m & 3)));
 #pragma unroll
         for (int c = 0; c < NR; c++) s[c][a] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
         for (int h = 0; h < KH; h++) {
-          const bf16x8_t k = e2m1_bf16x8(kr[a][h], ks);
+          const bf16x8_t k = e2m1_bf16x8(b.kr[a][h], ks);
 #pragma unroll
           for (int c = 0; c < NR; c++) s[c][a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, qf[c][h], s[c][a], 0, 0, 0);
         }
       }
-      if (more) load_k(t + step);
-      const bool edge = t * TILE + TILE - 1 > rows.pos0 || t * TILE < lo_max || __any(!vok);
-      if (edge) {                             // scales of tokens that not every row sees stay finite
-#pragma unroll
-        for (int b = 0; b < NB; b++) vsc[b] = finite_scales(vsc[b]);
-      }
+      if (more) load_k(b, t + DEEP * step, next.k);
+      const bool edge = t * TILE + TILE - 1 > rows.pos0 || t * TILE < lo_max || __any(!b.vok);
+      if (edge) b.vsc = finite_scales(b.vsc); // of tokens that not every row sees
       bf16x8_t p0[NR], p1[NR];
 #pragma unroll
       for (int c = 0; c < NR; c++) {
+        if (c > 0 && 16 * c >= n_rows) {      // a column without rows
+          p0[c] = p1[c] = __builtin_bit_cast(bf16x8_t, (u32x4_t{0, 0, 0, 0}));
+          continue;
+        }
         if constexpr (CAP) {
           float v[16];
 #pragma unroll
@@ -284,11 +309,11 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv4_decode(const KvArgs A, co
           for (int i = 0; i < 16; i++) s[c][i >> 2][i & 3] = v[i];
         }
         if (edge) {                           // tokens outside the row's limits
-          const int z = vok ? pos[c] - j0 : -1, b = rlo[c] - j0;
+          const int z = b.vok ? pos[c] - j0 : -1, low = rlo[c] - j0;
 #pragma unroll
           for (int a = 0; a < 4; a++)
 #pragma unroll
-            for (int i = 0; i < 4; i++) s[c][a][i] = 4 * i + a <= z && 4 * i + a >= b ? s[c][a][i] : -INFINITY;
+            for (int i = 0; i < 4; i++) s[c][a][i] = 4 * a + i <= z && 4 * a + i >= low ? s[c][a][i] : -INFINITY;
         }
         float mt = -INFINITY;
 #pragma unroll
@@ -308,37 +333,46 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv4_decode(const KvArgs A, co
         const float off = mx[c] == -INFINITY ? 0.0f : -mx[c];
         uint32_t pw[8];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
+        for (int a = 0; a < 4; a++) {
           float p[4];
 #pragma unroll
-          for (int a = 0; a < 4; a++) {
-            p[a] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[c][a][i], sc.mul, off));
-            l[c] += p[a];
+          for (int i = 0; i < 4; i++) {
+            p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[c][a][i], sc.mul, off));
+            l[c] += p[i];
           }
           // bf16 for the matrix cores: half a step of 2^-8 per probability, the sum l keeps fp32
-          pw[2 * i] = pack_bf16x2(p[0], p[1]);
-          pw[2 * i + 1] = pack_bf16x2(p[2], p[3]);
+          pw[2 * a] = pack_bf16x2(p[0], p[1]);
+          pw[2 * a + 1] = pack_bf16x2(p[2], p[3]);
         }
         p0[c] = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[0], pw[1], pw[2], pw[3]}));
         p1[c] = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[4], pw[5], pw[6], pw[7]}));
       }
-#pragma unroll
-      for (int b = 0; b < NB; b++) {
-        bf16x8_t v[2][2];                     // channels 32 b + 2 m and the next, tokens 0-7 and 8-15
-        value_pairs(vr[b][0], vr[b][1], vsc[b][0], vsc[b][1], v[0][0], v[1][0]);
-        value_pairs(vr[b][2], vr[b][3], vsc[b][2], vsc[b][3], v[0][1], v[1][1]);
+      const uint32_t vsc = b.vsc;
+      for_each(std::make_integer_sequence<int, NB>{}, [&](auto block) {
+        constexpr int B = decltype(block)::value;
+        bf16x8_t v[2][2];                     // channels 32 B + 2 m and the next, tokens 0-7 and 8-15
+        value_pairs(b.vr[B][0], b.vr[B][1], row_lane<4 * B>(vsc), row_lane<4 * B + 1>(vsc), v[0][0], v[1][0]);
+        value_pairs(b.vr[B][2], b.vr[B][3], row_lane<4 * B + 2>(vsc), row_lane<4 * B + 3>(vsc), v[0][1], v[1][1]);
 #pragma unroll
         for (int e = 0; e < 2; e++)
 #pragma unroll
           for (int c = 0; c < NR; c++) {
-            o[c][2 * b + e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[e][0], p0[c], o[c][2 * b + e], 0, 0, 0);
-            o[c][2 * b + e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[e][1], p1[c], o[c][2 * b + e], 0, 0, 0);
+            o[c][2 * B + e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[e][0], p0[c], o[c][2 * B + e], 0, 0, 0);
+            o[c][2 * B + e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[e][1], p1[c], o[c][2 * B + e], 0, 0, 0);
           }
-      }
+      });
       if (more) {
-        load_v(t + step);
-        if (t + 2 * step < t1) load_ids(t + 2 * step);
+        load_v(b, t + DEEP * step, next.v);
+        if (t + (DEEP + 1) * step < t1) next = ids_of(t + (DEEP + 1) * step);
       }
+    };
+    while (t < t1) {
+#pragma unroll
+      for (int x = 0; x < DEEP; x++)
+        if (x == 0 || t < t1) {
+          turn(buf[x], t);
+          t += step;
+        }
     }
 #pragma unroll
     for (int c = 0; c < NR; c++) {
@@ -349,12 +383,17 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv4_decode(const KvArgs A, co
     // this wave, or the workgroup, has units [from, to) of the row tile's
     const int64_t from = joined ? g0 : u, to = joined ? g1 : stop;
     const bool whole = from == row_begin && to == row_end;
-    const int slot = 2 * (joined ? 4 * group : x) + (from == row_begin ? 0 : 1);
-    if (from == row_begin && !whole && (!joined || wave == 0)) {
-      // the last wave: the one whose share holds unit row_end - 1
-      const int64_t last = (row_end * shares - 1) / total;
-      chain = KvChain{n_rows, q.q0 + rows.first, rows.head0, joined ? 4 * group : x, (int)last, joined,
-                      share_at((last | 3) + 1) <= row_end};
+    const int slot = 2 * (joined ? WAVES * group : x) + (from == row_begin ? 0 : 1);
+    if (from == row_begin && !solo && (!joined || wave == 0)) {
+      KvChain c = none;
+      if (!whole) {
+        // the last wave: the one whose share holds unit row_end - 1
+        const int64_t last = mul_div(row_end, shares, total), end = last * total < row_end * shares ? last : last - 1;
+        c = KvChain{n_rows, q.q0 + rows.first, rows.head0, joined ? WAVES * group : x, (int)end, joined,
+                    share_at((end | (WAVES - 1)) + 1) <= row_end};
+        chain = c;
+      }
+      if (part.by_tile && kvh == 0 && lane == 0 && tile0 + rt < part.chains) part.chain[tile0 + rt] = c;
     }
     auto put = [&](int row, int ch, const f32x4_t& v, float top, float sum) {      // 4 channels of a row
       if (!whole) {
@@ -389,6 +428,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv4_decode(const KvArgs A, co
       if (u >= u1) break;
       if (++rt == q.row_tiles) {              // on to the next request that has rows
         begin = row_end;
+        tile0 += q.row_tiles;
         rt = 0;
         do {
           request++;
@@ -411,14 +451,14 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv4_decode(const KvArgs A, co
         for (int e = 0; e < 2; e++) *reinterpret_cast<f32x4_t*>(&so[wave][16 * c + m][32 * b + 8 * g + 4 * e]) = four(c, b, e);
     }
     __syncthreads();
-    for (int i = tid; i < n_rows * (D / 4); i += KV_THREADS) {
+    for (int i = tid; i < n_rows * (D / 4); i += 64 * WAVES) {
       const int row = i / (D / 4), ch = i % (D / 4) * 4;
       float top = sm[0][row], sum = 0.0f;
 #pragma unroll
-      for (int w = 1; w < 4; w++) top = __builtin_fmaxf(top, sm[w][row]);
+      for (int w = 1; w < WAVES; w++) top = __builtin_fmaxf(top, sm[w][row]);
       f32x4_t acc = {0, 0, 0, 0};
 #pragma unroll
-      for (int w = 0; w < 4; w++) {
+      for (int w = 0; w < WAVES; w++) {
         const float f = sm[w][row] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(sm[w][row] - top);
         sum = __builtin_fmaf(f, sl[w][row], sum);
         const f32x4_t v = *reinterpret_cast<const f32x4_t*>(&so[w][row][ch]);
@@ -429,7 +469,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void k_kv4_decode(const KvArgs A, co
     }
     break;
   }
-  if (!solo && kvh == 0 && lane == 0) part.chain[x] = chain;
+  if (each && kvh == 0 && lane == 0) part.chain[x] = chain;
 }
 
 // Prompts and chunks, as over the 8-bit cache: 128 rows per workgroup, 32 per
@@ -785,6 +825,9 @@ __global__ __launch_bounds__(PTHREADS, D == 64 ? 3 : 2) void k_kv4_prompt(const 
   if (A.lse && h == 0) A.lse[orow] = l == 0.0f ? -INFINITY : (mx + __builtin_log2f(l)) * LN2;
 }
 
+// Workgroups of 8 waves for row tiles of their own, where each has a CU.
+constexpr unsigned SOLO_WIDE = 256;
+
 template <int D, bool CAP>
 void launch_attention(const KvArgs& A, const KvPlan& p, const KvShare& dec, const KvPart& pro, hipStream_t s) {
   const unsigned h = (unsigned)A.kv_heads, groups = (unsigned)p.groups * h;
@@ -795,11 +838,13 @@ void launch_attention(const KvArgs& A, const KvPlan& p, const KvShare& dec, cons
     k_kv4_decode<D, CAP, REQ_SHORT, 2><<<groups, KV_THREADS, 0, s>>>(A, dec);
   } else if (p.nr == 2) {
     k_kv4_decode<D, CAP, REQ_ALL, 2><<<groups, KV_THREADS, 0, s>>>(A, dec);
+  } else if (p.solo && groups <= SOLO_WIDE) {
+    k_kv4_decode<D, CAP, REQ_ALL, 1, 8><<<groups, 512, 0, s>>>(A, dec);
   } else {
     k_kv4_decode<D, CAP, REQ_ALL, 1><<<groups, KV_THREADS, 0, s>>>(A, dec);
   }
   if (p.solo) return;
-  const unsigned joins = (4 * groups << p.log_joins) + (unsigned)(p.pro_slots * (PROWS / 16)) * h;
+  const unsigned joins = ((unsigned)dec.chains * h << p.log_joins) + (unsigned)(p.pro_slots * (PROWS / 16)) * h;
   if (p.nr == 2) k_kv_join<D, 2><<<joins, KV_THREADS, 0, s>>>(A, dec, pro);
   else k_kv_join<D, 1><<<joins, KV_THREADS, 0, s>>>(A, dec, pro);
 }
@@ -830,6 +875,10 @@ wq_status wq_kv4_attention(const void* q_bf16, int64_t q_stride, const int32_t* 
   if (batch == 0 || tokens == 0) return WQ_OK;               // nothing to compute
   KvLaunch l;
   if (const wq_status bad = l.lay_out(c)) return bad;
+  if (l.plan.chains < l.dec.chains) {         // row tiles are fewer than waves
+    l.dec.chains = l.plan.chains;
+    l.dec.by_tile = !l.plan.solo;
+  }
   hipStream_t s = (hipStream_t)stream;
   if (head_dim == 128) {
     if (softcap > 0.0f) launch_attention<128, true>(l.args, l.plan, l.dec, l.pro, s);

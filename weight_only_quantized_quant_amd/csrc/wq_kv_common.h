@@ -16,14 +16,23 @@ namespace {
 
 constexpr int KV_THREADS = 256;
 
-// Sum of v over the lower lanes of the wave and this one.
-__device__ __forceinline__ int64_t wave_scan(int64_t v, int lane) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int64_t u = __shfl_up(v, o, 64);
-    if (lane >= o) v += u;
-  }
-  return v;
+// Sum of v over the lower lanes of the wave and this one: within rows of 16 lanes
+// by shifts of 1, 2, 4 and 8, then the last lane of a row into the next and of
+// the first half into the second (DPP moves; exchanges through LDS take ten times
+// as long).  Every lane of the wave has to be active.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int64_t scan_step(int64_t v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(v >> 32), CTRL, ROWS, 0xF, false);
+  return v + (int64_t)((uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ int64_t wave_scan(int64_t v) {
+  v = scan_step<0x111, 0xF>(v);
+  v = scan_step<0x112, 0xF>(v);
+  v = scan_step<0x114, 0xF>(v);
+  v = scan_step<0x118, 0xF>(v);
+  v = scan_step<0x142, 0xA>(v);
+  return scan_step<0x143, 0xC>(v);
 }
 
 // Rows of one key/value head are numbered r = query * group + head in group:
@@ -90,6 +99,8 @@ struct KvPart {
 // ends behind it, 2 x + 1 for one that began before.  A workgroup inside one
 // row tile joins its waves first and uses the slots of its first wave alone.
 // chain[x] describes the row tile of slot 2 x; every wave writes its own entry.
+// With `by_tile` there is an entry for each row tile instead, which the wave
+// that begins it writes: fewer for k_kv_join to look at where row tiles are few.
 struct KvChain {
   int32_t rows, query0, head0;                // 0 rows: none
   int32_t first, last;                        // waves that share the row tile
@@ -97,7 +108,9 @@ struct KvChain {
 };
 struct KvShare {
   int groups, rows;                           // workgroups per head (0: one a row tile), rows of a slot
+  int chains;                                 // entries of chain: 4 a workgroup, or fewer
   int log_joins;                              // log2 of the workgroups of k_kv_join for a row tile
+  bool by_tile;
   KvChain* chain;
   float* sums;
   float* stats;
@@ -115,14 +128,16 @@ struct KvItem {
   int64_t slot;                               // partial slot, where splits > 1
 };
 
-__device__ __forceinline__ int64_t wave_sum(int64_t v) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
 __device__ __forceinline__ int lane32(int v, int src) { return __builtin_amdgcn_readlane(v, src); }
 __device__ __forceinline__ int64_t lane64(int64_t v, int src) {
   return (int64_t)(((uint64_t)(uint32_t)lane32((int)(v >> 32), src) << 32) | (uint32_t)lane32((int)v, src));
+}
+__device__ __forceinline__ int64_t wave_sum(int64_t v) { return lane64(wave_scan(v), 63); }
+// a * b / c for a, b >= 0 and c > 0; a division of 64 bits takes a microsecond for several.
+__device__ __forceinline__ int64_t mul_div(int64_t a, int64_t b, int64_t c) {
+  const uint64_t n = (uint64_t)a * (uint64_t)b;
+  if ((n | (uint64_t)c) >> 32 == 0) return (uint32_t)n / (uint32_t)c;
+  return (int64_t)(n / (uint64_t)c);
 }
 
 // The lowest token that position `pos` sees (window 0: the first).
@@ -171,7 +186,7 @@ __device__ __forceinline__ bool kv_find(const KvArgs& A, const KvPart& part, int
     q.load<R, WHICH>(A, base + lane);
     total += (int64_t)q.tiles * q.row_tiles;
   }
-  total = lane64(wave_sum(total), 0);
+  total = wave_sum(total);
   int64_t share = (total + part.splits - 1) / part.splits;
   share = share < part.min_tiles ? part.min_tiles : share;
   const int per = share > 0x7FFFFFFF ? 0x7FFFFFFF : (int)share;
@@ -181,7 +196,7 @@ __device__ __forceinline__ bool kv_find(const KvArgs& A, const KvPart& part, int
     if (A.batch > 64) q.load<R, WHICH>(A, base + lane);
     const int rounded = (int)((2 * (int64_t)q.tiles + per) / (2 * (int64_t)per)), splits = rounded > 1 ? rounded : 1;
     const int64_t own = (int64_t)q.row_tiles * splits, part_own = splits > 1 ? own : 0;
-    const int64_t end = items + wave_scan(own, lane), part_end = slots + wave_scan(part_own, lane);
+    const int64_t end = items + wave_scan(own), part_end = slots + wave_scan(part_own);
     const unsigned long long at = __ballot(end > item);
     if (at && !found) {
       const int src = __builtin_ctzll(at);
@@ -356,11 +371,12 @@ template <int D, int NR>
 __global__ __launch_bounds__(KV_THREADS) void k_kv_join(const KvArgs A, const KvShare dec, const KvPart pro) {
   const int kvh = (int)(blockIdx.x % (unsigned)A.kv_heads);
   int64_t x = blockIdx.x / (unsigned)A.kv_heads;
-  const int64_t decode = 4 * (int64_t)dec.groups << dec.log_joins;
+  const int64_t decode = (int64_t)dec.chains << dec.log_joins;
   if (x < decode) {
     const KvChain c = dec.chain[x >> dec.log_joins];
     const int some = 16 * NR >> dec.log_joins, row0 = (int)(x & ((1 << dec.log_joins) - 1)) * some;
-    if (c.rows == 0) return;
+    // no row tile, or one that lengths changing under the kernel left unwritten
+    if (c.rows <= 0 || c.rows > 16 * NR || c.first < 0 || c.last < c.first || c.last >= 4 * dec.groups) return;
     // parts: the first workgroup's, one for each between, the last workgroup's
     const int ga = c.first / 4, gz = c.last / 4;
     const int a = c.first_joined ? 1 : (gz > ga ? 4 * ga + 3 : c.last) - c.first + 1;
@@ -402,6 +418,7 @@ struct KvPlan {
   bool prompt, solo;                          // solo: decode only, a workgroup a row tile, nothing to join
   int nr;                                     // 16-row columns of a decode tile
   int groups, rows, log_joins;                // decode workgroups per head, rows of its slots, joins a row tile
+  int chains;                                 // row tiles of the decode kernel, at most
   int64_t pro_splits, pro_items, pro_slots;
   size_t dec_sums, dec_stats, pro_used, pro_rec, pro_sums, pro_stats, bytes;
 };
@@ -422,6 +439,8 @@ KvPlan kv_plan(int64_t batch, int64_t tokens, int64_t max_q, int q_heads, int kv
   p.solo = !p.prompt && (seen < tiles ? seen : tiles) <= (work < DEC_GROUPS / 4 ? SOLO_TILES : SOLO_TILES_MANY) &&
            work <= 2 * DEC_GROUPS;
   p.groups = (int)(p.solo ? row_tiles : wgs > 1 ? wgs : 1);
+  const int64_t chains = p.prompt ? reqs * (SHORT_ROWS / p.rows) : row_tiles;
+  p.chains = (int)(chains < 4 * p.groups ? chains : 4 * p.groups);
   if (p.solo) return p;
   p.pro_splits = (PRO_ITEMS + kv_heads - 1) / kv_heads;
   const int64_t pro_rows = p.prompt ? tokens * group / PROWS + reqs : 0;
@@ -511,7 +530,7 @@ struct KvLaunch {
                   c.q_heads / c.kv_heads, (int)(c.window < 0x7FFFFFFF ? c.window : 0), c.k_codes, c.k_scales, c.v_codes,
                   c.v_scales, log2_page(c.page), c.num_pages, c.table, c.max_blocks, c.sm_scale, c.softcap, c.out, c.lse};
     uint8_t* ws = (uint8_t*)c.workspace;
-    dec = KvShare{p.solo ? 0 : p.groups, p.rows, p.log_joins, (KvChain*)ws, (float*)(ws + p.dec_sums),
+    dec = KvShare{p.solo ? 0 : p.groups, p.rows, 4 * p.groups, p.log_joins, false, (KvChain*)ws, (float*)(ws + p.dec_sums),
                   (float*)(ws + p.dec_stats)};
     pro = KvPart{p.pro_splits, p.pro_slots, PRO_MIN, (int64_t*)(ws + p.pro_used), (KvRec*)(ws + p.pro_rec),
                  (float*)(ws + p.pro_sums), (float*)(ws + p.pro_stats)};
