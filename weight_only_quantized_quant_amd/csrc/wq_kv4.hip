@@ -102,18 +102,22 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, co
   const bool solo = part.groups == 0;
   auto units_of = [&](const KvRequest& r) { return solo || r.tiles <= 0 ? 1 : r.tiles; };
   KvRequest lanes;
-  int64_t total = 0, all_tiles = 0;
-  for (int64_t base = 0; base < A.batch; base += 64) {
+  int64_t total = 0, tiles = 0, end = 0, tiles_end = 0;     // of all requests; up to and with the lane's
+  auto scan = [&](int64_t base, int64_t& before, int64_t& tiles_before) {      // 64 requests from `base` on
     lanes.load<R, WHICH>(A, base + lane);
-    total += (int64_t)units_of(lanes) * lanes.row_tiles;
-    all_tiles += lanes.row_tiles;
-  }
-  total = wave_sum(total);
+    end = before + wave_scan((int64_t)units_of(lanes) * lanes.row_tiles);
+    tiles_end = tiles_before + wave_scan(lanes.row_tiles);
+    before = lane64(end, 63);
+    tiles_before = lane64(tiles_end, 63);
+  };
+  for (int64_t base = 0; base < A.batch; base += 64) scan(base, total, tiles);
   if (part.by_tile && blockIdx.x == 0)        // entries behind the last row tile's
-    for (int64_t i = wave_sum(all_tiles) + tid; i < part.chains; i += 64 * WAVES) part.chain[i] = none;
+    for (int64_t i = tiles + tid; i < part.chains; i += 64 * WAVES) part.chain[i] = none;
   const bool each = !solo && !part.by_tile;   // an entry for each wave
+  // the first `extra` shares have one unit more
   const int64_t shares = solo ? WAVES * total : total < WAVES * part.groups ? total : WAVES * part.groups;
-  auto share_at = [&](int64_t y) { return y >= shares ? total : solo ? y / WAVES : mul_div(y, total, shares); };
+  const int64_t least = solo || total == 0 ? 0 : quotient(total, shares), extra = total - least * shares;
+  auto share_at = [&](int64_t y) { return y >= shares ? total : solo ? y / WAVES : y * least + (y < extra ? y : extra); };
   const int64_t u0 = share_at(x), u1 = share_at(x + 1), g0 = share_at(WAVES * group), g1 = share_at(WAVES * (group + 1));
   if (g0 >= g1) {                             // an idle workgroup
     if (each && kvh == 0 && lane == 0) part.chain[x] = none;
@@ -126,25 +130,21 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, co
   auto find = [&](int64_t u) {
     int64_t before = 0, tiles_before = 0;
     for (int64_t base = 0; base < A.batch; base += 64) {
-      if (A.batch > 64) lanes.load<R, WHICH>(A, base + lane);
-      const int64_t own = (int64_t)units_of(lanes) * lanes.row_tiles;
-      const int64_t end = before + wave_scan(own), tiles_end = tiles_before + wave_scan(lanes.row_tiles);
+      if (A.batch > 64) scan(base, before, tiles_before);
       const unsigned long long at = __ballot(end > u);
       if (at) {
         const int src = __builtin_ctzll(at);
         q = lanes.from(src);
         request = (int)base + src;
-        begin = lane64(end - own, src);
-        tile0 = lane64(tiles_end - lanes.row_tiles, src);
+        tile0 = lane64(tiles_end, src) - q.row_tiles;
+        begin = lane64(end, src) - (int64_t)units_of(q) * q.row_tiles;
         return;
       }
-      before = lane64(end, 63);
-      tiles_before = lane64(tiles_end, 63);
     }
   };
   find(g0);
   auto units = [&]() { return units_of(q); };
-  int rt = (int)mul_div(g0 - begin, 1, units());     // row tiles in order of their units, the last rows first
+  int rt = (int)quotient(g0 - begin, units());     // row tiles in order of their units, the last rows first
   const bool joined = g1 <= begin + (int64_t)(rt + 1) * units();   // always so if solo
   if (!joined) {
     if (u0 >= u1) {
@@ -152,7 +152,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, co
       return;
     }
     find(u0);
-    rt = (int)mul_div(u0 - begin, 1, units());
+    rt = (int)quotient(u0 - begin, units());
   }
   if (q.row_tiles == 0) {                     // lengths that changed under the kernel
     if (each && kvh == 0 && lane == 0) part.chain[x] = none;
@@ -388,9 +388,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, co
       KvChain c = none;
       if (!whole) {
         // the last wave: the one whose share holds unit row_end - 1
-        const int64_t last = mul_div(row_end, shares, total), end = last * total < row_end * shares ? last : last - 1;
-        c = KvChain{n_rows, q.q0 + rows.first, rows.head0, joined ? WAVES * group : x, (int)end, joined,
-                    share_at((end | (WAVES - 1)) + 1) <= row_end};
+        const int64_t wide = extra * (least + 1), unit = row_end - 1;
+        const int64_t last = unit < wide ? quotient(unit, least + 1) : extra + quotient(unit - wide, least);
+        c = KvChain{n_rows, q.q0 + rows.first, rows.head0, joined ? WAVES * group : x, (int)last, joined,
+                    share_at((last | (WAVES - 1)) + 1) <= row_end};
         chain = c;
       }
       if (part.by_tile && kvh == 0 && lane == 0 && tile0 + rt < part.chains) part.chain[tile0 + rt] = c;

@@ -74,6 +74,11 @@ struct KvArgs {
   float sm_scale, softcap;
   uint16_t* out;
   float* lse;
+  // x / group = x * group_mul >> 31 + group_shift for x below 2^31: group_mul =
+  // floor(2^(31 + s) / group) + 1 with 2^s >= group is above the quotient by at most
+  // 2^s / group 2^-(31 + s), which x below 2^31 does not take past the next whole number
+  uint32_t group_mul, group_shift;
+  __device__ __forceinline__ uint32_t by_group(uint32_t x) const { return (uint32_t)((uint64_t)x * group_mul >> 31 >> group_shift); }
 };
 
 // Partial results of the prompt kernel's split rows: `used[0]` slots are in
@@ -133,11 +138,10 @@ __device__ __forceinline__ int64_t lane64(int64_t v, int src) {
   return (int64_t)(((uint64_t)(uint32_t)lane32((int)(v >> 32), src) << 32) | (uint32_t)lane32((int)v, src));
 }
 __device__ __forceinline__ int64_t wave_sum(int64_t v) { return lane64(wave_scan(v), 63); }
-// a * b / c for a, b >= 0 and c > 0; a division of 64 bits takes a microsecond for several.
-__device__ __forceinline__ int64_t mul_div(int64_t a, int64_t b, int64_t c) {
-  const uint64_t n = (uint64_t)a * (uint64_t)b;
-  if ((n | (uint64_t)c) >> 32 == 0) return (uint32_t)n / (uint32_t)c;
-  return (int64_t)(n / (uint64_t)c);
+// a / b for a >= 0 and b > 0: a division of 64 bits takes five times one of 32.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if ((uint64_t)(a | b) >> 32 == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
 }
 
 // The lowest token that position `pos` sees (window 0: the first).
@@ -226,10 +230,9 @@ __device__ __forceinline__ bool kv_find(const KvArgs& A, const KvPart& part, int
 struct KvRows {
   int first, head0, pos0;                     // pos0: position of query `first`
   __device__ __forceinline__ KvRows(const KvArgs& A, int r0, int n, int len)
-      : first((int)((uint32_t)r0 / (uint32_t)A.group)), head0((int)((uint32_t)r0 % (uint32_t)A.group)),
-        pos0(len - n + first) {}
-  __device__ __forceinline__ int query(const KvArgs& A, int i) const { return (int)((uint32_t)(head0 + i) / (uint32_t)A.group); }
-  __device__ __forceinline__ int head(const KvArgs& A, int i) const { return (int)((uint32_t)(head0 + i) % (uint32_t)A.group); }
+      : first((int)A.by_group((uint32_t)r0)), head0(r0 - first * A.group), pos0(len - n + first) {}
+  __device__ __forceinline__ int query(const KvArgs& A, int i) const { return (int)A.by_group((uint32_t)(head0 + i)); }
+  __device__ __forceinline__ int head(const KvArgs& A, int i) const { return head0 + i - query(A, i) * A.group; }
 };
 
 // Tokens [lo, hi) that the item's rows see between them, and its tiles [t0, t1).
@@ -528,7 +531,9 @@ struct KvLaunch {
     if (p.pro_items * c.kv_heads > 0x7FFFFFFF / PTHREADS) return WQ_EINVAL;
     args = KvArgs{(const uint16_t*)c.q, c.q_stride, c.cu_q, c.kv_lens, c.batch, c.tokens, c.q_heads, c.kv_heads,
                   c.q_heads / c.kv_heads, (int)(c.window < 0x7FFFFFFF ? c.window : 0), c.k_codes, c.k_scales, c.v_codes,
-                  c.v_scales, log2_page(c.page), c.num_pages, c.table, c.max_blocks, c.sm_scale, c.softcap, c.out, c.lse};
+                  c.v_scales, log2_page(c.page), c.num_pages, c.table, c.max_blocks, c.sm_scale, c.softcap, c.out, c.lse, 0, 0};
+    while ((1 << args.group_shift) < args.group) args.group_shift++;
+    args.group_mul = (uint32_t)((uint64_t(1) << (31 + args.group_shift)) / (uint32_t)args.group + 1);
     uint8_t* ws = (uint8_t*)c.workspace;
     dec = KvShare{p.solo ? 0 : p.groups, p.rows, 4 * p.groups, p.log_joins, false, (KvChain*)ws, (float*)(ws + p.dec_sums),
                   (float*)(ws + p.dec_stats)};
