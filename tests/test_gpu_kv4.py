@@ -732,3 +732,37 @@ def test_workspace_of_the_caller(W):
         a = W.wq_kv4_attention(*args, max_q=max(ql))
         b = W.wq_kv4_attention(*args, max_q=max(ql), workspace=ws)
         assert torch.equal(a, b) and (ws[n:] == 0xFF).all()
+
+
+def test_calls_through_ctypes(W, monkeypatch):
+    """The same bits by the calls that go through ctypes (which those that the module of compiled calls
+    refuses do) as by the compiled ones; numbers of other types go that way by themselves."""
+    banner("kv4: compiled calls and ctypes")
+    g = np.random.default_rng(22)
+    Hq, H, D, P, T = 8, 2, 64, 16, 40
+    slots, N = _slots(g, [5], [T], P)
+    q, k, v = (dev_bf16(bf16_round(g.standard_normal((T, h, D)))) for h in (Hq, H, H))
+    pos, cs, start = _i32(5 + np.arange(T)), dev_f32(_angles(100, D)), [_cache4(g, N, H, P, D), _cache(g, N, H, P, D)]
+    args = (_i32([slots[::P] // P]), _i32([0, T]), _i32([T]))
+
+    def everything(window=np.int64(9)):
+        out = []
+        for c in start:
+            dev = [dev_u8(a) for a in c]
+            out += [W.wq_kv_append_rotary(q, k, v, pos, cs, _i64(slots), *dev, interleaved=True), *dev]
+        dev = [dev_u8(a) for a in start[0]]
+        assert W.wq_kv4_append(k, v, _i64(slots), *dev) is None
+        out += dev
+        out += W.wq_kv4_attention(q, *dev, *args, return_lse=True)
+        out.append(W.wq_kv4_attention(q, *dev, *args, window=window, softcap=20, sm_scale=1))
+        mine = torch.empty_like(q)
+        assert W.wq_kv4_attention(q, *dev, *args, window=9, softcap=20.0, sm_scale=1.0, out=mine) is mine
+        return out + [mine]
+
+    a = everything()
+    took = []
+    for name in ("kv4_append", "kv_append_rotary", "kv4_attention"):
+        monkeypatch.setattr(W._calls, name, lambda *x, name=name: took.append(name) or NotImplemented)
+    b = everything()
+    assert len(took) == 6 and len(a) == len(b) and all(torch.equal(x, y) for x, y in zip(a, b))
+    assert torch.equal(a[-1], a[-2])

@@ -31,6 +31,7 @@ if not os.path.exists(LIB_PATH):
         "(hipcc, gfx950). There is no fallback path.")
 
 lib = ctypes.CDLL(LIB_PATH)
+from . import _calls  # noqa: E402 (linked to the library)
 
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
 _SIGS = {
@@ -560,7 +561,8 @@ def wq_kv4_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_codes
     """wq_kv_append into the 4-bit cache: codes uint8 [N, heads, page, head_dim / 2] and
     [N, heads, head_dim / 2, page] (two E2M1 channels a byte), E8M0 scales uint8
     [N, heads, head_dim / 32, page]."""
-    _append(lib.wq_kv4_append, "wq_kv4_append", _kv4_cache, k, v, slots, k_codes, k_scales, v_codes, v_scales)
+    if _calls.kv4_append(k, v, slots, k_codes, k_scales, v_codes, v_scales) is NotImplemented:
+        _append(lib.wq_kv4_append, "wq_kv4_append", _kv4_cache, k, v, slots, k_codes, k_scales, v_codes, v_scales)
 
 
 def _append(fn, where, cache, k, v, slots, k_codes, k_scales, v_codes, v_scales):
@@ -583,6 +585,9 @@ def wq_kv_append_rotary(q, k: torch.Tensor, v: torch.Tensor, positions: torch.Te
     (i, i + rot / 2), or (2i, 2i + 1) if interleaved.  Returns the rotated queries, bf16: q_out
     (tokens may be strided; q itself if that is bf16) or a new tensor.  Rows of tokens whose
     position is outside [0, max_pos) are not written."""
+    got = _calls.kv_append_rotary(q, k, v, positions, cos_sin, slots, k_codes, k_scales, v_codes, v_scales, interleaved, q_out)
+    if got is not NotImplemented:
+        return got
     dev, T, heads, hd, k_stride = _token_rows(k, "k")
     v_stride = _token_rows(v, "v")[4]
     four = isinstance(k_scales, torch.Tensor) and k_scales.dim() == 4
@@ -651,6 +656,10 @@ def wq_kv4_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Ten
                      return_lse: bool = False, workspace=None):
     """wq_kv_attention over the 4-bit cache (layout: wq_kv4_append), with the same arguments; its
     workspace is of wq_kv4_attention_workspace_size."""
+    got = _calls.kv4_attention(q, k_codes, k_scales, v_codes, v_scales, block_table, cu_q, kv_lens, sm_scale, softcap,
+                               window, max_q, out, return_lse, workspace)
+    if got is not NotImplemented:
+        return got
     return _attention(lib.wq_kv4_attention_workspace_size, lib.wq_kv4_attention, "wq_kv4_attention", _kv4_cache, q, k_codes, k_scales,
                       v_codes, v_scales, block_table, cu_q, kv_lens, sm_scale, softcap, window, max_q, out, return_lse,
                       workspace)

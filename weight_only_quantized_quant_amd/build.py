@@ -6,8 +6,9 @@
 
 Always recompiles.  Each source is compiled to an object of its own in
 `_build/` at the repository root, in parallel, then the objects are linked.
-The library lands next to this file so that it travels with the source tree;
-nothing is installed.
+Beside the library, `_calls.so` is the Python module of the calls that a decode
+step makes for each layer.  Both land next to this file so that they travel with
+the source tree; nothing is installed.
 """
 from __future__ import annotations
 
@@ -22,6 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libwq.so")
+CALLS = os.path.join(HERE, "_calls.so")
 
 SOURCES = ["wq_quant.hip", "wq_gemm.hip", "wq_moe.hip", "wq_w8a8.hip", "wq_kv.hip", "wq_kv_append.hip", "wq_kv4.hip", "wq_util.hip", "wq_status.cpp"]
 
@@ -53,9 +55,25 @@ def _run(cmd, verbose):
     res = subprocess.run(cmd, capture_output=True, text=True)
     err = "\n".join(l for l in (res.stdout + res.stderr).splitlines() if NOISE not in l)
     if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}):\n{err}")
+        raise RuntimeError(f"{cmd[0]} failed ({res.returncode}):\n{err}")
     if verbose and err.strip():
         print(err, flush=True)
+
+
+def calls_commands(obj: str, out: str) -> list:
+    """The host compiler's two commands for the Python module of the per-layer calls.  torch's
+    libraries are in the process before the module is; libwq.so is found beside it."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    cxx = os.environ.get("CXX", "g++")
+    inc = [*include_paths(), "/opt/rocm/include", sysconfig.get_paths()["include"]]
+    return [[cxx, "-O2", "-std=c++17", "-fPIC", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *[x for i in inc for x in ("-isystem", i)],
+             "-I", INCLUDE, "-c", os.path.join(CSRC, "wq_calls.cpp"), "-o", obj],
+            [cxx, "-shared", obj, "-o", out, *[f"-L{p}" for p in library_paths()], "-ltorch_python", "-ltorch_cpu", "-lc10",
+             "-lc10_hip", f"-L{HERE}", "-l:libwq.so", "-Wl,-rpath,$ORIGIN"]]
 
 
 def build(verbose: bool = False) -> str:
@@ -63,12 +81,16 @@ def build(verbose: bool = False) -> str:
     objs = [os.path.join(OBJDIR, os.path.splitext(s)[0] + ".o") for s in SOURCES]
     cmds = [[hipcc(), *HIP_FLAGS, *SOURCE_FLAGS.get(s, []), "-I", INCLUDE, "-I", CSRC, "-c", os.path.join(CSRC, s),
              "-o", o] for s, o in zip(SOURCES, objs)]
+    compile_calls, link_calls = calls_commands(os.path.join(OBJDIR, "wq_calls.o"), CALLS + ".tmp")
+    cmds.append(compile_calls)
     jobs = max(1, min(len(cmds), int(os.environ.get("MAX_JOBS", "0")) or os.cpu_count() or 1, 16))
     with ThreadPoolExecutor(jobs) as pool:
         list(pool.map(lambda c: _run(c, verbose), cmds))
     tmp = LIB + ".tmp"
     _run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp], verbose)
     os.replace(tmp, LIB)
+    _run(link_calls, verbose)
+    os.replace(CALLS + ".tmp", CALLS)
     return LIB
 
 
