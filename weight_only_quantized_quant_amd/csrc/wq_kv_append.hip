@@ -11,6 +11,58 @@ namespace {
 
 typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 
+// Eight elements as they were loaded.
+template <bool BF16>
+struct Raw8 {
+  uint32_t w[BF16 ? 4 : 8];
+  __device__ __forceinline__ void load(const void* x, int64_t at) {
+#pragma unroll
+    for (int e = 0; e < (BF16 ? 1 : 2); e++) {
+      const u32x4_t q = ld16((const uint8_t*)x + at * (BF16 ? 2 : 4) + 16 * e);
+#pragma unroll
+      for (int b = 0; b < 4; b++) w[4 * e + b] = q[b];
+    }
+  }
+  // the larger of m and the magnitudes, as bit patterns: one half word each for
+  // bf16 (both halves of m), one word for fp32; NaN and infinity come out largest
+  __device__ __forceinline__ uint32_t magnitude(uint32_t m) const {
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 4 : 8); i++) {
+      if constexpr (BF16) {
+        const u16x2_t a = __builtin_bit_cast(u16x2_t, w[i] & 0x7FFF7FFFu), b = __builtin_bit_cast(u16x2_t, m);
+        m = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(a, b));
+      } else {
+        const uint32_t a = w[i] & 0x7FFFFFFFu;
+        m = a > m ? a : m;
+      }
+    }
+    return m;
+  }
+  __device__ __forceinline__ void widen(float v[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+      v[i] = BF16 ? (i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2])) : __uint_as_float(w[BF16 ? 0 : i]);
+  }
+  // E4M3 codes of x * 2^(127-c); the finite magnitudes are at most 448 then
+  __device__ __forceinline__ u32x2_t codes(float scale_as_e8m0) const {
+    u32x2_t out;
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      s16x2_t r = {0, 0};
+      if constexpr (BF16) {
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, w[2 * h]), scale_as_e8m0, false);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, w[2 * h + 1]), scale_as_e8m0, true);
+      } else {
+        const uint32_t* f = w + (BF16 ? 0 : 4 * h);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, __uint_as_float(f[0]), __uint_as_float(f[1]), scale_as_e8m0, false);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, __uint_as_float(f[2]), __uint_as_float(f[3]), scale_as_e8m0, true);
+      }
+      out[h] = __builtin_bit_cast(uint32_t, r);
+    }
+    return out;
+  }
+};
+
 // ---------------------------------------------------------------------------
 // Rotation by position
 // ---------------------------------------------------------------------------
@@ -74,21 +126,65 @@ __device__ __forceinline__ void rotate8(const void* x, int64_t row, int ch, cons
   }
 }
 
-// The queries, 8 channels a thread, rounded once to bf16 (half a step of 2^-8; fp32
-// before that).  q_out may be q itself: the 8 or 16 threads of a head are in one
-// wave, which has read them all before it writes.
+// The queries, rounded once to bf16 (half a step of 2^-8; fp32 before that).  A
+// thread takes 16 channels that are turned together (8 and their partners, or 16
+// behind `rot`) of QHEADS heads of a token, whose angles it reads once, with all of
+// its loads in flight.  It writes what it has read itself, so q_out may be q.
+// Bound by bytes: 8192 tokens x 32 heads of 128 take 24 us alone (5.6 TB/s; 8
+// channels a thread, one after the other, 40).  One head a thread: the same in
+// bf16, 29 us beside the 8-bit append; four: 4.2 us instead of 3.4 for 64 tokens.
+constexpr int QHEADS = 2;
+
 template <bool BF16, int D>
 __device__ __forceinline__ void rotate_queries(const KvRotary& R, int64_t tokens) {
-  const int64_t units = tokens * R.q_heads * (D / 8), groups = (int64_t)gridDim.x * gridDim.y * (gridDim.z - 2);
+  const int64_t sets = (R.q_heads + QHEADS - 1) / QHEADS, units = tokens * sets * (D / 16);
+  const int64_t groups = (int64_t)gridDim.x * gridDim.y * (gridDim.z - 2);
   const int64_t group = ((int64_t)(blockIdx.z - 2) * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+  const int half = R.rot >> 1;
   for (int64_t u = group * KV_THREADS + threadIdx.x; u < units; u += groups * KV_THREADS) {
-    const int64_t row = u / (D / 8), t = row / R.q_heads;
-    const int ch = (int)(u % (D / 8)) * 8, head = (int)(row % R.q_heads);
-    if (!R.there(t)) continue;
-    float f[8];
-    rotate8<BF16, float>(R.q, t * R.q_stride + (int64_t)head * D, ch, R, t, f);
-    *reinterpret_cast<u32x4_t*>(R.q_out + t * R.q_out_stride + (int64_t)head * D + ch) =
-        u32x4_t{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+    const int64_t set = u / (D / 16), t = set / sets;
+    const int i = (int)(u % (D / 16)), head = (int)(set - t * sets) * QHEADS;
+    const int64_t pos = R.positions[t];
+    if (pos < 0 || pos >= R.max_pos) continue;
+    const bool turned = 16 * i < R.rot;
+    const int a = turned && !R.interleaved ? 8 * i : 16 * i, b = turned && !R.interleaved ? a + half : a + 8;
+    float c[8], s[8];
+    Raw8<BF16> x[QHEADS][2];
+    const int64_t from = t * R.q_stride + (int64_t)head * D, to = t * R.q_out_stride + (int64_t)head * D;
+#pragma unroll
+    for (int h = 0; h < QHEADS; h++)
+      if (head + h < R.q_heads) {
+        x[h][0].load(R.q, from + h * D + a);
+        x[h][1].load(R.q, from + h * D + b);
+      }
+    if (turned) {
+      load8_f32(R.cos_sin + pos * R.rot + 8 * i, c);
+      load8_f32(R.cos_sin + pos * R.rot + half + 8 * i, s);
+    }
+#pragma unroll
+    for (int h = 0; h < QHEADS; h++)
+      if (head + h < R.q_heads) {
+        float f[16];
+        x[h][0].widen(f);
+        x[h][1].widen(f + 8);
+        auto turn = [&](float& v, float& w, int e) {
+          const float v0 = v, w0 = w;
+          v = __builtin_fmaf(v0, c[e], -(w0 * s[e]));
+          w = __builtin_fmaf(w0, c[e], v0 * s[e]);
+        };
+        if (turned && R.interleaved) {
+#pragma unroll
+          for (int e = 0; e < 8; e++) turn(f[2 * e], f[2 * e + 1], e);
+        } else if (turned) {
+#pragma unroll
+          for (int e = 0; e < 8; e++) turn(f[e], f[8 + e], e);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; k++)
+          *reinterpret_cast<u32x4_t*>(R.q_out + to + h * D + (k ? b : a)) =
+              u32x4_t{pack_bf16x2(f[8 * k], f[8 * k + 1]), pack_bf16x2(f[8 * k + 2], f[8 * k + 3]),
+                      pack_bf16x2(f[8 * k + 4], f[8 * k + 5]), pack_bf16x2(f[8 * k + 6], f[8 * k + 7])};
+      }
   }
 }
 
@@ -120,50 +216,6 @@ __device__ __forceinline__ int e8m0_cover(uint32_t bits) {
   const int c = (int)(bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   return c > 0 ? c : 0;
 }
-
-// Eight elements as they were loaded.
-template <bool BF16>
-struct Raw8 {
-  uint32_t w[BF16 ? 4 : 8];
-  // the larger of m and the magnitudes, as bit patterns: one half word each for
-  // bf16 (both halves of m), one word for fp32; NaN and infinity come out largest
-  __device__ __forceinline__ uint32_t magnitude(uint32_t m) const {
-#pragma unroll
-    for (int i = 0; i < (BF16 ? 4 : 8); i++) {
-      if constexpr (BF16) {
-        const u16x2_t a = __builtin_bit_cast(u16x2_t, w[i] & 0x7FFF7FFFu), b = __builtin_bit_cast(u16x2_t, m);
-        m = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(a, b));
-      } else {
-        const uint32_t a = w[i] & 0x7FFFFFFFu;
-        m = a > m ? a : m;
-      }
-    }
-    return m;
-  }
-  __device__ __forceinline__ void widen(float v[8]) const {
-#pragma unroll
-    for (int i = 0; i < 8; i++)
-      v[i] = BF16 ? (i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2])) : __uint_as_float(w[BF16 ? 0 : i]);
-  }
-  // E4M3 codes of x * 2^(127-c); the finite magnitudes are at most 448 then
-  __device__ __forceinline__ u32x2_t codes(float scale_as_e8m0) const {
-    u32x2_t out;
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-      s16x2_t r = {0, 0};
-      if constexpr (BF16) {
-        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, w[2 * h]), scale_as_e8m0, false);
-        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, w[2 * h + 1]), scale_as_e8m0, true);
-      } else {
-        const uint32_t* f = w + (BF16 ? 0 : 4 * h);
-        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, __uint_as_float(f[0]), __uint_as_float(f[1]), scale_as_e8m0, false);
-        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, __uint_as_float(f[2]), __uint_as_float(f[3]), scale_as_e8m0, true);
-      }
-      out[h] = __builtin_bit_cast(uint32_t, r);
-    }
-    return out;
-  }
-};
 
 // One run (tokens t .. t+n-1 at offsets off .. off+n-1 of one page) of one
 // head, keys or values, by the whole workgroup.  A thread takes 8 channels of
@@ -450,7 +502,14 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_append(
   const int64_t limit = num_pages * PAGE;
   const int64_t t0 = (int64_t)blockIdx.x * chunk;
   // every wave looks at the chunk's slots and those that a run of them may reach
-  auto slot_of = [&](int64_t t) { return t < tokens && (!ROT || rotary.there(t)) ? slots[t] : (int64_t)-1; };
+  auto slot_of = [&](int64_t t) {
+    int64_t s = -1;
+    if (t < tokens) {
+      s = slots[t];
+      if constexpr (ROT) s = rotary.there(t) ? s : -1;
+    }
+    return s;
+  };
   const int64_t s0 = slot_of(t0 + lane), s1 = slot_of(t0 + 64 + lane);
   const int64_t before0 = t0 ? slot_of(t0 - 1) : -1;
   int64_t before = __shfl_up(s0, 1, 64);
@@ -536,7 +595,10 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv4_append(const Kv4Append A, co
   const bool values = blockIdx.z == 1;
   const int64_t t0 = (int64_t)blockIdx.x * A.chunk, page = (int64_t)1 << A.log_page;
   int64_t slot = -1;                          // of token t0 + lane, in every wave
-  if (lane < A.chunk && t0 + lane < A.tokens && (!ROT || rotary.there(t0 + lane))) slot = A.slots[t0 + lane];
+  if (lane < A.chunk && t0 + lane < A.tokens) {
+    slot = A.slots[t0 + lane];
+    if constexpr (ROT) slot = rotary.there(t0 + lane) ? slot : -1;
+  }
   if (slot >= A.num_pages << A.log_page) slot = -1;
   const void* x = values ? A.v : A.k;
   const int64_t stride = values ? A.v_stride : A.k_stride;
@@ -643,12 +705,14 @@ wq_status append(const void* k, int64_t k_stride, const void* v, int64_t v_strid
   if (tokens == 0) return WQ_OK;
   hipStream_t s = (hipStream_t)stream;
   const bool eight = cache == WQ_E4M3;
-  int chunk = eight ? 1 : 16;
+  // tokens a workgroup: few at least, so that a step's are spread over the chip (64 tokens x 8 heads: 4-bit 4.0-4.2 us in
+  // fours, 4.3 singly, 5.0 in sixteens; 8-bit with rotation 4.5 in fours, 6.6 singly, where its workgroups are many)
+  int chunk = !eight || rotary ? 4 : 1;
   while (chunk < 64 && (chunk < page || !eight) && (tokens + chunk - 1) / chunk * heads * 2 > 2048) chunk *= 2;
   const int64_t gx = (tokens + chunk - 1) / chunk;
   unsigned gz = 2;
-  if (r.q_heads > 0) {                        // four times 8 channels a thread, or fewer
-    const int64_t groups = (tokens * r.q_heads * (head_dim / 8) + 4 * KV_THREADS - 1) / (4 * KV_THREADS);
+  if (r.q_heads > 0) {
+    const int64_t groups = (tokens * ((r.q_heads + QHEADS - 1) / QHEADS) * (head_dim / 16) + KV_THREADS - 1) / KV_THREADS;
     const int64_t z = (groups + gx * heads - 1) / (gx * heads);
     gz += (unsigned)(z < 65533 ? z : 65533);
   }
