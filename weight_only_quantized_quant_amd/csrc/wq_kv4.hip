@@ -87,7 +87,7 @@ struct KvAlike {
 // 16 (m / 4) + 4 a + m % 4, result rows 4 g + i are then tokens 16 g + 4 a + i;
 // step h of the products takes channels D / 4 g + 8 h on of each.  V^T: operand row m of tiles 2 b and 2 b + 1 are
 // channels 32 b + 2 m and the next.
-template <int D, bool CAP, int WHICH, int NR, int WAVES = 4, int DEEP = (D == 128 && NR == 2 ? 1 : 2)>
+template <int D, bool CAP, int WHICH, int NR, bool SOLO, int WAVES = 4>
 __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, const KvShare part) {
   constexpr int KH = D / 32, NB = D / 32, DT = D / 16, R = 16 * NR;   // k steps, blocks, channel tiles
   __shared__ __attribute__((aligned(16))) float so[WAVES][R][D + 4];
@@ -99,8 +99,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, co
   const KvChain none = {};
 
   // all the work, in tiles or in row tiles, and this wave's share [u0, u1) of it
-  const bool solo = part.groups == 0;
-  auto units_of = [&](const KvRequest& r) { return solo || r.tiles <= 0 ? 1 : r.tiles; };
+  auto units_of = [&](const KvRequest& r) { return SOLO || r.tiles <= 0 ? 1 : r.tiles; };
   KvRequest lanes;
   int64_t total = 0, tiles = 0, end = 0, tiles_end = 0;     // of all requests; up to and with the lane's
   auto scan = [&](int64_t base, int64_t& before, int64_t& tiles_before) {      // 64 requests from `base` on
@@ -111,13 +110,13 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, co
     tiles_before = lane64(tiles_end, 63);
   };
   for (int64_t base = 0; base < A.batch; base += 64) scan(base, total, tiles);
-  if (part.by_tile && blockIdx.x == 0)        // entries behind the last row tile's
+  if (!SOLO && part.by_tile && blockIdx.x == 0)        // entries behind the last row tile's
     for (int64_t i = tiles + tid; i < part.chains; i += 64 * WAVES) part.chain[i] = none;
-  const bool each = !solo && !part.by_tile;   // an entry for each wave
+  const bool each = !SOLO && !part.by_tile;   // an entry for each wave
   // the first `extra` shares have one unit more
-  const int64_t shares = solo ? WAVES * total : total < WAVES * part.groups ? total : WAVES * part.groups;
-  const int64_t least = solo || total == 0 ? 0 : quotient(total, shares), extra = total - least * shares;
-  auto share_at = [&](int64_t y) { return y >= shares ? total : solo ? y / WAVES : y * least + (y < extra ? y : extra); };
+  const int64_t shares = SOLO ? WAVES * total : total < WAVES * part.groups ? total : WAVES * part.groups;
+  const int64_t least = SOLO || total == 0 ? 0 : quotient(total, shares), extra = total - least * shares;
+  auto share_at = [&](int64_t y) { return y >= shares ? total : SOLO ? y / WAVES : y * least + (y < extra ? y : extra); };
   const int64_t u0 = share_at(x), u1 = share_at(x + 1), g0 = share_at(WAVES * group), g1 = share_at(WAVES * (group + 1));
   if (g0 >= g1) {                             // an idle workgroup
     if (each && kvh == 0 && lane == 0) part.chain[x] = none;
@@ -145,7 +144,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, co
   find(g0);
   auto units = [&]() { return units_of(q); };
   int rt = (int)quotient(g0 - begin, units());     // row tiles in order of their units, the last rows first
-  const bool joined = g1 <= begin + (int64_t)(rt + 1) * units();   // always so if solo
+  const bool joined = SOLO || g1 <= begin + (int64_t)(rt + 1) * units();
   if (!joined) {
     if (u0 >= u1) {
       if (each && kvh == 0 && lane == 0) part.chain[x] = none;
@@ -186,64 +185,53 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, co
       const int a = q.first + (int)((joined ? g0 : u) - row_begin);
       return a < lo / TILE ? lo / TILE : a;
     };
-    int t = first_tile(), t1 = q.first + (solo ? q.tiles : (int)((joined ? g1 : stop) - row_begin));
+    int t = first_tile(), t1 = q.first + (SOLO ? q.tiles : (int)((joined ? g1 : stop) - row_begin));
     t1 = t1 > (hi + TILE - 1) / TILE ? (hi + TILE - 1) / TILE : t1;
     t += joined ? wave : 0;
 
     const int32_t* tab = A.table + (int64_t)request * A.max_blocks;
-    struct Buffer {                           // a tile on its way
-      uint32_t kr[4][KH];
-      u32x4_t vr[NB];
-      u32x4_t ksc;                            // scales of 16 keys, this lane's among them
-      uint32_t vsc;                           // scales of four of its 16 values, in block m / 4
-      bool vok;
-    } buf[DEEP];
-    struct Ids {
-      int k, v;
-    } next;                                   // page ids of the next tile to load
-    auto ids_of = [&](int t) {
+    // a tile on its way
+    uint32_t kr[4][KH], vsc;                  // vsc: scales of four of the lane's 16 values, in block m / 4
+    u32x4_t vr[NB], ksc;                      // ksc: scales of 16 keys, this lane's among them
+    bool vok;
+    int idk, idv;                             // page ids of the next tile to load
+    auto load_ids = [&](int t) {
       const int ck = (t * TILE + 16 * (m >> 2)) >> A.log_page, cv = (t * TILE + 16 * g) >> A.log_page;
-      return Ids{tab[ck < last_col ? ck : last_col], tab[cv < last_col ? cv : last_col]};
+      idk = tab[ck < last_col ? ck : last_col];
+      idv = tab[cv < last_col ? cv : last_col];
     };
-    auto load_k = [&](Buffer& b, int t, int idk) {
+    auto load_k = [&](int t) {
       const uint64_t id = idk >= 0 && idk < A.num_pages ? idk : 0;
       const int off = (t * TILE + 16 * (m >> 2)) & in_page;
-      b.ksc = ld16(ksb + (id * page_scales + (((D == 128 ? g : g >> 1) << A.log_page) + off)));
+      ksc = ld16(ksb + (id * page_scales + (((D == 128 ? g : g >> 1) << A.log_page) + off)));
       const uint8_t* p = kbase + (id * page_bytes + (off + (m & 3)) * (D / 2) + 4 * KH * g);
 #pragma unroll
       for (int a = 0; a < 4; a++) {
         if constexpr (D == 128) {
           const u32x4_t w = ld16(p + 4 * a * (D / 2));
 #pragma unroll
-          for (int h = 0; h < KH; h++) b.kr[a][h] = w[h];
+          for (int h = 0; h < KH; h++) kr[a][h] = w[h];
         } else {
           const u32x2_t w = *reinterpret_cast<const u32x2_t*>(p + 4 * a * (D / 2));
 #pragma unroll
-          for (int h = 0; h < KH; h++) b.kr[a][h] = w[h];
+          for (int h = 0; h < KH; h++) kr[a][h] = w[h];
         }
       }
     };
-    auto load_v = [&](Buffer& b, int t, int idv) {
-      b.vok = idv >= 0 && idv < A.num_pages;
-      const uint64_t id = b.vok ? idv : 0;
+    auto load_v = [&](int t) {
+      vok = idv >= 0 && idv < A.num_pages;
+      const uint64_t id = vok ? idv : 0;
       const int off = (t * TILE + 16 * g) & in_page;
       const uint8_t* p = vbase + (id * page_bytes + ((m << A.log_page) + off));
-      b.vsc = *reinterpret_cast<const uint32_t*>(vsb + (id * page_scales + ((((m >> 2) & (NB - 1)) << A.log_page) + off + 4 * (m & 3))));
+      vsc = *reinterpret_cast<const uint32_t*>(vsb + (id * page_scales + ((((m >> 2) & (NB - 1)) << A.log_page) + off + 4 * (m & 3))));
 #pragma unroll
-      for (int i = 0; i < NB; i++) b.vr[i] = ld16(p + ((16 * i) << A.log_page));
+      for (int b = 0; b < NB; b++) vr[b] = ld16(p + ((16 * b) << A.log_page));
     };
     if (t < t1) {
-      Ids first[DEEP];
-#pragma unroll
-      for (int x = 0; x < DEEP; x++)
-        if (x == 0 || t + x * step < t1) first[x] = ids_of(t + x * step);
-#pragma unroll
-      for (int x = 0; x < DEEP; x++)
-        if (x == 0 || t + x * step < t1) {
-          load_k(buf[x], t + x * step, first[x].k);
-          load_v(buf[x], t + x * step, first[x].v);
-        }
-      if (t + DEEP * step < t1) next = ids_of(t + DEEP * step);
+      load_ids(t);
+      load_k(t);
+      load_v(t);
+      if (t + step < t1) load_ids(t + step);
     }
 
     // query fragments: columns m of q^T, channels D / 4 g + 8 h on in step h; row m's limits
@@ -273,26 +261,26 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, co
       mx[c] = -INFINITY;
       l[c] = 0.0f;
     }
-    auto turn = [&](Buffer& b, int t) {
+    for (; t < t1; t += step) {
       const int j0 = t * TILE + 16 * g;       // this lane's 16 tokens in scores and V^T
-      const bool more = t + DEEP * step < t1;
+      const bool more = t + step < t1;
       f32x4_t s[NR][4];
 #pragma unroll
       for (int a = 0; a < 4; a++) {
         // byte m % 4, turned to where the conversion reads a scale
-        const float ks = __uint_as_float(__builtin_amdgcn_alignbit(b.ksc[a], b.ksc[a], 9 + 8 * (m & 3)));
+        const float ks = __uint_as_float(__builtin_amdgcn_alignbit(ksc[a], ksc[a], 9 + 8 * (m & 3)));
 #pragma unroll
         for (int c = 0; c < NR; c++) s[c][a] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
         for (int h = 0; h < KH; h++) {
-          const bf16x8_t k = e2m1_bf16x8(b.kr[a][h], ks);
+          const bf16x8_t k = e2m1_bf16x8(kr[a][h], ks);
 #pragma unroll
           for (int c = 0; c < NR; c++) s[c][a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, qf[c][h], s[c][a], 0, 0, 0);
         }
       }
-      if (more) load_k(b, t + DEEP * step, next.k);
-      const bool edge = t * TILE + TILE - 1 > rows.pos0 || t * TILE < lo_max || __any(!b.vok);
-      if (edge) b.vsc = finite_scales(b.vsc); // of tokens that not every row sees
+      if (more) load_k(t + step);
+      const bool edge = t * TILE + TILE - 1 > rows.pos0 || t * TILE < lo_max || __any(!vok);
+      if (edge) vsc = finite_scales(vsc);     // of tokens that not every row sees
       bf16x8_t p0[NR], p1[NR];
 #pragma unroll
       for (int c = 0; c < NR; c++) {
@@ -309,7 +297,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, co
           for (int i = 0; i < 16; i++) s[c][i >> 2][i & 3] = v[i];
         }
         if (edge) {                           // tokens outside the row's limits
-          const int z = b.vok ? pos[c] - j0 : -1, low = rlo[c] - j0;
+          const int z = vok ? pos[c] - j0 : -1, low = rlo[c] - j0;
 #pragma unroll
           for (int a = 0; a < 4; a++)
 #pragma unroll
@@ -347,12 +335,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, co
         p0[c] = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[0], pw[1], pw[2], pw[3]}));
         p1[c] = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[4], pw[5], pw[6], pw[7]}));
       }
-      const uint32_t vsc = b.vsc;
       for_each(std::make_integer_sequence<int, NB>{}, [&](auto block) {
         constexpr int B = decltype(block)::value;
         bf16x8_t v[2][2];                     // channels 32 B + 2 m and the next, tokens 0-7 and 8-15
-        value_pairs(b.vr[B][0], b.vr[B][1], row_lane<4 * B>(vsc), row_lane<4 * B + 1>(vsc), v[0][0], v[1][0]);
-        value_pairs(b.vr[B][2], b.vr[B][3], row_lane<4 * B + 2>(vsc), row_lane<4 * B + 3>(vsc), v[0][1], v[1][1]);
+        value_pairs(vr[B][0], vr[B][1], row_lane<4 * B>(vsc), row_lane<4 * B + 1>(vsc), v[0][0], v[1][0]);
+        value_pairs(vr[B][2], vr[B][3], row_lane<4 * B + 2>(vsc), row_lane<4 * B + 3>(vsc), v[0][1], v[1][1]);
 #pragma unroll
         for (int e = 0; e < 2; e++)
 #pragma unroll
@@ -362,17 +349,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, co
           }
       });
       if (more) {
-        load_v(b, t + DEEP * step, next.v);
-        if (t + (DEEP + 1) * step < t1) next = ids_of(t + (DEEP + 1) * step);
+        load_v(t + step);
+        if (t + 2 * step < t1) load_ids(t + 2 * step);
       }
-    };
-    while (t < t1) {
-#pragma unroll
-      for (int x = 0; x < DEEP; x++)
-        if (x == 0 || t < t1) {
-          turn(buf[x], t);
-          t += step;
-        }
     }
 #pragma unroll
     for (int c = 0; c < NR; c++) {
@@ -382,9 +361,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, co
 
     // this wave, or the workgroup, has units [from, to) of the row tile's
     const int64_t from = joined ? g0 : u, to = joined ? g1 : stop;
-    const bool whole = from == row_begin && to == row_end;
+    const bool whole = SOLO || (from == row_begin && to == row_end);
     const int slot = 2 * (joined ? WAVES * group : x) + (from == row_begin ? 0 : 1);
-    if (from == row_begin && !solo && (!joined || wave == 0)) {
+    if (from == row_begin && !SOLO && (!joined || wave == 0)) {
       KvChain c = none;
       if (!whole) {
         // the last wave: the one whose share holds unit row_end - 1
@@ -665,7 +644,7 @@ __global__ __launch_bounds__(PTHREADS, D == 64 ? 3 : 2) void k_kv4_prompt(const 
   const uint8_t* vfrag[2];
 #pragma unroll
   for (int u = 0; u < 2; u++) vfrag[u] = sv[0] + (128 * u + 32 * h + (m ^ (2 * (2 * u + h)))) * 16;
-  constexpr int HOLD = 4;                     // fragments read ahead of their use
+  constexpr int HOLD = D == 128 ? 6 : 4;      // fragments read ahead of their use
   bf16x8_t kf[HOLD];
   auto frag_k = [&](int at, int u, int k) {
     return *reinterpret_cast<const bf16x8_t*>(kfrag + at + (u * KS + k) * 1024 + (m ^ (XK * k)) * 16);
@@ -826,7 +805,8 @@ __global__ __launch_bounds__(PTHREADS, D == 64 ? 3 : 2) void k_kv4_prompt(const 
   if (A.lse && h == 0) A.lse[orow] = l == 0.0f ? -INFINITY : (mx + __builtin_log2f(l)) * LN2;
 }
 
-// Workgroups of 8 waves for row tiles of their own, where each has a CU.
+// Workgroups of 8 waves for row tiles of their own, where each has a CU (1 x 1000 tokens 10.7 ->
+// 10.4 us, 16 x 2000 17.2 -> 16.0; 33 x 1000, 264 workgroups, 16.4 -> 20.3).
 constexpr unsigned SOLO_WIDE = 256;
 
 template <int D, bool CAP>
@@ -836,15 +816,17 @@ void launch_attention(const KvArgs& A, const KvPlan& p, const KvShare& dec, cons
     const unsigned items = (unsigned)p.pro_items * h;
     if (A.log_page >= 6) k_kv4_prompt<D, CAP, true><<<items, PTHREADS, 0, s>>>(A, pro);
     else k_kv4_prompt<D, CAP, false><<<items, PTHREADS, 0, s>>>(A, pro);
-    k_kv4_decode<D, CAP, REQ_SHORT, 2><<<groups, KV_THREADS, 0, s>>>(A, dec);
+    k_kv4_decode<D, CAP, REQ_SHORT, 2, false><<<groups, KV_THREADS, 0, s>>>(A, dec);
+  } else if (p.solo) {
+    if (p.nr == 2) k_kv4_decode<D, CAP, REQ_ALL, 2, true><<<groups, KV_THREADS, 0, s>>>(A, dec);
+    else if (groups <= SOLO_WIDE) k_kv4_decode<D, CAP, REQ_ALL, 1, true, 8><<<groups, 512, 0, s>>>(A, dec);
+    else k_kv4_decode<D, CAP, REQ_ALL, 1, true><<<groups, KV_THREADS, 0, s>>>(A, dec);
+    return;
   } else if (p.nr == 2) {
-    k_kv4_decode<D, CAP, REQ_ALL, 2><<<groups, KV_THREADS, 0, s>>>(A, dec);
-  } else if (p.solo && groups <= SOLO_WIDE) {
-    k_kv4_decode<D, CAP, REQ_ALL, 1, 8><<<groups, 512, 0, s>>>(A, dec);
+    k_kv4_decode<D, CAP, REQ_ALL, 2, false><<<groups, KV_THREADS, 0, s>>>(A, dec);
   } else {
-    k_kv4_decode<D, CAP, REQ_ALL, 1><<<groups, KV_THREADS, 0, s>>>(A, dec);
+    k_kv4_decode<D, CAP, REQ_ALL, 1, false><<<groups, KV_THREADS, 0, s>>>(A, dec);
   }
-  if (p.solo) return;
   const unsigned joins = ((unsigned)dec.chains * h << p.log_joins) + (unsigned)(p.pro_slots * (PROWS / 16)) * h;
   if (p.nr == 2) k_kv_join<D, 2><<<joins, KV_THREADS, 0, s>>>(A, dec, pro);
   else k_kv_join<D, 1><<<joins, KV_THREADS, 0, s>>>(A, dec, pro);
