@@ -766,3 +766,59 @@ def test_calls_through_ctypes(W, monkeypatch):
     b = everything()
     assert len(took) == 6 and len(a) == len(b) and all(torch.equal(x, y) for x, y in zip(a, b))
     assert torch.equal(a[-1], a[-2])
+
+
+@pytest.mark.parametrize("ql", [[1, 1, 5], [40, 3, 90]])
+def test_attention_nan_queries_and_keys(W, ql):
+    """A query that is NaN or infinite makes its own row NaN and no other; a key with the NaN scale the rows that see it."""
+    banner("kv4 attention: NaN queries and keys", ql)
+    q, cu, kv, cache, table = _problem(23, 8, 2, 64, 16, ql, [300, 70, 200])
+    args = (_i32(table), _i32(cu), _i32(kv))
+    clean = dev_bf16(bf16_round(q))
+    want = W.wq_kv4_attention(clean, *[dev_u8(c) for c in cache], *args)
+    x = clean.clone()
+    rows = [(0, 3), (q.shape[0] - 1, 0)]
+    for t, h in rows:
+        x[t, h, 5] = float("nan")
+    got = W.wq_kv4_attention(x, *[dev_u8(c) for c in cache], *args)
+    for t, h in rows:
+        assert torch.isnan(got[t, h]).all()
+        got[t, h] = want[t, h]
+    assert torch.equal(got, want)
+    bad = [c.copy() for c in cache]                        # the last key of request 2: its last row sees it alone
+    bad[1][table[2, 199 // 16], 0, 1, 199 % 16] = 255
+    got = W.wq_kv4_attention(clean, *[dev_u8(c) for c in bad], *args)
+    assert torch.equal(got[:-1], want[:-1]) and torch.equal(got[-1, 4:], want[-1, 4:])
+
+
+def test_append_rotary_on_a_side_stream_and_in_a_graph(W):
+    """Launches follow the current stream; replays rotate in place once each, as eager calls do."""
+    banner("kv append rotary: side stream, graph in place")
+    g = np.random.default_rng(24)
+    Hq, H, D, P, T = 4, 2, 64, 16, 33
+    slots, N = _slots(g, [3], [T], P)
+    q, k, v = (dev_bf16(bf16_round(g.standard_normal((T, h, D)))) for h in (Hq, H, H))
+    pos, cs, sl = _i32(3 + np.arange(T)), dev_f32(_angles(60, D)), _i64(slots)
+    for c in (_cache4(g, N, H, P, D), _cache(g, N, H, P, D)):
+        eager, side, graphed = ([dev_u8(a) for a in c] for _ in range(3))
+        want = [q.clone()]
+        for _ in range(4):
+            want.append(W.wq_kv_append_rotary(want[-1], k, v, pos, cs, sl, *eager).clone())
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            W.wq_util_spin(100000)
+            out = W.wq_kv_append_rotary(q, k, v, pos, cs, sl, *side)
+        s.synchronize()
+        assert torch.equal(out, want[1]) and all(torch.equal(a, b) for a, b in zip(side, eager))
+        x = q.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            W.wq_kv_append_rotary(x, k, v, pos, cs, sl, *graphed, q_out=x)
+        for i in range(4):
+            graph.replay()
+            torch.cuda.synchronize()
+            W.wq_kv_append_rotary(q, k, v, pos, cs, sl, *side)          # eager work between the replays
+            torch.cuda.synchronize()
+            assert torch.equal(x, want[i + 1]), f"replay {i}"
+        assert all(torch.equal(a, b) for a, b in zip(graphed, eager))

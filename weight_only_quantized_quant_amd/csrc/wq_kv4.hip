@@ -90,6 +90,7 @@ struct KvAlike {
 template <int D, bool CAP, int WHICH, int NR, bool SOLO, int WAVES = 4>
 __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, const KvShare part) {
   constexpr int KH = D / 32, NB = D / 32, DT = D / 16, R = 16 * NR;   // k steps, blocks, channel tiles
+  constexpr bool FINE = NR == 1 && !SOLO;     // probabilities in two bf16 terms
   __shared__ __attribute__((aligned(16))) float so[WAVES][R][D + 4];
   __shared__ float sm[WAVES][R], sl[WAVES][R];
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
@@ -281,7 +282,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, co
       if (more) load_k(t + step);
       const bool edge = t * TILE + TILE - 1 > rows.pos0 || t * TILE < lo_max || __any(!vok);
       if (edge) vsc = finite_scales(vsc);     // of tokens that not every row sees
-      bf16x8_t p0[NR], p1[NR];
+      // bf16 for the matrix cores: half a step of 2^-8 per probability, the sum l keeps fp32.  Where
+      // contexts are long and the products few (FINE), what that leaves is multiplied too (r0, r1): the
+      // error against 64 bits is then the output's own rounding, 1.7e-3 instead of 2.3e-3 (2-norm), for
+      // half a percent of a ragged batch's time (68.2 us) and 1.8 of one long context's (58.3); row tiles
+      // of their own would pay a tenth
+      bf16x8_t p0[NR], p1[NR], r0[NR], r1[NR];
 #pragma unroll
       for (int c = 0; c < NR; c++) {
         if (c > 0 && 16 * c >= n_rows) {      // a column without rows
@@ -319,7 +325,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, co
           for (int d = 0; d < DT; d++) o[c][d] *= f;
         }
         const float off = mx[c] == -INFINITY ? 0.0f : -mx[c];
-        uint32_t pw[8];
+        uint32_t pw[8], rw[8];
 #pragma unroll
         for (int a = 0; a < 4; a++) {
           float p[4];
@@ -328,12 +334,22 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, co
             p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[c][a][i], sc.mul, off));
             l[c] += p[i];
           }
-          // bf16 for the matrix cores: half a step of 2^-8 per probability, the sum l keeps fp32
           pw[2 * a] = pack_bf16x2(p[0], p[1]);
           pw[2 * a + 1] = pack_bf16x2(p[2], p[3]);
+          if constexpr (FINE) {
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+              const uint32_t w = pw[2 * a + i];
+              rw[2 * a + i] = pack_bf16x2(p[2 * i] - bf16_lo(w), p[2 * i + 1] - bf16_hi(w));
+            }
+          }
         }
         p0[c] = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[0], pw[1], pw[2], pw[3]}));
         p1[c] = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[4], pw[5], pw[6], pw[7]}));
+        if constexpr (FINE) {
+          r0[c] = __builtin_bit_cast(bf16x8_t, (u32x4_t{rw[0], rw[1], rw[2], rw[3]}));
+          r1[c] = __builtin_bit_cast(bf16x8_t, (u32x4_t{rw[4], rw[5], rw[6], rw[7]}));
+        }
       }
       for_each(std::make_integer_sequence<int, NB>{}, [&](auto block) {
         constexpr int B = decltype(block)::value;
@@ -341,12 +357,13 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, co
         value_pairs(vr[B][0], vr[B][1], row_lane<4 * B>(vsc), row_lane<4 * B + 1>(vsc), v[0][0], v[1][0]);
         value_pairs(vr[B][2], vr[B][3], row_lane<4 * B + 2>(vsc), row_lane<4 * B + 3>(vsc), v[0][1], v[1][1]);
 #pragma unroll
-        for (int e = 0; e < 2; e++)
+        for (int k = 0; k < (FINE ? 4 : 2); k++)
 #pragma unroll
-          for (int c = 0; c < NR; c++) {
-            o[c][2 * B + e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[e][0], p0[c], o[c][2 * B + e], 0, 0, 0);
-            o[c][2 * B + e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[e][1], p1[c], o[c][2 * B + e], 0, 0, 0);
-          }
+          for (int e = 0; e < 2; e++)
+#pragma unroll
+            for (int c = 0; c < NR; c++)
+              o[c][2 * B + e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  v[e][k & 1], k == 0 ? p0[c] : k == 1 ? p1[c] : k == 2 ? r0[c] : r1[c], o[c][2 * B + e], 0, 0, 0);
       });
       if (more) {
         load_v(t + step);
@@ -827,7 +844,7 @@ void launch_attention(const KvArgs& A, const KvPlan& p, const KvShare& dec, cons
   } else {
     k_kv4_decode<D, CAP, REQ_ALL, 1, false><<<groups, KV_THREADS, 0, s>>>(A, dec);
   }
-  const unsigned joins = ((unsigned)dec.chains * h << p.log_joins) + (unsigned)(p.pro_slots * (PROWS / 16)) * h;
+  const unsigned joins = ((unsigned)dec.chains * h << dec.log_joins) + (unsigned)(p.pro_slots * (PROWS / 16)) * h;
   if (p.nr == 2) k_kv_join<D, 2><<<joins, KV_THREADS, 0, s>>>(A, dec, pro);
   else k_kv_join<D, 1><<<joins, KV_THREADS, 0, s>>>(A, dec, pro);
 }
@@ -858,9 +875,11 @@ wq_status wq_kv4_attention(const void* q_bf16, int64_t q_stride, const int32_t* 
   if (batch == 0 || tokens == 0) return WQ_OK;               // nothing to compute
   KvLaunch l;
   if (const wq_status bad = l.lay_out(c)) return bad;
-  if (l.plan.chains < l.dec.chains) {         // row tiles are fewer than waves
+  if (!l.plan.solo && l.plan.chains < l.dec.chains) {         // row tiles are fewer than waves
     l.dec.chains = l.plan.chains;
-    l.dec.by_tile = !l.plan.solo;
+    l.dec.by_tile = true;
+    // few workgroups to join them then: one for 4 rows of 32 (24 requests of 1-7 drafted tokens 30.2 -> 29.1 us)
+    if (l.plan.nr == 2) l.dec.log_joins++;
   }
   hipStream_t s = (hipStream_t)stream;
   if (head_dim == 128) {
