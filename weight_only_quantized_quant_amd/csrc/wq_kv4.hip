@@ -283,11 +283,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, co
       const bool edge = t * TILE + TILE - 1 > rows.pos0 || t * TILE < lo_max || __any(!vok);
       if (edge) vsc = finite_scales(vsc);     // of tokens that not every row sees
       // bf16 for the matrix cores: half a step of 2^-8 per probability, the sum l keeps fp32.  Where
-      // contexts are long and the products few (FINE), what that leaves is multiplied too (r0, r1): the
+      // contexts are long and the products few (FINE), what that leaves is multiplied too (rest0, rest1): the
       // error against 64 bits is then the output's own rounding, 1.7e-3 instead of 2.3e-3 (2-norm), for
       // half a percent of a ragged batch's time (68.2 us) and 1.8 of one long context's (58.3); row tiles
       // of their own would pay a tenth
-      bf16x8_t p0[NR], p1[NR], r0[NR], r1[NR];
+      bf16x8_t p0[NR], p1[NR], rest0[NR], rest1[NR];
 #pragma unroll
       for (int c = 0; c < NR; c++) {
         if (c > 0 && 16 * c >= n_rows) {      // a column without rows
@@ -347,8 +347,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, co
         p0[c] = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[0], pw[1], pw[2], pw[3]}));
         p1[c] = __builtin_bit_cast(bf16x8_t, (u32x4_t{pw[4], pw[5], pw[6], pw[7]}));
         if constexpr (FINE) {
-          r0[c] = __builtin_bit_cast(bf16x8_t, (u32x4_t{rw[0], rw[1], rw[2], rw[3]}));
-          r1[c] = __builtin_bit_cast(bf16x8_t, (u32x4_t{rw[4], rw[5], rw[6], rw[7]}));
+          rest0[c] = __builtin_bit_cast(bf16x8_t, (u32x4_t{rw[0], rw[1], rw[2], rw[3]}));
+          rest1[c] = __builtin_bit_cast(bf16x8_t, (u32x4_t{rw[4], rw[5], rw[6], rw[7]}));
         }
       }
       for_each(std::make_integer_sequence<int, NB>{}, [&](auto block) {
@@ -363,7 +363,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, co
 #pragma unroll
             for (int c = 0; c < NR; c++)
               o[c][2 * B + e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  v[e][k & 1], k == 0 ? p0[c] : k == 1 ? p1[c] : k == 2 ? r0[c] : r1[c], o[c][2 * B + e], 0, 0, 0);
+                  v[e][k & 1], k == 0 ? p0[c] : k == 1 ? p1[c] : k == 2 ? rest0[c] : rest1[c], o[c][2 * B + e], 0, 0, 0);
       });
       if (more) {
         load_v(t + step);
