@@ -822,3 +822,32 @@ def test_append_rotary_on_a_side_stream_and_in_a_graph(W):
             torch.cuda.synchronize()
             assert torch.equal(x, want[i + 1]), f"replay {i}"
         assert all(torch.equal(a, b) for a, b in zip(graphed, eager))
+
+
+def test_append_rotary_in_place_once_where_an_earlier_call_failed(W):
+    """An error that another HIP call left is reported by the next launch's check; the call is not
+    made a second time, which would turn queries in place twice."""
+    rng = np.random.default_rng(77)
+    tokens, hq, hk, d = 5, 4, 2, 64
+    q, k, v = (torch.from_numpy(rng.standard_normal((tokens, h, d)).astype(np.float32)).to("cuda").bfloat16() for h in (hq, hk, hk))
+    positions = torch.arange(tokens, dtype=torch.int32, device="cuda")
+    angle = torch.arange(8, device="cuda")[:, None] * (0.3 / torch.arange(1, d // 2 + 1, device="cuda"))[None]
+    cos_sin = torch.cat([angle.cos(), angle.sin()], 1).contiguous()
+    slots = torch.arange(tokens, dtype=torch.int64, device="cuda")
+
+    def cache():
+        return [torch.zeros(s, dtype=torch.uint8, device="cuda") for s in ((1, hk, 16, d // 2), (1, hk, d // 32, 16), (1, hk, d // 2, 16), (1, hk, d // 32, 16))]
+
+    want_cache, got_cache = cache(), cache()
+    want = W.wq_kv_append_rotary(q, k, v, positions, cos_sin, slots, *want_cache)
+    torch.cuda.synchronize()
+    here = torch.cuda.current_device()
+    assert W.lib.hipSetDevice(100000) != 0      # no such device
+    try:
+        W.wq_kv_append_rotary(q, k, v, positions, cos_sin, slots, *got_cache, q_out=q)
+    except W.WQError as e:
+        assert e.status == W.WQ_EHIP and "wq_kv_append_rotary" in str(e)
+    torch.cuda.set_device(here)
+    torch.cuda.synchronize()
+    assert torch.equal(q, want)
+    assert all(torch.equal(a, b) for a, b in zip(got_cache, want_cache))

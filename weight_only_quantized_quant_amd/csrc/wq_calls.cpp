@@ -4,7 +4,8 @@
 // kernel).  Each function takes a call whose arguments are as the entry point
 // needs them and returns NotImplemented for any other, having done nothing: the
 // Python function of the same operator then says what is wrong with it, or
-// makes the call itself (tensors of another device than the current one).
+// makes the call itself (tensors of another device than the current one).  A
+// launch that fails is not tried again: it raises what the Python function would.
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
@@ -21,6 +22,9 @@ namespace {
 using at::Tensor;
 
 struct Refused {};                            // thrown by the readers below, caught at the entry
+struct Failed {                               // a launch that may have run
+  wq_status status;
+};
 
 const Tensor& tensor(PyObject* o) {
   if (!THPVariable_Check(o)) throw Refused();
@@ -105,13 +109,24 @@ float number(PyObject* o) {
 }
 bool small(int64_t v) { return v >= 0 && v <= INT32_MAX; }
 void done(wq_status s) {
+  if (s == WQ_EHIP) throw Failed{s};
   if (s != WQ_OK) throw Refused();
+}
+PyObject* raise(wq_status s, const char* where) {
+  PyObject* m = PyImport_ImportModule("weight_only_quantized_quant_amd");
+  PyObject* r = m ? PyObject_CallMethod(m, "_check", "is", (int)s, where) : nullptr;
+  Py_XDECREF(m);
+  Py_XDECREF(r);
+  if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, where);
+  return nullptr;
 }
 
 template <typename F>
-PyObject* call(Py_ssize_t given, Py_ssize_t wanted, F f) {
+PyObject* call(const char* name, Py_ssize_t given, Py_ssize_t wanted, F f) {
   try {
     if (given == wanted) return f();
+  } catch (const Failed& e) {
+    return raise(e.status, name);
   } catch (...) {                             // a refusal, or an error that the Python function will meet too
   }
   PyErr_Clear();
@@ -120,7 +135,7 @@ PyObject* call(Py_ssize_t given, Py_ssize_t wanted, F f) {
 
 // (k, v, slots, k_codes, k_scales, v_codes, v_scales)
 PyObject* kv4_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return call(n, 7, [&]() -> PyObject* {
+  return call("wq_kv4_append", n, 7, [&]() -> PyObject* {
     const Rows k(tensor(a[0])), v(tensor(a[1]));
     const Cache c(a + 3, k.dev);
     if (!c.four || k.heads != c.heads || k.dim != c.dim || v.tokens != k.tokens || v.heads != k.heads || v.dim != k.dim ||
@@ -135,7 +150,7 @@ PyObject* kv4_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // (q or None, k, v, positions, cos_sin, slots, k_codes, k_scales, v_codes, v_scales, interleaved, q_out or None)
 PyObject* kv_append_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return call(n, 12, [&]() -> PyObject* {
+  return call("wq_kv_append_rotary", n, 12, [&]() -> PyObject* {
     const Rows k(tensor(a[1])), v(tensor(a[2]));
     const Cache c(a + 6, k.dev);
     if (k.heads != c.heads || k.dim != c.dim || v.tokens != k.tokens || v.heads != k.heads || v.dim != k.dim ||
@@ -182,7 +197,7 @@ PyObject* kv_append_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // (q, k_codes, k_scales, v_codes, v_scales, block_table, cu_q, kv_lens, sm_scale or None, softcap, window, max_q,
 //  out or None, return_lse, workspace or None)
 PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return call(n, 15, [&]() -> PyObject* {
+  return call("wq_kv4_attention", n, 15, [&]() -> PyObject* {
     const Tensor& q = tensor(a[0]);
     const Rows r(q);
     const Cache c(a + 1, r.dev);
