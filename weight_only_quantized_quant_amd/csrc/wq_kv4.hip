@@ -80,13 +80,28 @@ struct KvAlike {
   }
   __device__ __forceinline__ bool operator()(int j) const { return j >= lo && j <= hi - 16; }
 };
+
 // Decode, as over the 8-bit cache: 16 or 32 rows a row tile, tiles of 64 tokens cut
-// into equal shares, one a wave, K and V from HBM straight into registers.
+// into equal shares, one a wave, K and V from HBM straight into registers.  SOLO:
+// a workgroup of WAVES waves has a row tile and nothing is joined, by a kernel
+// without shares, whose start is shorter (one request of 1000 tokens 9.8 -> 8.2 us).
+//
+// Bound by bytes where contexts are long: D / 2 + D / 32 for K and for V a token and
+// head, 64 requests of 2048-8192 tokens x 8 heads of 128 (296 MB) 68.5 us in all,
+// 4.3 TB/s, of which the joins are 5 and start and end 10; longer ones add 6.0
+// TB/s.  One 131072 tokens beside four short (243 MB): 58.5 us, 4.2 TB/s.  Half the
+// bytes of the 8-bit cache bring the conversions to the front: vector units are
+// busy 0.43 of the cycles, matrix cores 0.15, neither 0.46.  Two waves a SIMD
+// with one tile each on its way: two or three tiles on their way took the same
+// time, three waves a SIMD 71.5 us instead of 68.
+// Short contexts and drafted tokens are bound by latency (33 windows of 1000 tokens,
+// 16 heads of 64: 11.0 us; 24 requests of 1-7 queries: 29.0 us).
 //
 // Lane l = 16 g + m.  K tile a (of 4): operand row m is token
 // 16 (m / 4) + 4 a + m % 4, result rows 4 g + i are then tokens 16 g + 4 a + i;
-// step h of the products takes channels D / 4 g + 8 h on of each.  V^T: operand row m of tiles 2 b and 2 b + 1 are
-// channels 32 b + 2 m and the next.
+// step h of the products takes channels D / 4 g + 8 h on of each, so that a lane's
+// codes of a token are one load and four lanes' make a whole row.  V^T: operand
+// row m of tiles 2 b and 2 b + 1 are channels 32 b + 2 m and the next.
 template <int D, bool CAP, int WHICH, int NR, bool SOLO, int WAVES = 4>
 __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, const KvShare part) {
   constexpr int KH = D / 32, NB = D / 32, DT = D / 16, R = 16 * NR;   // k steps, blocks, channel tiles
@@ -471,6 +486,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, co
 
 // Prompts and chunks, as over the 8-bit cache: 128 rows per workgroup, 32 per
 // wave, a tile of 64 tokens converted to bf16 once per workgroup on its way to LDS.
+// Bound by the matrix cores and the vector units in turn: three prompts of
+// 1500-4096 tokens, 32 heads of 128 on 8 (264 GFLOP) 300 us, 880 TFLOP/s, where the
+// matrix cores are busy 0.38 of the cycles, the vector units 0.50, both 0.16,
+// neither 0.28; two chunks on up to 16000 tokens with capped scores 543 us with
+// four single tokens beside them.  The 8-bit cache's prompts take 304-326 us: what
+// halves here is read once per workgroup and was never the bound.
 //
 // Lane l = 32 h + m.  Within a 32-token half u of the tile, operand row
 // 8 (r / 4) + 4 h + r % 4 is token 32 u + 16 h + r: result register r of lane
@@ -822,8 +843,8 @@ __global__ __launch_bounds__(PTHREADS, D == 64 ? 3 : 2) void k_kv4_prompt(const 
   if (A.lse && h == 0) A.lse[orow] = l == 0.0f ? -INFINITY : (mx + __builtin_log2f(l)) * LN2;
 }
 
-// Workgroups of 8 waves for row tiles of their own, where each has a CU (1 x 1000 tokens 10.7 ->
-// 10.4 us, 16 x 2000 17.2 -> 16.0; 33 x 1000, 264 workgroups, 16.4 -> 20.3).
+// Workgroups of 8 waves for row tiles of their own, where each has a CU (8 heads of 128: 1 x 1000
+// tokens 9.3 -> 9.0 us, 16 x 2000 16.3 -> 14.0; 33 x 1000, 264 workgroups, 14.2 -> 17.1).
 constexpr unsigned SOLO_WIDE = 256;
 
 template <int D, bool CAP>
@@ -878,7 +899,7 @@ wq_status wq_kv4_attention(const void* q_bf16, int64_t q_stride, const int32_t* 
   if (!l.plan.solo && l.plan.chains < l.dec.chains) {         // row tiles are fewer than waves
     l.dec.chains = l.plan.chains;
     l.dec.by_tile = true;
-    // few workgroups to join them then: one for 4 rows of 32 (24 requests of 1-7 drafted tokens 30.2 -> 29.1 us)
+    // few workgroups to join them then: half the rows each (24 requests of 1-7 drafted tokens 30.2 -> 29.1 us)
     if (l.plan.nr == 2) l.dec.log_joins++;
   }
   hipStream_t s = (hipStream_t)stream;
