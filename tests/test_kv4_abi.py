@@ -1,5 +1,10 @@
 """Refusals of the 4-bit cache's entry points and of the rotating append: on the
 host, before any launch (CPU only)."""
+import os
+import shutil
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -92,3 +97,14 @@ def test_binding_refuses_host_tensors():
         W.wq_kv_append_rotary(x, x, x, i, torch.zeros(9, 64), i.long(), c, s, v, s)
     with pytest.raises(ValueError, match="q must"):
         W.wq_kv4_attention(x, c, s, v, s, i.view(2, 1), torch.zeros(3, dtype=torch.int32), i)
+
+
+def test_a_package_without_its_compiled_calls_says_so(tmp_path):
+    import weight_only_quantized_quant_amd as W
+    here, name = os.path.dirname(W.__file__), "weight_only_quantized_quant_amd"
+    (tmp_path / name).mkdir()
+    shutil.copy(os.path.join(here, "__init__.py"), tmp_path / name)
+    os.symlink(os.path.join(here, "libwq.so"), tmp_path / name / "libwq.so")
+    got = subprocess.run([sys.executable, "-c", f"import {name}"], cwd=tmp_path, capture_output=True, text=True,
+                         env={**os.environ, "PYTHONPATH": str(tmp_path)})
+    assert got.returncode != 0 and "_calls.so is missing: build it with" in got.stderr

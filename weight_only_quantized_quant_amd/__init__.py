@@ -25,10 +25,11 @@ WQ_OK, WQ_EINVAL, WQ_EALIGN, WQ_EUNSUPPORTED, WQ_EHIP = range(5)
 MX_RULES = {"round": 0, "half": 1, "ocp": 2, "floor_div": 3, "ceil_div": 4}
 MX_ELEMS = {"e2m1": WQ_E2M1X2, "e4m3": WQ_E4M3}
 
-if not os.path.exists(LIB_PATH):
-    raise ImportError(
-        f"{LIB_PATH} is missing: build it with `python weight_only_quantized_quant_amd/build.py` "
-        "(hipcc, gfx950). There is no fallback path.")
+for _path in (LIB_PATH, os.path.join(_HERE, "_calls.so")):
+    if not os.path.exists(_path):
+        raise ImportError(
+            f"{_path} is missing: build it with `python weight_only_quantized_quant_amd/build.py` "
+            "(hipcc, gfx950). There is no fallback path.")
 
 lib = ctypes.CDLL(LIB_PATH)
 from . import _calls  # noqa: E402 (linked to the library)
