@@ -13,8 +13,11 @@
  *   16-byte aligned (WQ_EALIGN otherwise) where an entry point does not say less.
  * - Shapes and divisibility are validated on the host before anything is
  *   launched: violations return WQ_EINVAL, unsupported dtype/block/group
- *   combinations WQ_EUNSUPPORTED, launch failures WQ_EHIP.  An error return
- *   means nothing was enqueued.
+ *   combinations WQ_EUNSUPPORTED; nothing is enqueued then.  WQ_EHIP: a HIP
+ *   call of the entry point failed.  Where it launches one kernel nothing was
+ *   enqueued either; where it launches several, those before the failed one
+ *   were.  What the thread's earlier HIP calls left as its last error is not
+ *   reported, and is cleared.
  * - Out-of-range values never raise: they saturate, as the formats define.
  * - Element counts are int64_t; rows * cols must fit in 2^40.
  *

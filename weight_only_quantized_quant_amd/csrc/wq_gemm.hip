@@ -1704,7 +1704,7 @@ wq_status wq_gemm(const void* x_bf16, int64_t M, int64_t N, int64_t K, const voi
   else if (w_dtype == WQ_E4M3 && s_dtype == WQ_F32 && group == K) wdt = W_FP8;
   else return WQ_EUNSUPPORTED;
   if (M > 16 && (int64_t)((M + 255) / 256) * ((N + 255) / 256) > 0x7FFFFFFF) return WQ_EINVAL;   // prefill tiles
-  hipStream_t s = (hipStream_t)stream;
+  hipStream_t s = wq_stream(stream);
   const uint16_t* x = (const uint16_t*)x_bf16;
   const uint8_t* w = (const uint8_t*)wqp;
   uint16_t* y = (uint16_t*)y_bf16;

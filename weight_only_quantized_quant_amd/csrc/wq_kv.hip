@@ -1028,7 +1028,7 @@ wq_status wq_kv_blocks(const int32_t* ctx_lens, const int32_t* new_lens, int64_t
     for (int j = i + 1; j < 10; j++)
       if (at[i] && at[i] == at[j]) return WQ_EINVAL;
   const int64_t groups = (tokens + KV_THREADS - 1) / KV_THREADS;
-  k_kv_blocks<<<(unsigned)(groups > 1 ? groups : 1), KV_THREADS, 0, (hipStream_t)stream>>>(
+  k_kv_blocks<<<(unsigned)(groups > 1 ? groups : 1), KV_THREADS, 0, wq_stream(stream)>>>(
       ctx_lens, new_lens, batch, free_pages, num_free, cursor, log2_page(page), block_table, max_blocks, tokens, slots,
       positions, cu_new, kv_lens, state);
   return wq_launch_status();
@@ -1079,7 +1079,7 @@ wq_status wq_kv_attention(const void* q_bf16, int64_t q_stride, const int32_t* c
   if (batch == 0 || tokens == 0) return WQ_OK;               // nothing to compute
   KvLaunch l;
   if (const wq_status bad = l.lay_out(c)) return bad;
-  hipStream_t s = (hipStream_t)stream;
+  hipStream_t s = wq_stream(stream);
   if (head_dim == 128) {
     if (softcap > 0.0f) launch_attention<128, true>(l.args, l.plan, l.dec, l.pro, s);
     else launch_attention<128, false>(l.args, l.plan, l.dec, l.pro, s);

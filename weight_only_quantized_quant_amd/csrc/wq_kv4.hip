@@ -902,7 +902,7 @@ wq_status wq_kv4_attention(const void* q_bf16, int64_t q_stride, const int32_t* 
     // few workgroups to join them then: half the rows each (24 requests of 1-7 drafted tokens 30.2 -> 29.1 us)
     if (l.plan.nr == 2) l.dec.log_joins++;
   }
-  hipStream_t s = (hipStream_t)stream;
+  hipStream_t s = wq_stream(stream);
   if (head_dim == 128) {
     if (softcap > 0.0f) launch_attention<128, true>(l.args, l.plan, l.dec, l.pro, s);
     else launch_attention<128, false>(l.args, l.plan, l.dec, l.pro, s);

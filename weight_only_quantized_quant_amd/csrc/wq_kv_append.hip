@@ -708,7 +708,7 @@ wq_status append(const void* k, int64_t k_stride, const void* v, int64_t v_strid
     if (!wq_aligned(r.cos_sin) || !wq_aligned(r.q) || !wq_aligned(r.q_out)) return WQ_EALIGN;
   }
   if (tokens == 0) return WQ_OK;
-  hipStream_t s = (hipStream_t)stream;
+  hipStream_t s = wq_stream(stream);
   const bool eight = cache == WQ_E4M3;
   // tokens a workgroup: few at least, so that a step's are spread over the chip (64 tokens x 8 heads: 4-bit 4.0-4.2 us in
   // fours, 4.3 singly, 5.0 in sixteens; 8-bit with rotation 4.5 in fours, 6.6 singly, where its workgroups are many)

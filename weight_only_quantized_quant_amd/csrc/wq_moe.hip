@@ -564,7 +564,7 @@ wq_status wq_moe_route(const float* logits, int64_t T, int32_t E, int32_t k, int
   if (T < 0 || E < 1 || E > 64 || k < 1 || k > E) return WQ_EINVAL;
   if (T * k > 0x7FFFFFFFLL) return WQ_EINVAL;
   if (!offsets || (T > 0 && (!logits || !ids || !weights || !row_token || !row_slot))) return WQ_EINVAL;
-  hipStream_t s = (hipStream_t)stream;
+  hipStream_t s = wq_stream(stream);
   if (T > 0) k_route<<<(unsigned)((T + 3) / 4), 256, 0, s>>>(logits, T, E, k, ids, weights);
   k_group<<<(unsigned)E, 1024, 0, s>>>(ids, T, E, k, offsets, row_token, row_slot);
   return wq_launch_status();
@@ -576,7 +576,7 @@ wq_status wq_w4a8_prepack(const uint32_t* wq, const uint16_t* scales, int64_t ex
   if (!wq || !scales || !wq_out || !s8 || !ch) return WQ_EINVAL;
   if (!wq_aligned(wq) || !wq_aligned(wq_out)) return WQ_EALIGN;
   if (!wq_numel_ok(experts * N, K)) return WQ_EINVAL;
-  hipStream_t s = (hipStream_t)stream;
+  hipStream_t s = wq_stream(stream);
   const int64_t rows = experts * N, G = K / 128, words = rows * (K / 8);
   const int64_t scale_waves = G <= 32 ? (rows + 64 / scales_lanes((int)G) - 1) / (64 / scales_lanes((int)G)) : rows;
   k_w4a8_scales<<<(unsigned)((scale_waves + 3) / 4), 256, 0, s>>>(scales, rows, (int)G, s8, ch);
@@ -588,7 +588,7 @@ wq_status wq_w4a8_dequant(const uint32_t* wq, const uint8_t* s8, int64_t N, int6
   if (N < 1 || K < 128 || K % 128 || !wq || !s8 || !codes) return WQ_EINVAL;
   if (!wq_numel_ok(N, K)) return WQ_EINVAL;
   const int64_t words = N * (K / 8);
-  k_w4a8_dequant<<<(unsigned)((words + 255) / 256), 256, 0, (hipStream_t)stream>>>(wq, s8, N, K, codes);
+  k_w4a8_dequant<<<(unsigned)((words + 255) / 256), 256, 0, wq_stream(stream)>>>(wq, s8, N, K, codes);
   return wq_launch_status();
 }
 
@@ -617,7 +617,7 @@ wq_status wq_moe_gemm_w4a8(const uint8_t* x8, int64_t T, const float* a_scale, c
   const int64_t tiles_m = (R + MBM - 1) / MBM + experts;   // each expert adds at most one partial tile
   const int64_t tiles_n = (N + MBN - 1) / MBN;
   if (tiles_m * tiles_n > 0x7FFFFFFFLL) return WQ_EINVAL;
-  k_moe_gemm<<<(unsigned)(tiles_m * tiles_n), 512, MLDS, (hipStream_t)stream>>>(
+  k_moe_gemm<<<(unsigned)(tiles_m * tiles_n), 512, MLDS, wq_stream(stream)>>>(
       x8, T, a_scale, row_token, R, offsets, experts, N, K, wq, s8, ch, y, (int)tiles_n);
   return wq_launch_status();
 }

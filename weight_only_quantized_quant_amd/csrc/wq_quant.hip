@@ -475,7 +475,7 @@ wq_status quantize_e4m3(const void* x, int x_dtype, int64_t rows, int64_t cols, 
   if (x_dtype != WQ_F32 && x_dtype != WQ_BF16) return WQ_EUNSUPPORTED;
   if (!wq_numel_ok(rows, cols)) return WQ_EINVAL;
   if (!wq_aligned(x) || !wq_aligned(codes) || (scales && !wq_aligned(scales))) return WQ_EALIGN;
-  hipStream_t s = (hipStream_t)stream;
+  hipStream_t s = wq_stream(stream);
   const bool bf = x_dtype == WQ_BF16;
   const int64_t n = rows * cols;
   if (block == 0) {
@@ -520,7 +520,7 @@ wq_status quantize_mxfp4(const void* x, int x_dtype, int64_t rows, int64_t cols,
   if (block != 16 && block != 32) return WQ_EUNSUPPORTED;
   if (cols % 32 || !wq_numel_ok(rows, cols)) return WQ_EINVAL;
   if (!wq_aligned(x) || !wq_aligned(codes) || !wq_aligned(scales)) return WQ_EALIGN;
-  hipStream_t s = (hipStream_t)stream;
+  hipStream_t s = wq_stream(stream);
   const int64_t nch = rows * cols / 16;
   if (x_dtype == WQ_BF16) k_mxfp4<true><<<grid_for(nch), kThreads, 0, s>>>(x, nch, block, codes, scales);
   else k_mxfp4<false><<<grid_for(nch), kThreads, 0, s>>>(x, nch, block, codes, scales);
@@ -536,7 +536,7 @@ wq_status quantize_mx(const void* x, int x_dtype, int64_t rows, int64_t cols, in
   if (block != 16 && block != 32) return WQ_EUNSUPPORTED;
   if (cols % 32 || !wq_numel_ok(rows, cols)) return WQ_EINVAL;
   if (!wq_aligned(x) || !wq_aligned(codes) || !wq_aligned(scales)) return WQ_EALIGN;
-  hipStream_t s = (hipStream_t)stream;
+  hipStream_t s = wq_stream(stream);
   const int64_t nch = rows * cols / 16;
   const unsigned g = grid_for(nch);
   const bool bf = x_dtype == WQ_BF16;
@@ -557,7 +557,7 @@ wq_status quantize_nvfp4(const void* x, int x_dtype, int64_t rows, int64_t cols,
   if (!(tensor_scale > 0.0f) || !(tensor_scale <= 3.4028234e38f)) return WQ_EINVAL;
   if (!wq_numel_ok(rows, cols)) return WQ_EINVAL;
   if (!wq_aligned(x) || !wq_aligned(codes) || !wq_aligned(scales)) return WQ_EALIGN;
-  hipStream_t s = (hipStream_t)stream;
+  hipStream_t s = wq_stream(stream);
   const int64_t nb = rows * cols / 16;
   if (x_dtype == WQ_BF16) k_nvfp4<true><<<grid_for(nb), kThreads, 0, s>>>(x, nb, tensor_scale, codes, scales);
   else k_nvfp4<false><<<grid_for(nb), kThreads, 0, s>>>(x, nb, tensor_scale, codes, scales);
@@ -571,7 +571,7 @@ wq_status quantize_int4(const void* w, int w_dtype, int64_t rows, int64_t cols, 
   if (group != 32 && group != 64 && group != 128) return WQ_EUNSUPPORTED;
   if (cols % group || cols % 32 || !wq_numel_ok(rows, cols)) return WQ_EINVAL;
   if (!wq_aligned(w) || !wq_aligned(packed) || !wq_aligned(scales)) return WQ_EALIGN;
-  hipStream_t s = (hipStream_t)stream;
+  hipStream_t s = wq_stream(stream);
   const int64_t nch = rows * cols / 16;
   const int lpg = group / 16;
   if (w_dtype == WQ_BF16) k_int4<true><<<grid_for(nch), kThreads, 0, s>>>(w, nch, lpg, packed, scales);
@@ -586,7 +586,7 @@ wq_status quantize_int4_asym(const void* w, int w_dtype, int64_t rows, int64_t c
   if (group != 32 && group != 64 && group != 128) return WQ_EUNSUPPORTED;
   if (cols % group || !wq_numel_ok(rows, cols)) return WQ_EINVAL;
   if (!wq_aligned(w) || !wq_aligned(packed) || !wq_aligned(scalezero)) return WQ_EALIGN;
-  hipStream_t s = (hipStream_t)stream;
+  hipStream_t s = wq_stream(stream);
   const int64_t nch = rows * cols / 16;
   const int lpg = group / 16;
   if (w_dtype == WQ_BF16) k_int4_asym<true><<<grid_for(nch), kThreads, 0, s>>>(w, nch, lpg, packed, scalezero);
@@ -598,7 +598,7 @@ wq_status wq_dequant(const void* wqp, int w_dtype, const void* w_scales, int s_d
                      int64_t K, uint16_t* w_bf16, void* stream) {
   if (!wqp || !w_bf16 || N <= 0 || K <= 0 || K % 32 || !wq_numel_ok(N, K)) return WQ_EINVAL;
   if (!wq_aligned(wqp) || !wq_aligned(w_bf16)) return WQ_EALIGN;
-  hipStream_t s = (hipStream_t)stream;
+  hipStream_t s = wq_stream(stream);
   const int64_t nch = N * K / 8;
   if (w_dtype == WQ_INT4X8) {
     if (s_dtype != WQ_BF16 || (group != 32 && group != 64 && group != 128)) return WQ_EUNSUPPORTED;

@@ -67,7 +67,7 @@ wq_status wq_util_stream_read(const void* buf, int64_t bytes, uint32_t magic, ui
   if (!buf || !sink || bytes <= 0 || bytes % 16 || bytes > (int64_t(1) << 40)) return WQ_EINVAL;
   if (!wq_aligned(buf)) return WQ_EALIGN;
   const int64_t grid = (bytes + SR_PIECE - 1) / SR_PIECE;
-  k_stream_read<<<(unsigned)grid, SR_THREADS, 0, (hipStream_t)stream>>>((const uint8_t*)buf, bytes, magic, sink);
+  k_stream_read<<<(unsigned)grid, SR_THREADS, 0, wq_stream(stream)>>>((const uint8_t*)buf, bytes, magic, sink);
   return wq_launch_status();
 }
 
@@ -77,14 +77,14 @@ wq_status wq_util_spin(int64_t iters, uint32_t magic, uint32_t* sink, void* stre
   if (hipGetDevice(&dev) != hipSuccess ||
       hipDeviceGetAttribute(&ncu, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || ncu <= 0)
     return WQ_EHIP;
-  k_spin<<<(unsigned)ncu, 256, 0, (hipStream_t)stream>>>(iters, magic, sink);
+  k_spin<<<(unsigned)ncu, 256, 0, wq_stream(stream)>>>(iters, magic, sink);
   return wq_launch_status();
 }
 
 wq_status wq_util_clock(int64_t ticks, int64_t* out, void* stream) {
   if (!out || ticks < 1 || ticks > (int64_t(1) << 20)) return WQ_EINVAL;
   if (!wq_aligned(out)) return WQ_EALIGN;
-  k_clock<<<1, 64, 0, (hipStream_t)stream>>>(ticks, out);
+  k_clock<<<1, 64, 0, wq_stream(stream)>>>(ticks, out);
   return wq_launch_status();
 }
 

@@ -310,7 +310,7 @@ wq_status quantize_e4m3_static(const void* x, int x_dtype, int64_t rows, int64_t
   if (x_dtype != WQ_F32 && x_dtype != WQ_BF16) return WQ_EUNSUPPORTED;
   if (!wq_numel_ok(rows, cols)) return WQ_EINVAL;
   if (!wq_aligned(x) || !wq_aligned(codes) || ((uintptr_t)scale & 3u)) return WQ_EALIGN;
-  hipStream_t s = (hipStream_t)stream;
+  hipStream_t s = wq_stream(stream);
   const int64_t nch = rows * cols / 16;
   if (x_dtype == WQ_BF16) k_e4m3_static<true><<<grid_for(nch), kThreads, 0, s>>>(x, nch, scale, codes);
   else k_e4m3_static<false><<<grid_for(nch), kThreads, 0, s>>>(x, nch, scale, codes);
@@ -323,7 +323,7 @@ wq_status quantize_e4m3_block2d(const void* w, int w_dtype, int64_t rows, int64_
   if (w_dtype != WQ_F32 && w_dtype != WQ_BF16) return WQ_EUNSUPPORTED;
   if (!wq_numel_ok(rows, cols) || (rows + 127) / 128 > 65535 || cols / 128 > 0x7FFFFFFF) return WQ_EINVAL;
   if (!wq_aligned(w) || !wq_aligned(codes) || ((uintptr_t)scales & 3u)) return WQ_EALIGN;
-  hipStream_t s = (hipStream_t)stream;
+  hipStream_t s = wq_stream(stream);
   const dim3 grid((unsigned)(cols / 128), (unsigned)((rows + 127) / 128));
   if (w_dtype == WQ_BF16) k_e4m3_block2d<true><<<grid, kThreads, 0, s>>>(w, rows, cols, codes, scales);
   else k_e4m3_block2d<false><<<grid, kThreads, 0, s>>>(w, rows, cols, codes, scales);
@@ -345,7 +345,7 @@ wq_status wq_gemm_w8a8(const uint8_t* a, const float* a_scale, int64_t as_m, int
   if (tm * tn > 0x7FFFFFFF) return WQ_EINVAL;
   if (!wq_aligned(a) || !wq_aligned(b) || !wq_aligned(y)) return WQ_EALIGN;
   if (((uintptr_t)a_scale & 3u) || ((uintptr_t)b_scale & 3u)) return WQ_EALIGN;
-  hipStream_t s = (hipStream_t)stream;
+  hipStream_t s = wq_stream(stream);
   const unsigned grid = (unsigned)(tm * tn);
   if (as_k != 0 || bs_k != 0) {
     if (allow_lds128<k_w8a8<true>>() != hipSuccess) return WQ_EHIP;
