@@ -663,8 +663,8 @@ size_t wq_kv4_attention_workspace_size(int64_t batch, int64_t tokens, int64_t ma
  * cache_dtype  WQ_E4M3 (8-bit cache) or WQ_E2M1X2 (4-bit cache).
  * q_out        tokens x q_heads x head_dim bf16 (output), rows q_out_stride elements
  *              apart.  May be q itself where x_dtype is WQ_BF16 and the strides are
- *              equal (WQ_EINVAL otherwise); any other overlap with an input is
- *              outside the contract.
+ *              equal (WQ_EINVAL otherwise).  Any other overlap with an input or the
+ *              cache is outside the contract; an equal pointer is WQ_EINVAL.
  * Strides and the other arguments as wq_kv_append's; q, q_out and cos_sin are
  * 16-byte aligned.
  */

@@ -52,6 +52,20 @@ def test_rotary_refusals(lib, cache):
     assert call(tokens=0) == 0 and call(tokens=0, q=None, out=None, hq=0, qs=0, os=0) == 0
 
 
+@pytest.mark.parametrize("cache", [2, 3])
+def test_rotary_refuses_an_output_that_is_another_argument(lib, cache):
+    """Keys, values, indices, angles and the cache are read or written while the queries are written."""
+    where = {n: 0x100000 * (i + 1) for i, n in enumerate(("q", "k", "v", "pos", "cs", "slots", "kc", "ksc", "vc", "vsc"))}
+
+    def call(out):
+        w = where
+        return lib.wq_kv_append_rotary(w["q"], 1024, 8, w["k"], 1024, w["v"], 1024, 1, w["pos"], w["cs"], 100, 128, 0,
+                                       w["slots"], 4, 8, 128, cache, 64, 10, w["kc"], w["ksc"], w["vc"], w["vsc"], out, 1024, None)
+    for name in where:
+        if name != "q":
+            assert call(where[name]) == 1, name
+
+
 def test_attention_refusals(lib):
     def call(q=P, qs=1024, cu=P, kv=P, batch=2, tokens=4, max_q=0, hq=8, hk=4, dim=128, kc=P, ksc=P, vc=P, vsc=P,
              page=64, pages=10, table=P, width=4, sm=0.1, cap=0.0, window=0, out=P2, lse=None, ws=P, wsb=1 << 40):

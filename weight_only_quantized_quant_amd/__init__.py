@@ -584,7 +584,7 @@ def wq_kv_append_rotary(q, k: torch.Tensor, v: torch.Tensor, positions: torch.Te
     [tokens, heads, head_dim], bf16 or fp32, tokens may be strided; positions int32 [tokens], cos_sin
     fp32 [max_pos, rot]: cosines of the rot / 2 pairs, then their sines.  Pairs are channels
     (i, i + rot / 2), or (2i, 2i + 1) if interleaved.  Returns the rotated queries, bf16: q_out
-    (tokens may be strided; q itself if that is bf16) or a new tensor.  Rows of tokens whose
+    (tokens may be strided; q itself if that is bf16, no other argument) or a new tensor.  Rows of tokens whose
     position is outside [0, max_pos) are not written."""
     got = _calls.kv_append_rotary(q, k, v, positions, cos_sin, slots, k_codes, k_scales, v_codes, v_scales, interleaved, q_out)
     if got is not NotImplemented:

@@ -703,8 +703,14 @@ wq_status append(const void* k, int64_t k_stride, const void* v, int64_t v_strid
                           r.q_stride > (int64_t(1) << 40) || r.q_out_stride > (int64_t(1) << 40) ||
                           !wq_numel_ok(tokens ? tokens : 1, q_row)))
       return WQ_EINVAL;
-    // in place row by row only
-    if (r.q_heads > 0 && tokens > 0 && r.q == r.q_out && (!bf || (r.q_stride != r.q_out_stride && tokens > 1))) return WQ_EINVAL;
+    if (r.q_heads > 0 && tokens > 0) {
+      // in place row by row only
+      if (r.q == r.q_out && (!bf || (r.q_stride != r.q_out_stride && tokens > 1))) return WQ_EINVAL;
+      // other workgroups read or write these while the queries are written
+      for (const void* p : {k, v, (const void*)slots, (const void*)r.positions, (const void*)r.cos_sin, (const void*)k_codes,
+                            (const void*)k_scales, (const void*)v_codes, (const void*)v_scales})
+        if (r.q_out == p) return WQ_EINVAL;
+    }
     if (!wq_aligned(r.cos_sin) || !wq_aligned(r.q) || !wq_aligned(r.q_out)) return WQ_EALIGN;
   }
   if (tokens == 0) return WQ_OK;
