@@ -1,4 +1,11 @@
-"""What the entry points report of errors that are not theirs."""
+"""What the entry points report of errors that are not theirs, and the compiled calls over entry
+points that fail."""
+import json
+import os
+import shutil
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -84,3 +91,56 @@ def test_an_earlier_error_is_not_reported(W):
             got = [t for t in (got if isinstance(got, tuple) else (got,)) if torch.is_tensor(t)]
             assert len(got) == len(want) and all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want)), name
     assert not bad, bad
+
+
+# Entry points in place of the library's, which the compiled calls find first because they are loaded
+# into the process's own scope before them.  The calls through ctypes are the library's still.
+STUB = r"""
+static int calls;
+int stub_calls(void) { return calls; }
+int wq_kv_append_rotary(void) { calls++; return 4; }
+"""
+CHILD = r"""
+import ctypes, json, sys
+stub = ctypes.CDLL(sys.argv[1], ctypes.RTLD_GLOBAL)
+import torch
+import weight_only_quantized_quant_amd as W
+heads, dim, page, tokens = 2, 64, 16, 5
+q, k, v = (torch.randn(tokens, n, dim, device="cuda").bfloat16() for n in (4, heads, heads))
+slots, positions = torch.arange(tokens, device="cuda"), torch.arange(1, tokens + 1, dtype=torch.int32, device="cuda")
+cos_sin = torch.cat([torch.zeros(8, dim // 2, device="cuda"), torch.ones(8, dim // 2, device="cuda")], 1)
+shapes = ((1, heads, page, dim // 2), (1, heads, dim // 32, page), (1, heads, dim // 2, page), (1, heads, dim // 32, page))
+cache = [torch.zeros(s, dtype=torch.uint8, device="cuda") for s in shapes]
+before = q.clone()
+torch.cuda.synchronize()
+said = None
+try:
+    W.wq_kv_append_rotary(q, k, v, positions, cos_sin, slots, *cache, q_out=q)
+except W.WQError as e:
+    said = str(e)
+torch.cuda.synchronize()
+got = {"said": said, "calls": stub.stub_calls(), "queries": torch.equal(q, before), "cache": not any(c.any().item() for c in cache)}
+print(json.dumps(got))
+"""
+
+
+@pytest.fixture(scope="module")
+def child(W, tmp_path_factory):
+    """What a process says whose compiled calls reach the entry points above."""
+    where = tmp_path_factory.mktemp("stub")
+    (where / "stub.c").write_text(STUB)
+    subprocess.run([shutil.which("gcc") or "cc", "-shared", "-fPIC", "-o", str(where / "stub.so"), str(where / "stub.c")], check=True)
+    (where / "child.py").write_text(CHILD)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    banner("errors: a process with entry points that fail")
+    run = subprocess.run([sys.executable, str(where / "child.py"), str(where / "stub.so")], cwd=root, capture_output=True, text=True,
+                         timeout=100, env={**os.environ, "PYTHONPATH": root})
+    assert run.returncode == 0, run.stderr[-2000:]
+    return json.loads(run.stdout.splitlines()[-1])
+
+
+def test_a_launch_that_fails_is_not_made_again(child):
+    """The compiled call raises what the entry point said and does not go the other way, where queries in
+    place would be turned by a call that has failed."""
+    assert child["said"] and "wq_kv_append_rotary" in child["said"] and "WQ_EHIP" in child["said"]
+    assert child["calls"] == 1 and child["queries"] and child["cache"]
