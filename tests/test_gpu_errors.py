@@ -1,5 +1,5 @@
 """What the entry points report of errors that are not theirs, and the compiled calls over entry
-points that fail."""
+points that fail or take their time."""
 import json
 import os
 import shutil
@@ -96,12 +96,15 @@ def test_an_earlier_error_is_not_reported(W):
 # Entry points in place of the library's, which the compiled calls find first because they are loaded
 # into the process's own scope before them.  The calls through ctypes are the library's still.
 STUB = r"""
+#include <unistd.h>
 static int calls;
 int stub_calls(void) { return calls; }
 int wq_kv_append_rotary(void) { calls++; return 4; }
+int wq_kv4_append(void) { usleep(400000); return 0; }
+int wq_kv4_attention(void) { usleep(400000); return 0; }
 """
 CHILD = r"""
-import ctypes, json, sys
+import ctypes, json, sys, threading, time
 stub = ctypes.CDLL(sys.argv[1], ctypes.RTLD_GLOBAL)
 import torch
 import weight_only_quantized_quant_amd as W
@@ -111,6 +114,7 @@ slots, positions = torch.arange(tokens, device="cuda"), torch.arange(1, tokens +
 cos_sin = torch.cat([torch.zeros(8, dim // 2, device="cuda"), torch.ones(8, dim // 2, device="cuda")], 1)
 shapes = ((1, heads, page, dim // 2), (1, heads, dim // 32, page), (1, heads, dim // 2, page), (1, heads, dim // 32, page))
 cache = [torch.zeros(s, dtype=torch.uint8, device="cuda") for s in shapes]
+table, cu, lens = (torch.tensor(t, dtype=torch.int32, device="cuda") for t in ([[0]], [0, tokens], [tokens]))
 before = q.clone()
 torch.cuda.synchronize()
 said = None
@@ -120,6 +124,21 @@ except W.WQError as e:
     said = str(e)
 torch.cuda.synchronize()
 got = {"said": said, "calls": stub.stub_calls(), "queries": torch.equal(q, before), "cache": not any(c.any().item() for c in cache)}
+ticks, stop = [], threading.Event()
+def tick():
+    while not stop.is_set():
+        ticks.append(time.monotonic())
+        time.sleep(0.001)
+t = threading.Thread(target=tick)
+t.start()
+for name, call in (("append", lambda: W.wq_kv4_append(k, v, slots, *cache)),
+                   ("attention", lambda: W.wq_kv4_attention(q, *cache, table, cu, lens))):
+    start = time.monotonic()
+    call()
+    got[name + " us"] = int(1e6 * (time.monotonic() - start))
+    got[name] = sum(start + 0.1 < x < start + 0.3 for x in ticks)
+stop.set()
+t.join()
 print(json.dumps(got))
 """
 
@@ -132,7 +151,7 @@ def child(W, tmp_path_factory):
     subprocess.run([shutil.which("gcc") or "cc", "-shared", "-fPIC", "-o", str(where / "stub.so"), str(where / "stub.c")], check=True)
     (where / "child.py").write_text(CHILD)
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-    banner("errors: a process with entry points that fail")
+    banner("errors: a process with entry points that fail or sleep")
     run = subprocess.run([sys.executable, str(where / "child.py"), str(where / "stub.so")], cwd=root, capture_output=True, text=True,
                          timeout=100, env={**os.environ, "PYTHONPATH": root})
     assert run.returncode == 0, run.stderr[-2000:]
@@ -144,3 +163,10 @@ def test_a_launch_that_fails_is_not_made_again(child):
     place would be turned by a call that has failed."""
     assert child["said"] and "wq_kv_append_rotary" in child["said"] and "WQ_EHIP" in child["said"]
     assert child["calls"] == 1 and child["queries"] and child["cache"]
+
+
+@pytest.mark.parametrize("name", ["append", "attention"])
+def test_other_threads_run_during_a_launch(child, name):
+    """An entry point that waits for 0.4 s: another thread, which ticks every millisecond, goes on."""
+    assert child[name + " us"] >= 400000, "the call did not reach the stub"
+    assert child[name] >= 20

@@ -112,6 +112,17 @@ void done(wq_status s) {
   if (s == WQ_EHIP) throw Failed{s};
   if (s != WQ_OK) throw Refused();
 }
+// The interpreter's lock is given back while memory is allocated and kernels are
+// launched: either may wait for the device.  Arguments are read before and results
+// made after; what is thrown between takes the lock again on its way.
+class Unlocked {
+  PyThreadState* const state = PyEval_SaveThread();
+
+ public:
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
 PyObject* raise(wq_status s, const char* where) {
   PyObject* m = PyImport_ImportModule("weight_only_quantized_quant_amd");
   PyObject* r = m ? PyObject_CallMethod(m, "_check", "is", (int)s, where) : nullptr;
@@ -142,8 +153,13 @@ PyObject* kv4_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         v.type != k.type || v.dev != k.dev || !small(k.heads))
       throw Refused();
     const int64_t* slots = dense_at<int64_t>(a[2], at::kLong, k.dev, {k.tokens});
-    done(wq_kv4_append(k.at, k.stride, v.at, v.stride, type_of(k), slots, k.tokens, (int32_t)k.heads, (int32_t)k.dim,
-                       (int32_t)c.page, c.pages, c.kc, c.ks, c.vc, c.vs, stream_on(k.dev)));
+    const int type = type_of(k);
+    hipStream_t stream = stream_on(k.dev);
+    {
+      const Unlocked unlocked;
+      done(wq_kv4_append(k.at, k.stride, v.at, v.stride, type, slots, k.tokens, (int32_t)k.heads, (int32_t)k.dim,
+                         (int32_t)c.page, c.pages, c.kc, c.ks, c.vc, c.vs, stream));
+    }
     Py_RETURN_NONE;
   });
 }
@@ -166,26 +182,40 @@ PyObject* kv_append_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const void* qp = nullptr;
     uint16_t* op = nullptr;
     int64_t q_heads = 0, q_stride = 0, o_stride = 0;
+    const int type = type_of(k);
     hipStream_t stream = stream_on(k.dev);
+    const float* cos_sin = (const float*)angles.data_ptr();
+    const int64_t max_pos = angles.size(0), rot = angles.size(1);
+    at::TensorOptions made;
     if (a[0] != Py_None) {
       const Tensor& q = tensor(a[0]);
       const Rows r(q);
       if (r.tokens != k.tokens || r.dim != k.dim || r.type != k.type || r.dev != k.dev || !small(r.heads)) throw Refused();
-      out = a[11] == Py_None ? at::empty({r.tokens, r.heads, r.dim}, q.options().dtype(at::kBFloat16)) : tensor(a[11]);
-      const Rows o(out);
-      if (o.tokens != r.tokens || o.heads != r.heads || o.dim != r.dim || o.type != at::kBFloat16 || o.dev != k.dev) throw Refused();
       qp = r.at;
       q_heads = r.heads;
       q_stride = r.stride;
-      op = (uint16_t*)o.at;
-      o_stride = o.stride;
+      made = q.options().dtype(at::kBFloat16);
+      if (a[11] != Py_None) {
+        const Rows o(tensor(a[11]));
+        if (o.tokens != r.tokens || o.heads != r.heads || o.dim != r.dim || o.type != at::kBFloat16 || o.dev != k.dev) throw Refused();
+        op = (uint16_t*)o.at;
+        o_stride = o.stride;
+      }
     } else if (a[11] != Py_None) {
       throw Refused();
     }
-    done(wq_kv_append_rotary(qp, q_stride, (int32_t)q_heads, k.at, k.stride, v.at, v.stride, type_of(k), positions,
-                             (const float*)angles.data_ptr(), angles.size(0), (int32_t)angles.size(1), inter, slots,
-                             k.tokens, (int32_t)k.heads, (int32_t)k.dim, c.four ? WQ_E2M1X2 : WQ_E4M3, (int32_t)c.page,
-                             c.pages, c.kc, c.ks, c.vc, c.vs, op, o_stride, stream));
+    {
+      const Unlocked unlocked;
+      if (a[0] != Py_None && a[11] == Py_None) {
+        out = at::empty({k.tokens, q_heads, k.dim}, made);
+        op = (uint16_t*)out.data_ptr();
+        o_stride = q_heads * k.dim;
+      }
+      done(wq_kv_append_rotary(qp, q_stride, (int32_t)q_heads, k.at, k.stride, v.at, v.stride, type, positions, cos_sin,
+                               max_pos, (int32_t)rot, inter, slots, k.tokens, (int32_t)k.heads, (int32_t)k.dim,
+                               c.four ? WQ_E2M1X2 : WQ_E4M3, (int32_t)c.page, c.pages, c.kc, c.ks, c.vc, c.vs, op, o_stride,
+                               stream));
+    }
     if (a[11] != Py_None || a[0] == Py_None) {
       Py_INCREF(a[11]);
       return a[11];
@@ -212,10 +242,13 @@ PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int with_lse = PyObject_IsTrue(a[13]);
     if (with_lse < 0) throw Refused();
     hipStream_t stream = stream_on(r.dev);
-    Tensor out = a[12] == Py_None ? at::empty({r.tokens, r.heads, r.dim}, q.options()) : dense(a[12], at::kBFloat16, r.dev);
-    if (out.sizes() != q.sizes()) throw Refused();
-    Tensor lse, ws;
-    if (with_lse) lse = at::empty({r.tokens, r.heads}, q.options().dtype(at::kFloat));
+    const int32_t* table_at = (const int32_t*)table.data_ptr();
+    const at::TensorOptions like = q.options();
+    Tensor out, lse, ws;
+    if (a[12] != Py_None) {
+      out = dense(a[12], at::kBFloat16, r.dev);
+      if (out.sizes() != q.sizes()) throw Refused();
+    }
     void* ws_at = nullptr;
     size_t ws_bytes = 0;
     if (a[14] != Py_None) {
@@ -223,18 +256,24 @@ PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (ws.get_device() != r.dev || !ws.is_contiguous()) throw Refused();
       ws_bytes = ws.nbytes();
       ws_at = ws.data_ptr();
-    } else {
-      ws_bytes = wq_kv4_attention_workspace_size(batch, r.tokens, max_q, (int32_t)r.heads, (int32_t)c.heads, (int32_t)r.dim,
-                                                 (int32_t)c.page, width, window);
-      if (ws_bytes) {
-        ws = at::empty({(int64_t)ws_bytes}, q.options().dtype(at::kByte));
-        ws_at = ws.data_ptr();
-      }
     }
-    done(wq_kv4_attention(r.at, r.stride, cu, lens, batch, r.tokens, max_q, (int32_t)r.heads, (int32_t)c.heads,
-                          (int32_t)r.dim, c.kc, c.ks, c.vc, c.vs, (int32_t)c.page, c.pages,
-                          (const int32_t*)table.data_ptr(), width, sm_scale, softcap, window, (uint16_t*)out.data_ptr(),
-                          with_lse ? (float*)lse.data_ptr() : nullptr, ws_at, ws_bytes, stream));
+    {
+      const Unlocked unlocked;
+      if (!out.defined()) out = at::empty({r.tokens, r.heads, r.dim}, like);
+      if (with_lse) lse = at::empty({r.tokens, r.heads}, like.dtype(at::kFloat));
+      if (!ws.defined()) {
+        ws_bytes = wq_kv4_attention_workspace_size(batch, r.tokens, max_q, (int32_t)r.heads, (int32_t)c.heads, (int32_t)r.dim,
+                                                   (int32_t)c.page, width, window);
+        if (ws_bytes) {
+          ws = at::empty({(int64_t)ws_bytes}, like.dtype(at::kByte));
+          ws_at = ws.data_ptr();
+        }
+      }
+      done(wq_kv4_attention(r.at, r.stride, cu, lens, batch, r.tokens, max_q, (int32_t)r.heads, (int32_t)c.heads,
+                            (int32_t)r.dim, c.kc, c.ks, c.vc, c.vs, (int32_t)c.page, c.pages, table_at, width, sm_scale, softcap,
+                            window, (uint16_t*)out.data_ptr(), with_lse ? (float*)lse.data_ptr() : nullptr, ws_at, ws_bytes,
+                            stream));
+    }
     PyObject* o = a[12];
     if (o == Py_None) o = THPVariable_Wrap(out);
     else Py_INCREF(o);
