@@ -152,8 +152,9 @@ def child(W, tmp_path_factory):
     (where / "child.py").write_text(CHILD)
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     banner("errors: a process with entry points that fail or sleep")
+    paths = os.pathsep.join(p for p in (root, os.environ.get("PYTHONPATH")) if p)
     run = subprocess.run([sys.executable, str(where / "child.py"), str(where / "stub.so")], cwd=root, capture_output=True, text=True,
-                         timeout=100, env={**os.environ, "PYTHONPATH": root})
+                         timeout=100, env={**os.environ, "PYTHONPATH": paths})
     assert run.returncode == 0, run.stderr[-2000:]
     return json.loads(run.stdout.splitlines()[-1])
 
