@@ -122,3 +122,49 @@ def test_a_package_without_its_compiled_calls_says_so(tmp_path):
     got = subprocess.run([sys.executable, "-c", f"import {name}"], cwd=tmp_path, capture_output=True, text=True,
                          env={**os.environ, "PYTHONPATH": str(tmp_path)})
     assert got.returncode != 0 and "_calls.so is missing: build it with" in got.stderr
+
+
+@pytest.mark.parametrize("why", ["not loadable", "other torch"])
+def test_compiled_calls_that_do_not_fit_the_process(tmp_path, why):
+    """The package works as it does without them, by ctypes, and says so once."""
+    import weight_only_quantized_quant_amd as W
+    here, name = os.path.dirname(W.__file__), "weight_only_quantized_quant_amd"
+    (tmp_path / name).mkdir()
+    shutil.copy(os.path.join(here, "__init__.py"), tmp_path / name)
+    os.symlink(os.path.join(here, "libwq.so"), tmp_path / name / "libwq.so")
+    if why == "other torch":
+        os.symlink(os.path.join(here, "_calls.so"), tmp_path / name / "_calls.so")
+    else:
+        (tmp_path / name / "_calls.so").write_bytes(b"no library")
+    (tmp_path / "child.py").write_text(f"""
+import warnings
+import torch
+if {why == "other torch"}:
+    torch.__version__ = "1.0"
+with warnings.catch_warnings(record=True) as got:
+    warnings.simplefilter("always")
+    import {name} as W
+assert [w.category for w in got] == [RuntimeWarning] and "ctypes" in str(got[0].message), got
+assert W._calls.kv4_append(1, 2) is W._calls.kv_append_rotary() is W._calls.kv4_attention(3) is NotImplemented
+assert W.lib.wq_kv4_attention_workspace_size(3, 3, 1, 32, 8, 128, 64, 512, 0) > 0
+x, i = torch.zeros(2, 1, 64, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int64)
+c, s = torch.zeros(2, 1, 16, 32, dtype=torch.uint8), torch.zeros(2, 1, 2, 16, dtype=torch.uint8)
+try:
+    W.wq_kv4_append(x, x, i, c, s, c.transpose(2, 3).contiguous(), s)
+except ValueError as e:
+    assert "k must" in str(e)
+else:
+    raise AssertionError("host tensors were taken")
+print(got[0].message)
+""")
+    got = subprocess.run([sys.executable, str(tmp_path / "child.py")], cwd=tmp_path, capture_output=True, text=True,
+                         env={**os.environ, "PYTHONPATH": str(tmp_path)})
+    assert got.returncode == 0, got.stderr
+    assert (why != "other torch") or "built for torch" in got.stdout
+
+
+def test_compiled_calls_that_fit_load_without_a_warning():
+    import weight_only_quantized_quant_amd as W
+    got = subprocess.run([sys.executable, "-W", "error::RuntimeWarning", "-c", "import weight_only_quantized_quant_amd as W; print(W._calls.__file__)"],
+                         cwd=os.path.dirname(os.path.dirname(W.__file__)), capture_output=True, text=True)
+    assert got.returncode == 0 and "_calls.so" in got.stdout, got.stderr

@@ -6,12 +6,16 @@ marshal arguments: they check devices, dtypes, shapes and contiguity of
 PyTorch tensors, allocate outputs with PyTorch when none are given, and pass
 raw device pointers plus the current HIP stream.  Every step of the
 computation runs in the HIP kernels; there is no other code path.  If the
-library has not been built the import fails.
+library has not been built the import fails.  Calls of a decode step's layers go
+through a compiled module; where that was built for another torch or Python
+than the process's, they go through ctypes to the same entry points, with a
+warning at import.
 """
 from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 import torch
 
@@ -32,7 +36,15 @@ for _path in (LIB_PATH, os.path.join(_HERE, "_calls.so")):
             "(hipcc, gfx950). There is no fallback path.")
 
 lib = ctypes.CDLL(LIB_PATH)
-from . import _calls  # noqa: E402 (linked to the library)
+try:
+    from . import _calls  # linked to the library, and to the torch and the Python that it was built with
+except ImportError as _e:
+    warnings.warn(f"the compiled calls do not fit this process ({_e}): every call goes through ctypes, some microseconds "
+                  "slower each, until weight_only_quantized_quant_amd/build.py is run with this torch and Python", RuntimeWarning)
+
+    class _calls:
+        """Takes no call: the Python functions make them themselves."""
+        kv4_append = kv_append_rotary = kv4_attention = staticmethod(lambda *a: NotImplemented)
 
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
 _SIGS = {

@@ -70,7 +70,7 @@ def calls_commands(obj: str, out: str) -> list:
     cxx = os.environ.get("CXX", "g++")
     inc = [*include_paths(), "/opt/rocm/include", sysconfig.get_paths()["include"]]
     return [[cxx, "-O2", "-std=c++17", "-fPIC", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
-             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *[x for i in inc for x in ("-isystem", i)],
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f'-DWQ_TORCH="{torch.__version__}"', *[x for i in inc for x in ("-isystem", i)],
              "-I", INCLUDE, "-c", os.path.join(CSRC, "wq_calls.cpp"), "-o", obj],
             [cxx, "-shared", obj, "-o", out, *[f"-L{p}" for p in library_paths()], "-ltorch_python", "-ltorch_cpu", "-lc10",
              "-lc10_hip", f"-L{HERE}", "-l:libwq.so", "-Wl,-rpath,$ORIGIN"]]

@@ -14,6 +14,7 @@
 
 #include <cfloat>
 #include <cmath>
+#include <cstring>
 
 #include "wq.h"
 
@@ -293,6 +294,26 @@ PyMethodDef methods[] = {
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
+// What lies inside a tensor is the torch's that this was compiled against, and the calling
+// convention its Python's; under another of either the module must not be used.
+bool built_for_this_process() {
+  static const char python[] = Py_STRINGIFY(PY_MAJOR_VERSION) "." Py_STRINGIFY(PY_MINOR_VERSION) ".";
+  if (strncmp(Py_GetVersion(), python, sizeof python - 1) != 0) {
+    PyErr_Format(PyExc_ImportError, "_calls.so was built for Python %s* and runs under %.20s", python, Py_GetVersion());
+    return false;
+  }
+  PyObject* torch = PyImport_ImportModule("torch");
+  PyObject* version = torch ? PyObject_GetAttrString(torch, "__version__") : nullptr;
+  PyObject* text = version ? PyObject_Str(version) : nullptr;
+  const char* now = text ? PyUnicode_AsUTF8(text) : nullptr;
+  const bool same = now && strcmp(now, WQ_TORCH) == 0;
+  if (now && !same) PyErr_Format(PyExc_ImportError, "_calls.so was built for torch %s and runs under torch %s", WQ_TORCH, now);
+  Py_XDECREF(text);
+  Py_XDECREF(version);
+  Py_XDECREF(torch);
+  return same;
+}
+
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__calls() { return built_for_this_process() ? PyModule_Create(&module) : nullptr; }
