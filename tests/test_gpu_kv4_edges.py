@@ -1,10 +1,12 @@
-"""GPU parity of the rotating append where the other tests do not reach: workgroups that take many tokens."""
+"""GPU parity of the 4-bit cache and the rotating append where the other tests do not reach: workgroups
+that take many tokens, capped scores over shares of the work, row tiles of their own by the hundred and more
+row tiles than waves."""
 import numpy as np
 import pytest
 
 from tests.gpu_helpers import banner
 from tests.test_gpu_kv import W, _cache, _slots  # noqa: F401 (W is a fixture)
-from tests.test_gpu_kv4 import _angles, _cache4, _check_rotary
+from tests.test_gpu_kv4 import _angles, _cache4, _check_attention, _check_rotary, _problem
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +44,66 @@ def test_append_rotary_many_tokens_a_workgroup(W, bits, bf16, Hq, H, D, page, ro
     q = g.standard_normal((T, Hq, D)).astype(np.float32)
     cache = _cache4(g, N, H, page, D) if bits == 4 else _cache(g, N, H, page, D)
     _check_rotary(W, q, k, v, pos, cs, slots, cache, bf16, inter)
+
+
+# ---------------------------------------------------------------------------
+# attention
+# ---------------------------------------------------------------------------
+def _kind(W, q, kv, H, page, table, most_q, window=0):
+    """Whether the call joins nothing ("alone") or cuts its work into shares, as its workspace says."""
+    n = W.wq_kv4_attention_workspace_size(len(kv), q.shape[0], most_q, q.shape[1], H, q.shape[2], page, table.shape[1], window)
+    return "shares" if n else "alone"
+
+
+@pytest.mark.parametrize("H,group,most_q,D", [(8, 2, 1, 64), (8, 2, 1, 128), (5, 3, 4, 128), (8, 4, 6, 64), (8, 4, 6, 128),
+                                              (3, 16, 4, 128)])
+@pytest.mark.parametrize("softcap", [3.0, 40.0])
+def test_attention_capped_shares(W, H, group, most_q, D, softcap):
+    """Ragged decode batches and drafted tokens with capped scores, shares that begin and end anywhere:
+    16-row tiles, whose probabilities are multiplied in two terms, and tiles of 32 rows."""
+    banner("kv4 attention: capped shares", H, group, most_q, D, softcap)
+    g = np.random.default_rng(H + D)
+    kl = np.exp(g.uniform(0, np.log(3000), 40)).astype(int)
+    ql = g.integers(1, most_q + 1, 40)
+    kl[[3, 17]], ql[[5, 6, 30]], kl[[9, 22]] = 0, 0, [2999, 2048]
+    q, cu, kv, cache, table = _problem(24, H * group, H, D, 32, ql, kl, spare_rows=2)
+    assert _kind(W, q, kv, H, 32, table, most_q) == "shares"
+    for kw in ({}, {"window": 700}):
+        _check_attention(W, q, cu, kv, cache, table, max_q=most_q, softcap=softcap, sm_scale=0.3, **kw)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("softcap", [0.0, 5.0])
+def test_attention_capped_long_context(W, D, softcap):
+    """One context beside short ones, all of whose shares are one row tile's."""
+    banner("kv4 attention: capped long context", D, softcap)
+    q, cu, kv, cache, table = _problem(25, 8, 2, D, 128, [1, 1, 1], [20000, 3, 900])
+    assert _kind(W, q, kv, 2, 128, table, 1) == "shares"
+    _check_attention(W, q, cu, kv, cache, table, poison=False, max_q=1, softcap=softcap, sm_scale=0.2)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("group,most_q", [(2, 1), (4, 6)])
+@pytest.mark.parametrize("softcap,window", [(0.0, 0), (4.0, 0), (30.0, 90)])
+def test_attention_row_tiles_alone_by_the_hundred(W, D, group, most_q, softcap, window):
+    """More row tiles than CUs, each a workgroup's own: 40 requests, 8 heads, tables of at most 1500 tokens."""
+    banner("kv4 attention: row tiles of their own", D, group, most_q, softcap, window)
+    g = np.random.default_rng(D + most_q)
+    kl, ql = np.exp(g.uniform(0, np.log(1500), 40)).astype(int), g.integers(1, most_q + 1, 40)
+    kl[:3], ql[7] = [1499, 1, 0], 0
+    q, cu, kv, cache, table = _problem(26, 8 * group, 8, D, 64, ql, kl, spare_rows=1)
+    assert _kind(W, q, kv, 8, 64, table, most_q, window) == "alone"
+    _check_attention(W, q, cu, kv, cache, table, max_q=most_q, softcap=softcap, window=window, sm_scale=0.3)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("softcap", [0.0, 6.0])
+def test_attention_more_row_tiles_than_waves(W, D, softcap):
+    """Requests beyond the waves of a head (128 at 16 heads): every wave has an entry of its own for the join."""
+    banner("kv4 attention: more row tiles than waves", D, softcap)
+    g = np.random.default_rng(D)
+    kl = np.exp(g.uniform(0, np.log(700), 150)).astype(int)
+    kl[[0, 77]] = [699, 0]
+    q, cu, kv, cache, table = _problem(27, 32, 16, D, 16, [1] * 150, kl)
+    assert _kind(W, q, kv, 16, 16, table, 1) == "shares"
+    _check_attention(W, q, cu, kv, cache, table, max_q=1, softcap=softcap, sm_scale=0.3)
