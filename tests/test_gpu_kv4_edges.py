@@ -1,11 +1,14 @@
 """GPU parity of the 4-bit cache and the rotating append where the other tests do not reach: workgroups
-that take many tokens, capped scores over shares of the work, row tiles of their own by the hundred and more
-row tiles than waves."""
+that take many tokens, capped scores over shares of the work, row tiles of their own by the hundred, more
+row tiles than waves, and the second term of the probabilities."""
 import numpy as np
 import pytest
+import torch
 
-from tests.gpu_helpers import banner
-from tests.test_gpu_kv import W, _cache, _slots  # noqa: F401 (W is a fixture)
+from oracle import kv4 as O4
+from oracle.formats import bf16_decode, bf16_round
+from tests.gpu_helpers import banner, dev_bf16, dev_u8, host_bits16
+from tests.test_gpu_kv import W, _cache, _i32, _slots  # noqa: F401 (W is a fixture)
 from tests.test_gpu_kv4 import _angles, _cache4, _check_attention, _check_rotary, _problem
 
 pytestmark = pytest.mark.gpu
@@ -107,3 +110,32 @@ def test_attention_more_row_tiles_than_waves(W, D, softcap):
     q, cu, kv, cache, table = _problem(27, 32, 16, D, 16, [1] * 150, kl)
     assert _kind(W, q, kv, 16, 16, table, 1) == "shares"
     _check_attention(W, q, cu, kv, cache, table, max_q=1, softcap=softcap, sm_scale=0.3)
+
+
+@pytest.mark.parametrize("H,group,D", [(8, 1, 64), (2, 8, 128), (8, 4, 128), (1, 16, 64)])
+@pytest.mark.parametrize("softcap", [0.0, 8.0])
+def test_attention_probabilities_in_two_terms(W, H, group, D, softcap):
+    """Tiles of 16 rows cut into shares: the output is off by its own rounding and by what 64 bits do
+    not know of, not by a rounding of the probabilities to bf16.
+
+    The bound is the other tests' with that rounding's 2^-8 of sum w |v| taken out: what it leaves is exact
+    in fp32 and is multiplied too, rounded to bf16 itself, so that 2^-8 of 2^-8 remains; the sums have twice
+    as many terms.  Few tokens and small scores keep the bound's other parts below what a
+    lost second term does (a table wider than the contexts gives the shares)."""
+    banner("kv4 attention: probabilities in two terms", H, group, D, softcap)
+    g = np.random.default_rng(28)
+    kl = g.integers(5, 40, 60)
+    q, cu, kv, cache, table = _problem(28, H * group, H, D, 16, [1] * 60, kl, spare_cols=300)
+    assert _kind(W, q, kv, H, 16, table, 1) == "shares"
+    cache[1][:], cache[3][:] = 127, g.integers(126, 129, cache[3].shape)
+    bits, scale = bf16_round(q), 0.02
+    ref, _, weight, spread = O4.attention(bf16_decode(bits), cu, kv, *cache, table, scale, softcap)
+    got = W.wq_kv4_attention(dev_bf16(bits), *[dev_u8(c) for c in cache], _i32(table), _i32(cu), _i32(kv), sm_scale=scale,
+                             softcap=softcap, max_q=1)
+    torch.cuda.synchronize()
+    e = (D + 16) * 2.0 ** -24 * spread + softcap * 2.0 ** -22
+    rel = np.expm1(2 * e) + (2 * max(kl) + 8) * 2.0 ** -23 + 2.0 ** -20 + 2.0 ** -16
+    tol = 2.0 ** -8 * np.abs(ref) + rel[..., None] * 1.01 * weight + 1e-30
+    worst = (np.abs(bf16_decode(host_bits16(got)) - ref) / tol).max()
+    # what the probabilities' rounding alone does to this problem passes the bound many times over
+    assert worst <= 1.0, f"error / bound = {worst:.3f}"
