@@ -545,7 +545,9 @@ wq_status wq_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v
  *   out = sum_j exp(s_j) v_j / sum_j exp(s_j),  lse = log sum_j exp(s_j).
  * Query head h reads key/value head h / (q_heads / kv_heads).  fp32 scores,
  * softmax statistics and sums; the probabilities are rounded to bf16 for the
- * second product, the output once.  A row that sees no token gets out 0 and
+ * second product, the output once.  The sums are of values times up to 2^8
+ * each before they are divided: of values beyond 2^119 / tokens they may pass
+ * fp32's range, and the output is infinite or NaN then.  A row that sees no token gets out 0 and
  * lse -inf.  Rows behind cu_q[batch] stay as they were.
  *
  * q           tokens x q_heads x head_dim bf16; rows of a token q_stride elements
@@ -617,7 +619,8 @@ size_t wq_kv_attention_workspace_size(int64_t batch, int64_t tokens, int64_t max
  * sign, and a NaN becomes 0.
  * Arguments as wq_kv_append's.  A token whose slot is outside [0, num_pages *
  * page) is skipped; slots may come in any order.  A slot given twice in one call
- * holds bytes of either token.  Bytes of other slots stay as they were.
+ * holds bytes of either token, codes and scales not always of the same one.
+ * Bytes of other slots stay as they were.
  */
 wq_status wq_kv4_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride, int x_dtype,
                         const int64_t* slots, int64_t tokens, int32_t heads, int32_t head_dim, int32_t page,
@@ -664,7 +667,9 @@ size_t wq_kv4_attention_workspace_size(int64_t batch, int64_t tokens, int64_t ma
  *              elements apart; NULL with q_heads 0 for keys alone.
  * positions    `tokens` int32 device positions (wq_kv_blocks writes them).  A token
  *              whose position is outside [0, max_pos) is left out: its row of
- *              q_out stays as it was and its slot is not written.
+ *              q_out stays as it was and its slot is not written.  (In the 8-bit
+ *              cache one between others of its page makes two runs of them, which
+ *              wq_kv_append does not take.)
  * cos_sin      max_pos x rot fp32; rot is 16 to head_dim and a multiple of 16
  *              (WQ_EUNSUPPORTED otherwise).
  * cache_dtype  WQ_E4M3 (8-bit cache) or WQ_E2M1X2 (4-bit cache).

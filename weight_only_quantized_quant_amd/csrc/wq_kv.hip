@@ -153,8 +153,7 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_blocks(
 // as V^T follows it, so it is chosen such that a lane's probabilities belong to
 // 16 consecutive tokens: one page, one scale, and one 16-byte load per
 // channel of V^T.
-//
-// Rows of one key/value head are numbered r = query * group + head in group:
+
 // Eight E4M3 bytes with E8M0 scale operand -> eight bf16.
 __device__ __forceinline__ bf16x8_t e4m3_bf16x8(uint32_t a, uint32_t b, float scale) {
   const u32x4_t w = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, false)),

@@ -95,7 +95,7 @@ struct KvAlike {
 // with one tile each on its way: two or three tiles on their way took the same
 // time, three waves a SIMD 71.5 us instead of 68.
 // Short contexts and drafted tokens are bound by latency (33 windows of 1000 tokens,
-// 16 heads of 64: 11.0 us; 24 requests of 1-7 queries: 29.0 us).
+// 16 heads of 64: 11.0 us; 24 requests of 1-7 queries: 28.8 us).
 //
 // Lane l = 16 g + m.  K tile a (of 4): operand row m is token
 // 16 (m / 4) + 4 a + m % 4, result rows 4 g + i are then tokens 16 g + 4 a + i;
@@ -487,9 +487,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_decode(const KvArgs A, co
 // Prompts and chunks, as over the 8-bit cache: 128 rows per workgroup, 32 per
 // wave, a tile of 64 tokens converted to bf16 once per workgroup on its way to LDS.
 // Bound by the matrix cores and the vector units in turn: three prompts of
-// 1500-4096 tokens, 32 heads of 128 on 8 (264 GFLOP) 300 us, 880 TFLOP/s, where the
+// 1500-4096 tokens, 32 heads of 128 on 8 (264 GFLOP) 294-302 us, 875-898 TFLOP/s, where the
 // matrix cores are busy 0.38 of the cycles, the vector units 0.50, both 0.16,
-// neither 0.28; two chunks on up to 16000 tokens with capped scores 543 us with
+// neither 0.28; two chunks on up to 16000 tokens with capped scores 538-543 us with
 // four single tokens beside them.  The 8-bit cache's prompts take 304-326 us: what
 // halves here is read once per workgroup and was never the bound.
 //

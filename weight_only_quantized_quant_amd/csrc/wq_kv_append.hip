@@ -89,12 +89,12 @@ struct KvRotary {
   }
 };
 
-// 8 channels of a row that begins at element `row` of x, token t, turned.  T is
-// double for keys: the products of two fp32 numbers are exact there, so that
+// 8 channels of a row that begins at element `row` of x, token t, turned: keys,
+// in fp64, where the products of two fp32 numbers are exact, so that
 // the result, rounded once to fp32, is the nearest to what the formula gives, and
 // the code that follows from it does not depend on how the sum was made (fp32
 // moved 1 code in some thousand to its neighbour, and a scale now and then).
-template <bool BF16, typename T = double>
+template <bool BF16>
 __device__ __forceinline__ void rotate8(const void* x, int64_t row, int ch, const KvRotary& R, int64_t t, float out[8]) {
   float a[8];
   load8<BF16>(x, row + ch, a);
@@ -109,9 +109,9 @@ __device__ __forceinline__ void rotate8(const void* x, int64_t row, int ch, cons
     const f32x4_t c = *reinterpret_cast<const f32x4_t*>(cs + ch / 2), s = *reinterpret_cast<const f32x4_t*>(cs + half + ch / 2);
 #pragma unroll
     for (int e = 0; e < 4; e++) {
-      const T u = a[2 * e], v = a[2 * e + 1];
-      out[2 * e] = (float)__builtin_elementwise_fma(u, (T)c[e], -(v * (T)s[e]));
-      out[2 * e + 1] = (float)__builtin_elementwise_fma(v, (T)c[e], u * (T)s[e]);
+      const double u = a[2 * e], v = a[2 * e + 1];
+      out[2 * e] = (float)__builtin_elementwise_fma(u, (double)c[e], -(v * (double)s[e]));
+      out[2 * e + 1] = (float)__builtin_elementwise_fma(v, (double)c[e], u * (double)s[e]);
     }
   } else {
     const bool lower = ch < half;
@@ -122,7 +122,7 @@ __device__ __forceinline__ void rotate8(const void* x, int64_t row, int ch, cons
     load8_f32(cs + half + i, s);
 #pragma unroll
     for (int e = 0; e < 8; e++)
-      out[e] = (float)__builtin_elementwise_fma((T)a[e], (T)c[e], (T)b[e] * (T)(lower ? -s[e] : s[e]));
+      out[e] = (float)__builtin_elementwise_fma((double)a[e], (double)c[e], (double)b[e] * (double)(lower ? -s[e] : s[e]));
   }
 }
 
