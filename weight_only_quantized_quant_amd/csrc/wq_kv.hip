@@ -26,8 +26,8 @@ __device__ __forceinline__ int first_above(const int64_t* sums, int count, int64
 // same way.  Workgroup 0 writes the per-request outputs.  There is no
 // dependence between workgroups, so one launch does it all: the new pages of a
 // token come from the free list itself, not from the table that another
-// workgroup fills.  Bound by latency: 4.4 us for 256 requests of one token,
-// 4.0 us for 7 prompts of 16384 tokens (an empty launch takes 2.5 us).
+// workgroup fills.  Bound by latency: 4.0 us for 256 requests of one token,
+// 3.8 us for 7 prompts of 16384 tokens (an empty launch takes 2.5 us).
 __global__ __launch_bounds__(KV_THREADS) void k_kv_blocks(
     const int32_t* __restrict__ ctx_lens, const int32_t* __restrict__ new_lens, int64_t batch,
     const int32_t* __restrict__ free_pages, int64_t num_free, const int32_t* __restrict__ cursor, int log_page,
