@@ -1,6 +1,8 @@
 """GPU parity of the 4-bit cache and the rotating append where the other tests do not reach: workgroups
 that take many tokens, capped scores over shares of the work, row tiles of their own by the hundred, more
 row tiles than waves, and the second term of the probabilities."""
+from concurrent.futures import ThreadPoolExecutor
+
 import numpy as np
 import pytest
 import torch
@@ -139,3 +141,38 @@ def test_attention_probabilities_in_two_terms(W, H, group, D, softcap):
     worst = (np.abs(bf16_decode(host_bits16(got)) - ref) / tol).max()
     # what the probabilities' rounding alone does to this problem passes the bound many times over
     assert worst <= 1.0, f"error / bound = {worst:.3f}"
+
+
+# ---------------------------------------------------------------------------
+# threads
+# ---------------------------------------------------------------------------
+def test_calls_from_several_threads(W):
+    """Compiled calls give the interpreter's lock back, so calls of several threads are inside the library
+    at once: each on a stream of its own, with outputs, workspaces and a cache of its own."""
+    banner("kv4: appends and attention from four threads at once")
+    g = np.random.default_rng(29)
+    H, D, P, T = 2, 64, 16, 70
+    slots, N = _slots(g, [5], [T], P)
+    pos, cs, sl = _i32(5 + np.arange(T)), torch.from_numpy(_angles(100, D)).cuda(), torch.from_numpy(slots).cuda()
+    start = [dev_u8(c) for c in _cache4(g, N, H, P, D)]
+    q, cu, kv, cache, table = _problem(30, 8, 2, 128, 64, [1, 1, 5], [900, 4000, 300])
+    args = (dev_bf16(bf16_round(q)), *[dev_u8(c) for c in cache], _i32(table), _i32(cu), _i32(kv))
+    new = [[dev_bf16(bf16_round(g.standard_normal((T, h, D)))) for h in (4, H, H)] for _ in range(4)]
+
+    def work(i, times):
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.default_stream())
+        with torch.cuda.stream(stream):
+            mine = [c.clone() for c in start]
+            for _ in range(times):
+                out = W.wq_kv_append_rotary(*new[i], pos, cs, sl, *mine)
+                W.wq_kv4_append(new[i][2], new[i][1], sl, *mine)
+                got = W.wq_kv4_attention(*args, return_lse=True)
+        stream.synchronize()
+        return [out, *mine, *got]
+
+    want = [work(i, 1) for i in range(4)]
+    with ThreadPoolExecutor(4) as pool:
+        got = list(pool.map(lambda i: work(i, 50), range(4)))
+    for a, b in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
